@@ -189,10 +189,136 @@ vdx_status vdx_rope3d_attn_noalloc(const void* q, const void* k, const void* v, 
                                    int sec_t, int sec_h, int sec_w, double theta, float scale,
                                    void* stream);
 
+/* ---- Streaming and conditioning: a paged key/value cache, attention of new tokens over it, and
+ * cross attention.  A transformer block that generates video chunk by chunk (each new chunk of
+ * latent tokens attends to every token before it) appends the chunk's rotated keys and its
+ * values to a cache and attends over the cache; the same block attends to the text or image
+ * encoder's states.
+ *
+ * Element types VDX_DTYPE_BF16 and VDX_DTYPE_FP16 (all tensors of a call share one), head
+ * dimension 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128 (query head h reads key/value
+ * head h / (Hq / Hkv)).  Strides count elements.  The channels of one (token, head) are
+ * contiguous; base pointers are 16-byte aligned and strides are multiples of 8, so slices of
+ * one fused projection and caches in [page, token, head] or [page, head, token] order are taken
+ * as they are.  Every pointer is a device pointer; these calls allocate nothing and keep nothing
+ * between calls (scratch comes from the caller), so they may be captured into CUDA graphs and
+ * run at once on several streams, each with its own workspace.
+ *
+ * Lengths live on the device and may change between replays of a captured call; what the host
+ * passes are upper bounds.  Values that break a bound are never followed: the kernel clamps or
+ * skips them and vdx_sync_check reports VDX_ERR_ARG. */
+#define VDX_DTYPE_BF16 0
+#define VDX_DTYPE_FP16 1
+
+/* A cache of num_pages pages of page_size tokens each.  Key c of sequence s is token
+ * c % page_size of page page_table[s * table_stride + c / page_size], for every head.
+ * page_size: 16, 32, 64, or any size >= 128 (a page may hold one latent frame).  Entries of
+ * page_table past a sequence's length are not read; a page index outside [0, num_pages) is
+ * reported, nothing is written through it and its keys read as zeros.  Slots past a sequence's
+ * length may hold anything, NaN included; within it the cache has to be finite. */
+typedef struct vdx_paged_kv {
+  void* k;                  /* [num_pages, page_size, Hkv, d] with the strides below              */
+  void* v;
+  long long k_page, k_token, k_head;   /* strides of k                                            */
+  long long v_page, v_token, v_head;   /* strides of v                                            */
+  const int32_t* page_table;           /* [seqs][table_stride], the first max_pages of a row used */
+  long long table_stride;
+  int num_pages, page_size, max_pages;
+  int Hkv, d, dtype;
+  int seqs;
+} vdx_paged_kv;
+
+/* New tokens of seqs sequences, packed: row r of q, k and v belongs to the sequence s with
+ * cu[s] <= r < cu[s + 1] (cu: device int32 [seqs + 1], not decreasing, cu[seqs] <= rows; rows
+ * outside every sequence are left alone).  kv_len[s] (device int32) counts the sequence's keys
+ * with its new ones: with n = cu[s + 1] - cu[s], row i of the sequence has cache index
+ * c = kv_len[s] - n + i. */
+
+/* Append: for every row, write v and the rotated key into the cache at index c, and the rotated
+ * query into q_out.  The rotation is that of vdx_rope3d_attn at grid token
+ * pos_offset[s] + c (pos_offset NULL: c; larger than 0 when a sequence's oldest pages have been
+ * dropped from its table).  With q_norm / k_norm (d values of the call's type, shared by the
+ * heads) x * rsqrt(mean(x^2) + eps) * weight is applied to each head before the rotation.
+ * fp32 arithmetic, angles reduced exactly, one rounding at the end; v is copied bit for bit.
+ * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place);
+ * otherwise the outputs must not overlap an input.  A token outside the grid's T*Hgrid*Wgrid
+ * positions, or with a cache index below 0 or past its page table, is skipped and reported.
+ * Two rows of one call that land in the same cache slot leave one of them there. */
+typedef struct vdx_append_args {
+  const void* q;            /* [rows, Hq, d] or NULL                                              */
+  const void* k;            /* [rows, Hkv, d]                                                     */
+  const void* v;
+  void* q_out;              /* [rows, Hq, d]; NULL with q NULL                                    */
+  long long q_row, q_head, k_row, k_head, v_row, v_head, q_out_row, q_out_head;   /* strides      */
+  int rows, Hq;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* pos_offset;   /* [seqs] or NULL                                                  */
+  int T, Hgrid, Wgrid, sec_t, sec_h, sec_w;   /* as in vdx_rope3d_attn                            */
+  double theta;
+  const void* q_norm;       /* [d] or NULL                                                        */
+  const void* k_norm;       /* [d] or NULL                                                        */
+  float eps;
+} vdx_append_args;
+vdx_status vdx_rope3d_append(const vdx_paged_kv* cache, const vdx_append_args* args, void* stream);
+
+/* Attention of the new tokens over the cache (q already rotated, keys already appended):
+ *     lse = log sum_c exp(scale * <q, k_c>),   out = sum_c exp(scale * <q, k_c> - lse) v_c
+ * over the visible keys c of row i of its sequence, with p = kv_len - n + i:
+ *     c < kv_len,  and with causal_block = m > 0 also  c < (floor(p / m) + 1) * m
+ * (m = 1: each token sees the tokens up to itself; m = tokens of a latent frame: whole frames up
+ * to its own; m = 0: every key).  A row that sees no key gets out = 0 and lse = -inf.
+ * q, k and v enter the products as they are; scores, softmax statistics and accumulators are
+ * fp32; the softmax weights are rounded to the call's type for the product with v.
+ *   out: [rows, Hq, d] contiguous;  lse: float32 [Hq, rows] or NULL.
+ *   max_q, max_kv: host bounds on n and on kv_len (they size the launch; 0 takes rows and
+ *   max_pages * page_size).  Rows and keys past them are not computed, and reported.
+ *   scale <= 0 selects 1/sqrt(d).  out must not overlap q, k or v.
+ *   workspace: >= vdx_paged_attn_workspace_bytes() bytes of the device, 16-byte aligned, used by
+ *   this call alone until it has run; NULL where that is 0. */
+typedef struct vdx_paged_attn_args {
+  const void* q;            /* [rows, Hq, d]                                                      */
+  void* out;
+  float* lse;
+  long long q_row, q_head;  /* strides of q                                                       */
+  int rows, Hq;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  int max_q, max_kv;
+  int causal_block;
+  float scale;
+  void* workspace;
+  size_t workspace_bytes;
+} vdx_paged_attn_args;
+vdx_status vdx_paged_attn(const vdx_paged_kv* cache, const vdx_paged_attn_args* args, void* stream);
+size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* cache, const vdx_paged_attn_args* args);
+
+/* Cross attention: q [B, N, Hq, d] over k, v [B, M, Hkv, d] (an encoder's states; no positions).
+ * kv_len (device int32 [B], or NULL: M) limits batch entry b to its first kv_len[b] keys; keys
+ * past it may hold anything.  A batch stride of 0 shares one q, k or v over the batch.
+ * Formulas, arithmetic, scale and workspace as vdx_paged_attn; M may be 0 and N may be 0.
+ *   out: [B, N, Hq, d] contiguous;  lse: float32 [B, Hq, N] or NULL. */
+typedef struct vdx_cross_attn_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  long long q_batch, q_row, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head;
+  int B, N, M, Hq, Hkv, d, dtype;
+  const int32_t* kv_len;
+  float scale;
+  void* workspace;
+  size_t workspace_bytes;
+} vdx_cross_attn_args;
+vdx_status vdx_cross_attn(const vdx_cross_attn_args* args, void* stream);
+size_t vdx_cross_attn_workspace_bytes(const vdx_cross_attn_args* args);
+
 /* Synchronise `stream`, then read and clear the device error word.  Returns VDX_OK,
  * VDX_ERR_TIMEOUT (a kernel gave up on a pipeline wait; the output of that call is
  * undefined), VDX_ERR_RANGE (a rotated q/k value was clamped to the fp16 range; the output
- * is inexact), VDX_ERR_ARG (a q_index entry was out of range; its row was skipped) or
+ * is inexact), VDX_ERR_ARG (a q_index entry was out of range; its row was skipped; or a page,
+ * length or position that the paged-cache or cross-attention calls clamped or skipped) or
  * VDX_ERR_CUDA (an asynchronous CUDA error is pending). */
 vdx_status vdx_sync_check(void* stream);
 

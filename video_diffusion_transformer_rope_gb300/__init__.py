@@ -7,3 +7,5 @@ from ._binding import (VdxError, lib, rope3d_attn, sync_check, shutdown, version
                        K_ROPE_FUSED, KERNEL_DEFAULT, KERNEL_SINGLE, KERNEL_PAIR, QK_FP16, QK_SPLIT, QK_MODES, rope3d_attn_sparse, pack_block_mask,
                        window_block_mask, block_mask_words, SPARSE_QBLOCK, SPARSE_KBLOCK,
                        rope3d_attn_subset)
+from .streaming import (PagedKV, rope3d_append, paged_attn, cross_attn,  # noqa: F401
+                        paged_attn_workspace_bytes, cross_attn_workspace_bytes)

@@ -26,6 +26,43 @@ class AttnOptions(ctypes.Structure):
     _fields_ = [("k_rope", ctypes.c_int), ("qk_precision", ctypes.c_int),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("test_withhold_kv", ctypes.c_int), ("kernel", ctypes.c_int)]
+
+
+_ll, _z = ctypes.c_longlong, ctypes.c_size_t
+DTYPE_BF16, DTYPE_FP16 = 0, 1
+
+
+class PagedKvStruct(ctypes.Structure):
+    """vdx_paged_kv (include/vdx.h)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_page", _ll), ("k_token", _ll), ("k_head", _ll), ("v_page", _ll),
+                ("v_token", _ll), ("v_head", _ll), ("page_table", _p), ("table_stride", _ll), ("num_pages", _i),
+                ("page_size", _i), ("max_pages", _i), ("Hkv", _i), ("d", _i), ("dtype", _i), ("seqs", _i)]
+
+
+class AppendArgs(ctypes.Structure):
+    """vdx_append_args (include/vdx.h)."""
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("q_out", _p), ("q_row", _ll), ("q_head", _ll), ("k_row", _ll),
+                ("k_head", _ll), ("v_row", _ll), ("v_head", _ll), ("q_out_row", _ll), ("q_out_head", _ll),
+                ("rows", _i), ("Hq", _i), ("cu", _p), ("kv_len", _p), ("pos_offset", _p), ("T", _i), ("Hgrid", _i),
+                ("Wgrid", _i), ("sec_t", _i), ("sec_h", _i), ("sec_w", _i), ("theta", _d), ("q_norm", _p),
+                ("k_norm", _p), ("eps", _f)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    """vdx_paged_attn_args (include/vdx.h)."""
+    _fields_ = [("q", _p), ("out", _p), ("lse", _p), ("q_row", _ll), ("q_head", _ll), ("rows", _i), ("Hq", _i),
+                ("cu", _p), ("kv_len", _p), ("max_q", _i), ("max_kv", _i), ("causal_block", _i), ("scale", _f),
+                ("workspace", _p), ("workspace_bytes", _z)]
+
+
+class CrossAttnArgs(ctypes.Structure):
+    """vdx_cross_attn_args (include/vdx.h)."""
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("out", _p), ("lse", _p), ("q_batch", _ll), ("q_row", _ll),
+                ("q_head", _ll), ("k_batch", _ll), ("k_token", _ll), ("k_head", _ll), ("v_batch", _ll),
+                ("v_token", _ll), ("v_head", _ll), ("B", _i), ("N", _i), ("M", _i), ("Hq", _i), ("Hkv", _i),
+                ("d", _i), ("dtype", _i), ("kv_len", _p), ("scale", _f), ("workspace", _p), ("workspace_bytes", _z)]
+
+
 # name -> (restype, argtypes); mirrors include/vdx.h
 SIGNATURES = {
     "vdx_rope3d_attn": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _d, _f, _p]),
@@ -40,6 +77,11 @@ SIGNATURES = {
     "vdx_rope3d_block_mask_words": (_i, [_i, _i, _i]),
     "vdx_window_block_mask": (_i, [_p, _i, _i, _i, _i, _i, _i]),
     "vdx_rope3d_attn_noalloc": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _d, _f, _p]),
+    "vdx_rope3d_append": (_i, [_p, _p, _p]),
+    "vdx_paged_attn": (_i, [_p, _p, _p]),
+    "vdx_paged_attn_workspace_bytes": (ctypes.c_size_t, [_p, _p]),
+    "vdx_cross_attn": (_i, [_p, _p]),
+    "vdx_cross_attn_workspace_bytes": (ctypes.c_size_t, [_p]),
     "vdx_sync_check": (_i, [_p]),
     "vdx_last_error": (ctypes.c_char_p, []),
     "vdx_shutdown": (None, []),

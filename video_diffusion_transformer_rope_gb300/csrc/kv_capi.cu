@@ -1,0 +1,381 @@
+// C-ABI front end of the paged-cache and cross-attention calls: argument checks, the launch plan,
+// dispatch.  Nothing here allocates, synchronises or keeps state between calls.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "kv_internal.h"
+#include "vdx.h"
+
+namespace {
+
+vdx_status fail(vdx_status s, const char* fmt, ...) noexcept {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  try {
+    vdx::set_last_error(buf);
+  } catch (...) {               // no memory for the message: the status still says what happened
+  }
+  return s;
+}
+void clear_error() noexcept { fail(VDX_OK, "%s", ""); }
+
+struct NvtxScope {
+  explicit NvtxScope(const char* name) { nvtxRangePushA(name); }
+  ~NvtxScope() { nvtxRangePop(); }
+};
+
+int multiprocessors() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return 152;
+  }
+  return sms;
+}
+
+// A strided [n0, n1, n2, d] tensor of 2-byte elements; extents of 0 make it empty.
+struct Tensor {
+  const void* ptr;
+  long long n[3];
+  long long stride[3];
+  int d;
+  bool empty() const { return n[0] == 0 || n[1] == 0 || n[2] == 0; }
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(ptr); }
+  uintptr_t end() const {
+    if (empty()) return begin();
+    long long last = d;
+    for (int i = 0; i < 3; ++i) last += (n[i] - 1) * stride[i];
+    return begin() + static_cast<uintptr_t>(last) * 2;
+  }
+};
+bool overlap(const Tensor& a, const Tensor& b) {
+  return !a.empty() && !b.empty() && a.begin() < b.end() && b.begin() < a.end();
+}
+bool overlap(const Tensor& a, const void* p, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  return p && bytes && !a.empty() && a.begin() < x + bytes && x < a.end();
+}
+
+constexpr long long kMaxStride = 1ll << 38;   // elements: a tensor map's strides stay below 2^40 bytes
+constexpr long long kMaxSpan = 1ll << 46;     // elements of a whole tensor
+
+// 16-byte alignment, strides in multiples of 8 elements, no zero stride but the batch's.
+vdx_status check_tensor(const char* name, const Tensor& t, bool batch_may_repeat) {
+  if (t.empty()) return VDX_OK;
+  if (!t.ptr) return fail(VDX_ERR_ARG, "%s must be non-NULL", name);
+  if (t.begin() & 15) return fail(VDX_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  long long span = t.d;
+  for (int i = 0; i < 3; ++i) {
+    if (t.n[i] == 1) continue;
+    const long long s = t.stride[i];
+    if (s < 0 || s > kMaxStride || s % 8)
+      return fail(VDX_ERR_ARG, "%s: stride %lld must be a multiple of 8 elements in [0, 2^38]", name, s);
+    if (s < t.d && !(s == 0 && i == 0 && batch_may_repeat))
+      return fail(VDX_ERR_ARG, "%s: stride %lld is smaller than a row of %d channels", name, s, t.d);
+    if (s && t.n[i] - 1 > kMaxSpan / s) return fail(VDX_ERR_ARG, "%s is too large", name);
+    span += (t.n[i] - 1) * s;
+  }
+  if (span > kMaxSpan) return fail(VDX_ERR_ARG, "%s is too large", name);
+  return VDX_OK;
+}
+
+vdx_status check_i32(const char* name, const int32_t* p, bool optional) {
+  if (!p) return optional ? VDX_OK : fail(VDX_ERR_ARG, "%s must be non-NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 3) return fail(VDX_ERR_ALIGN, "%s is not 4-byte aligned", name);
+  return VDX_OK;
+}
+
+vdx_status check_heads(int Hq, int Hkv, int d, int dtype) {
+  if (dtype != VDX_DTYPE_BF16 && dtype != VDX_DTYPE_FP16) return fail(VDX_ERR_ARG, "unknown dtype %d", dtype);
+  if (d != 64 && d != 128) return fail(VDX_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
+  if (Hkv < 1 || Hq < 1) return fail(VDX_ERR_ARG, "head counts must be >= 1 (got %d and %d)", Hq, Hkv);
+  if (Hq % Hkv) return fail(VDX_ERR_ARG, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(VDX_ERR_UNSUPPORTED, "more than 128 query heads per kv head (%d / %d)", Hq, Hkv);
+  return VDX_OK;
+}
+
+Tensor cache_tensor(const vdx_paged_kv& c, bool v) {
+  Tensor t{v ? c.v : c.k, {c.num_pages, c.page_size, c.Hkv}, {0, 0, 0}, c.d};
+  t.stride[0] = v ? c.v_page : c.k_page;
+  t.stride[1] = v ? c.v_token : c.k_token;
+  t.stride[2] = v ? c.v_head : c.k_head;
+  return t;
+}
+
+vdx_status check_cache(const vdx_paged_kv* c, int Hq) {
+  if (!c) return fail(VDX_ERR_ARG, "the cache must be non-NULL");
+  if (vdx_status s = check_heads(Hq, c->Hkv, c->d, c->dtype)) return s;
+  if (c->seqs < 0 || c->num_pages < 1 || c->max_pages < 1)
+    return fail(VDX_ERR_ARG, "seqs must be >= 0, num_pages and max_pages >= 1 (got %d, %d, %d)", c->seqs, c->num_pages,
+                c->max_pages);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size < 128)
+    return fail(VDX_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or >= 128 (got %d)", c->page_size);
+  if (static_cast<long long>(c->max_pages) * c->page_size > 0x3fffffffll)
+    return fail(VDX_ERR_ARG, "max_pages * page_size = %lld is too large",
+                static_cast<long long>(c->max_pages) * c->page_size);
+  if (c->table_stride < c->max_pages && c->seqs > 1)
+    return fail(VDX_ERR_ARG, "table_stride %lld is smaller than max_pages %d", c->table_stride, c->max_pages);
+  if (c->seqs > 0)
+    if (vdx_status s = check_i32("page_table", c->page_table, false)) return s;
+  if (vdx_status s = check_tensor("the key cache", cache_tensor(*c, false), false)) return s;
+  if (vdx_status s = check_tensor("the value cache", cache_tensor(*c, true), false)) return s;
+  return VDX_OK;
+}
+
+// ------------------------------------------------------------------------------------- attention
+struct Problem {
+  vdx::KvParams p{};
+  int d = 0, dtype = 0;
+  bool nothing = false;        // no rows: nothing to launch
+  size_t workspace = 0;
+};
+
+vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v, long long out_elems,
+                  long long lse_elems, float scale, const void* workspace, size_t workspace_bytes, bool size_only) {
+  vdx::KvParams& p = pb->p;
+  if (!std::isfinite(scale)) return fail(VDX_ERR_ARG, "scale must be finite");
+  p.scale_log2 = static_cast<float>((scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(pb->d))) * 1.4426950408889634);
+  pb->nothing = q.empty();
+  if (pb->nothing) return VDX_OK;
+  if (static_cast<long long>(p.max_q) * p.g > 0x7fffffffll)
+    return fail(VDX_ERR_ARG, "%d rows of %d heads per kv head are too many", p.max_q, p.g);
+  if (vdx_status s = check_tensor("q", q, true)) return s;
+  if (vdx_status s = check_tensor("k", k, true)) return s;
+  if (vdx_status s = check_tensor("v", v, true)) return s;
+  pb->workspace = vdx::plan_attention(&p, pb->d, multiprocessors());
+  if (size_only) return VDX_OK;
+  if (!p.out) return fail(VDX_ERR_ARG, "out must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(p.out) & 15) || (reinterpret_cast<uintptr_t>(p.lse) & 3))
+    return fail(VDX_ERR_ALIGN, "out is not 16-byte aligned or lse not 4-byte aligned");
+  const size_t out_bytes = static_cast<size_t>(out_elems) * 2, lse_bytes = static_cast<size_t>(lse_elems) * 4;
+  const Tensor* in[3] = {&q, &k, &v};
+  const Tensor out{p.out, {1, 1, out_elems / pb->d}, {0, 0, pb->d}, pb->d};
+  for (const Tensor* t : in) {
+    if (overlap(*t, out)) return fail(VDX_ERR_ARG, "out overlaps q, k or v");
+    if (overlap(*t, p.lse, lse_bytes)) return fail(VDX_ERR_ARG, "lse overlaps q, k or v");
+  }
+  if (overlap(out, p.lse, lse_bytes)) return fail(VDX_ERR_ARG, "lse overlaps out");
+  if (pb->workspace) {
+    if (!workspace || workspace_bytes < pb->workspace)
+      return fail(VDX_ERR_ARG, "workspace of %zu bytes is smaller than the %zu needed", workspace ? workspace_bytes : 0,
+                  pb->workspace);
+    if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(VDX_ERR_ALIGN, "workspace is not 16-byte aligned");
+    const uintptr_t w = reinterpret_cast<uintptr_t>(workspace);
+    const uintptr_t l = reinterpret_cast<uintptr_t>(p.lse);
+    if (overlap(q, workspace, pb->workspace) || overlap(k, workspace, pb->workspace) || overlap(v, workspace, pb->workspace) ||
+        overlap(out, workspace, pb->workspace) || (p.lse && w < l + lse_bytes && l < w + pb->workspace))
+      return fail(VDX_ERR_ARG, "workspace overlaps q, k, v, out or lse");
+    uint8_t* ws = const_cast<uint8_t*>(static_cast<const uint8_t*>(workspace));
+    const long long rows = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit * p.block_rows;
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(rows) * pb->d * 4);
+  }
+  (void)out_bytes;
+  return VDX_OK;
+}
+
+vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bool size_only, Problem* pb) {
+  if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
+  if (vdx_status s = check_cache(c, a->Hq)) return s;
+  if (a->rows < 0 || a->max_q < 0 || a->max_kv < 0 || a->causal_block < 0)
+    return fail(VDX_ERR_ARG, "rows, max_q, max_kv and causal_block must be >= 0 (got %d, %d, %d, %d)", a->rows, a->max_q,
+                a->max_kv, a->causal_block);
+  vdx::KvParams& p = pb->p;
+  pb->d = c->d;
+  pb->dtype = c->dtype;
+  p.q = a->q; p.k = c->k; p.v = c->v; p.out = a->out; p.lse = a->lse;
+  p.q_b = 0; p.q_t = a->q_row; p.q_h = a->q_head;
+  p.k_p = c->k_page; p.k_t = c->k_token; p.k_h = c->k_head;
+  p.v_p = c->v_page; p.v_t = c->v_token; p.v_h = c->v_head;
+  p.cu = a->cu; p.kv_len = a->kv_len; p.table = c->page_table;
+  p.table_stride = c->table_stride;
+  p.max_pages = c->max_pages; p.num_pages = c->num_pages; p.P = c->page_size;
+  p.S = c->seqs; p.N = a->rows; p.Hq = a->Hq; p.Hkv = c->Hkv; p.g = a->Hq / c->Hkv;
+  const int cap = c->max_pages * c->page_size;
+  p.max_q = a->max_q > 0 ? std::min(a->max_q, a->rows) : a->rows;
+  p.max_kv = a->max_kv > 0 ? std::min(a->max_kv, cap) : cap;
+  p.causal_block = a->causal_block;
+  const Tensor q{a->q, {1, c->seqs > 0 ? a->rows : 0, a->Hq}, {0, a->q_row, a->q_head}, c->d};
+  if (!q.empty()) {
+    if (vdx_status s = check_i32("cu", a->cu, false)) return s;
+    if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
+  }
+  return finish(pb, q, cache_tensor(*c, false), cache_tensor(*c, true),
+                static_cast<long long>(a->rows) * a->Hq * c->d, a->lse ? static_cast<long long>(a->rows) * a->Hq : 0,
+                a->scale, a->workspace, a->workspace_bytes, size_only);
+}
+
+vdx_status cross_problem(const vdx_cross_attn_args* a, bool size_only, Problem* pb) {
+  if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
+  if (vdx_status s = check_heads(a->Hq, a->Hkv, a->d, a->dtype)) return s;
+  if (a->B < 0 || a->N < 0 || a->M < 0) return fail(VDX_ERR_ARG, "B, N and M must be >= 0 (got %d, %d, %d)", a->B, a->N, a->M);
+  if (a->M > 0x3fffffff) return fail(VDX_ERR_ARG, "M = %d is too large", a->M);
+  vdx::KvParams& p = pb->p;
+  pb->d = a->d;
+  pb->dtype = a->dtype;
+  p.q = a->q; p.k = a->k; p.v = a->v; p.out = a->out; p.lse = a->lse;
+  p.q_b = a->q_batch; p.q_t = a->q_row; p.q_h = a->q_head;
+  p.k_p = a->k_batch; p.k_t = a->k_token; p.k_h = a->k_head;
+  p.v_p = a->v_batch; p.v_t = a->v_token; p.v_h = a->v_head;
+  p.kv_len = a->kv_len;
+  p.num_pages = a->B; p.P = a->M;
+  p.S = a->B; p.N = a->N; p.Hq = a->Hq; p.Hkv = a->Hkv; p.g = a->Hq / a->Hkv;
+  p.max_q = a->N; p.max_kv = a->M;
+  if (vdx_status s = check_i32("kv_len", a->kv_len, true)) return s;
+  const Tensor q{a->q, {a->B, a->N, a->Hq}, {a->q_batch, a->q_row, a->q_head}, a->d};
+  const Tensor k{a->k, {a->B, a->M, a->Hkv}, {a->k_batch, a->k_token, a->k_head}, a->d};
+  const Tensor v{a->v, {a->B, a->M, a->Hkv}, {a->v_batch, a->v_token, a->v_head}, a->d};
+  const long long rows = static_cast<long long>(a->B) * a->N * a->Hq;
+  if (rows > kMaxSpan / a->d) return fail(VDX_ERR_ARG, "out is too large");
+  return finish(pb, q, k, v, rows * a->d, a->lse ? rows : 0, a->scale, a->workspace, a->workspace_bytes, size_only);
+}
+
+vdx_status launch(const Problem& pb, void* stream) {
+  if (pb.nothing) return VDX_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = vdx::launch_attn_rows(pb.p, pb.d, pb.dtype, st);
+  if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
+  if (pb.p.nsplit > 1) {
+    e = vdx::launch_attn_combine(pb.p, pb.d, pb.dtype, st);
+    if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
+  }
+  return VDX_OK;
+}
+
+}  // namespace
+
+namespace vdx {
+
+size_t plan_attention(KvParams* p, int d, int sms) {
+  const long long rows = static_cast<long long>(p->max_q) * p->g;
+  p->rows_kernel = 1;
+  p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  p->nblk = static_cast<int>((rows + p->block_rows - 1) / p->block_rows);
+  const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
+  // Two CTAs to a multiprocessor.  Splits of equal key counts keep ragged lengths balanced: about
+  // four waves of them, but no split below 512 keys (8 blocks per warp), whose start and join
+  // would cost more than its reads.
+  const long long want = static_cast<long long>(p->max_kv) * units / (8ll * sms);
+  long long keys = std::max<long long>(512, (want + 63) / 64 * 64);
+  p->nsplit = static_cast<int>((p->max_kv + keys - 1) / keys);
+  if (p->nsplit <= 1) {
+    p->nsplit = 1;
+    keys = std::max(p->max_kv, 1);
+  }
+  p->split_keys = static_cast<int>(keys);
+  if (p->nsplit == 1) return 0;
+  return static_cast<size_t>(units) * p->nsplit * p->block_rows * (static_cast<size_t>(d) * 4 + 8);
+}
+
+}  // namespace vdx
+
+extern "C" {
+
+vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, void* stream) {
+  NvtxScope nvtx("vdx_rope3d_append");
+  clear_error();
+  if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
+  if (vdx_status s = check_cache(c, a->q ? a->Hq : (c ? c->Hkv : 1))) return s;
+  const int d = c->d;
+  if (a->rows < 0) return fail(VDX_ERR_ARG, "rows must be >= 0 (got %d)", a->rows);
+  if (!a->q != !a->q_out) return fail(VDX_ERR_ARG, "q and q_out go together");
+  if (a->T < 1 || a->Hgrid < 1 || a->Wgrid < 1)
+    return fail(VDX_ERR_ARG, "T, Hgrid and Wgrid must be >= 1 (got %d %d %d)", a->T, a->Hgrid, a->Wgrid);
+  if (static_cast<long long>(a->Hgrid) * a->Wgrid > 0x7fffffffll)
+    return fail(VDX_ERR_ARG, "a frame of %d x %d tokens is too large", a->Hgrid, a->Wgrid);
+  int st = a->sec_t, sh = a->sec_h, sw = a->sec_w;
+  if (st == 0 && sh == 0 && sw == 0) {
+    sh = sw = 2 * (d / 6);
+    st = d - sh - sw;
+  }
+  if (st < 0 || sh < 0 || sw < 0 || ((st | sh | sw) & 1) || static_cast<long long>(st) + sh + sw != d)
+    return fail(VDX_ERR_ARG, "rotary sections %d/%d/%d must be even, non-negative and sum to d=%d", st, sh, sw, d);
+  if (!(a->theta > 0.0) || !std::isfinite(a->theta)) return fail(VDX_ERR_ARG, "theta must be > 0");
+  if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return fail(VDX_ERR_ARG, "eps must be finite and >= 0");
+  if (!a->q && a->q_norm) return fail(VDX_ERR_ARG, "q_norm without q");
+  if (a->rows == 0 || c->seqs == 0) return VDX_OK;
+  const Tensor q{a->q, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_row, a->q_head}, d};
+  const Tensor qo{a->q_out, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_out_row, a->q_out_head}, d};
+  const Tensor k{a->k, {1, a->rows, c->Hkv}, {0, a->k_row, a->k_head}, d};
+  const Tensor v{a->v, {1, a->rows, c->Hkv}, {0, a->v_row, a->v_head}, d};
+  if (vdx_status s = check_tensor("q", q, false)) return s;
+  if (vdx_status s = check_tensor("q_out", qo, false)) return s;
+  if (vdx_status s = check_tensor("k", k, false)) return s;
+  if (vdx_status s = check_tensor("v", v, false)) return s;
+  if (vdx_status s = check_i32("cu", a->cu, false)) return s;
+  if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
+  if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
+  if ((reinterpret_cast<uintptr_t>(a->q_norm) | reinterpret_cast<uintptr_t>(a->k_norm)) & 15)
+    return fail(VDX_ERR_ALIGN, "q_norm or k_norm is not 16-byte aligned");
+  const Tensor kc = cache_tensor(*c, false), vc = cache_tensor(*c, true);
+  const bool in_place = a->q && a->q == a->q_out && a->q_row == a->q_out_row && a->q_head == a->q_out_head;
+  if (a->q && !in_place && (overlap(qo, q) || overlap(qo, k) || overlap(qo, v)))
+    return fail(VDX_ERR_ARG, "q_out overlaps q, k or v");
+  for (const Tensor* t : {&kc, &vc})
+    if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
+      return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
+
+  vdx::AppendParams p{};
+  p.q = a->q; p.k = a->k; p.v = a->v; p.q_out = a->q_out; p.k_cache = c->k; p.v_cache = c->v;
+  p.q_row = a->q_row; p.q_head = a->q_head; p.k_row = a->k_row; p.k_head = a->k_head;
+  p.v_row = a->v_row; p.v_head = a->v_head; p.q_out_row = a->q_out_row; p.q_out_head = a->q_out_head;
+  p.kc_page = c->k_page; p.kc_token = c->k_token; p.kc_head = c->k_head;
+  p.vc_page = c->v_page; p.vc_token = c->v_token; p.vc_head = c->v_head;
+  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->pos_offset;
+  p.table = c->page_table; p.table_stride = c->table_stride;
+  p.q_norm = a->q_norm; p.k_norm = a->k_norm; p.eps = a->eps;
+  p.rows = a->rows; p.S = c->seqs; p.Hq = a->q ? a->Hq : 0; p.Hkv = c->Hkv;
+  p.P = c->page_size; p.num_pages = c->num_pages; p.max_pages = c->max_pages;
+  p.T = a->T; p.Hg = a->Hgrid; p.Wg = a->Wgrid;
+  p.half_t = st / 2; p.half_h = sh / 2;
+  const int sec[3] = {st, sh, sw};
+  int pair = 0;
+  for (int x = 0; x < 3; ++x)
+    for (int j = 0; j < sec[x] / 2; ++j) {
+      const double turns = std::pow(a->theta, -2.0 * j / sec[x]) / 6.283185307179586476925286766559;
+      const double frac = turns - std::floor(turns);
+      p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
+    }
+  const cudaError_t e = vdx::launch_append(p, d, c->dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
+  return VDX_OK;
+}
+
+vdx_status vdx_paged_attn(const vdx_paged_kv* c, const vdx_paged_attn_args* a, void* stream) {
+  NvtxScope nvtx("vdx_paged_attn");
+  clear_error();
+  Problem pb;
+  if (vdx_status s = paged_problem(c, a, false, &pb)) return s;
+  return launch(pb, stream);
+}
+
+size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* c, const vdx_paged_attn_args* a) {
+  clear_error();
+  Problem pb;
+  return paged_problem(c, a, true, &pb) == VDX_OK ? pb.workspace : 0;
+}
+
+vdx_status vdx_cross_attn(const vdx_cross_attn_args* a, void* stream) {
+  NvtxScope nvtx("vdx_cross_attn");
+  clear_error();
+  Problem pb;
+  if (vdx_status s = cross_problem(a, false, &pb)) return s;
+  return launch(pb, stream);
+}
+
+size_t vdx_cross_attn_workspace_bytes(const vdx_cross_attn_args* a) {
+  clear_error();
+  Problem pb;
+  return cross_problem(a, true, &pb) == VDX_OK ? pb.workspace : 0;
+}
+
+}  // extern "C"

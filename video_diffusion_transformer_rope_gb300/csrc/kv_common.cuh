@@ -1,0 +1,140 @@
+// Device helpers shared by the paged-cache and cross-attention kernels: element conversions,
+// sequence lookup, visibility limits, and the translation unit's error word.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cmath>
+#include <cstdint>
+
+#include "kv_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace vdx {
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = unpack2<T>(w[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+}
+// Chunk `lane` of 8 weights as floats (ones without weights).
+template <typename T>
+__device__ __forceinline__ void load8(const void* w, int lane, float (&f)[8]) {
+  if (w) {
+    unpack8<T>(__ldg(static_cast<const uint4*>(w) + lane), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  }
+}
+
+// The last s in [0, S) with cu[s] <= r (0 if none), found by the whole warp: each step its lanes
+// probe 32 evenly spaced starts, so up to 32 sequences take one load.  With cu not decreasing it
+// is the sequence that owns row r, if any does; the caller checks cu[s] <= r < cu[s + 1].
+__device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int S, int r) {
+  int lo = 0, n = S;                      // the answer is in [lo, lo + n)
+  const int lane = threadIdx.x & 31;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int off = lane * step;
+    const bool le = off < n && __ldg(cu + lo + off) <= r;
+    // the highest probe at or below r; probes past a decreasing cu only make the result wrong,
+    // not out of range
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int top = m ? 31 - __clz(m) : 0;
+    lo += top * step;
+    n = min(step, n - top * step);
+  }
+  return lo;
+}
+
+// Rows and keys of one sequence, clamped to what was passed by the host.
+struct SeqInfo {
+  int row0;   // first token in q / out
+  int n;      // tokens
+  int len;    // keys
+};
+__device__ __forceinline__ SeqInfo sequence_info(const KvParams& p, int s, bool report) {
+  SeqInfo q;
+  bool bad = false;
+  if (p.cu) {
+    int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
+    bad = a < 0 || b < a || b > p.N;
+    a = min(max(a, 0), p.N);
+    b = min(max(b, a), p.N);
+    q.row0 = a;
+    q.n = b - a;
+    bad = bad || q.n > p.max_q;
+  } else {
+    q.row0 = 0;
+    q.n = p.N;
+  }
+  if (p.kv_len) {
+    const int len = __ldg(p.kv_len + s);
+    q.len = min(max(len, 0), p.max_kv);
+    bad = bad || len != q.len;
+  } else {
+    q.len = p.max_kv;
+  }
+  if (bad && report) atomicOr(&g_error_word, kErrLength);
+  return q;
+}
+// Keys that row i of the sequence sees: keys 0 .. limit-1.
+__device__ __forceinline__ int visible_limit(const KvParams& p, const SeqInfo& q, int i) {
+  if (p.causal_block <= 0) return q.len;
+  const int pos = q.len - q.n + i;        // q.n may exceed q.len: negative positions see nothing
+  if (pos < 0) return 0;
+  const long long lim = (static_cast<long long>(pos / p.causal_block) + 1) * p.causal_block;
+  return lim < q.len ? static_cast<int>(lim) : q.len;
+}
+
+// Offset of token `tok` of sequence s in q, and in out (elements, head 0).
+__device__ __forceinline__ long long out_row(const KvParams& p, int s, const SeqInfo& q, int tok) {
+  return p.cu ? static_cast<long long>(q.row0) + tok : static_cast<long long>(s) * p.N + tok;
+}
+__device__ __forceinline__ long long lse_index(const KvParams& p, int s, const SeqInfo& q, int h, int tok) {
+  return p.cu ? static_cast<long long>(h) * p.N + q.row0 + tok
+              : (static_cast<long long>(s) * p.Hq + h) * p.N + tok;
+}
+
+// Host: read and reset this translation unit's error word.
+inline cudaError_t read_and_clear_word(unsigned int* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_error_word, sizeof(unsigned int));
+  if (e != cudaSuccess || *word == 0) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+}
+
+}  // namespace vdx

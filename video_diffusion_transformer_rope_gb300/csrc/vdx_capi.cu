@@ -23,6 +23,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "vdx.h"
+#include "kv_internal.h"
 #include "vdx_internal.h"
 
 namespace {
@@ -194,6 +195,7 @@ vdx_status prepare(const void* q, const void* k, const void* v, void* out, float
 
 namespace vdx {
 void set_last_error(const char* message) { t_last_error = message; }
+bool encode_tiled_fn(EncodeTiledFn* fn) { return get_encode(fn) == VDX_OK; }
 }  // namespace vdx
 
 extern "C" {
@@ -436,6 +438,11 @@ vdx_status vdx_sync_check(void* stream) {
   if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "cudaStreamSynchronize: %s", cudaGetErrorString(e));
   unsigned int word = 0;
   e = vdx::read_and_clear_error_word_sm103(&word);
+  for (auto read : {vdx::read_and_clear_error_word_append, vdx::read_and_clear_error_word_rows}) {
+    unsigned int more = 0;
+    if (e == cudaSuccess) e = read(&more);
+    word |= more;
+  }
   if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "reading the error word: %s", cudaGetErrorString(e));
   if (word & 1u)
     return fail(VDX_ERR_TIMEOUT, "a kernel pipeline wait gave up (site %u)", (word >> 8) & 0xff);
@@ -444,6 +451,12 @@ vdx_status vdx_sync_check(void* stream) {
                                "it was clamped and the result is inexact");
   if (word & 4u)
     return fail(VDX_ERR_ARG, "a q_index entry was outside [0, N); those rows were skipped");
+  if (word & vdx::kErrPage)
+    return fail(VDX_ERR_ARG, "a page index was outside the cache; nothing was written there, and its keys read as zeros");
+  if (word & vdx::kErrLength)
+    return fail(VDX_ERR_ARG, "cu or kv_len broke a bound of its call (rows, max_q, max_kv); it was clamped");
+  if (word & vdx::kErrPosition)
+    return fail(VDX_ERR_ARG, "an appended token was outside the position grid or its page table; it was skipped");
   return VDX_OK;
 }
 
