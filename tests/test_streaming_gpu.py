@@ -169,6 +169,9 @@ PAGED = [
     ("bf16", 128, 64, 1, 16, [9, 2], [200, 2], 1),
     ("fp16", 128, 128, 1, 128, [3], [150], 1),
     ("bf16", 128, 1, 1, 128, [2048], [2048], 1),
+    # more units of work than multiprocessors, of very different lengths
+    ("bf16", 128, 12, 4, 64, [1, 300, 0, 77, 500, 33, 257, 2, 128, 90, 400, 5], [900, 300, 10, 1077, 500, 40, 600, 3, 129, 2000, 411, 5], 1),
+    ("fp16", 64, 8, 8, 200, [256, 40, 0, 1, 600, 100, 90, 300], [300, 40, 200, 401, 1000, 150, 2090, 300], 50),
 ]
 
 
@@ -324,6 +327,9 @@ CROSS = [
     ("fp16", 64, 2, 20, 7, 6, 6, [7, 3]),
     ("bf16", 128, 1, 256, 1024, 40, 8, None),
     ("bf16", 128, 4, 700, 129, 1, 1, [129, 128, 0, 64]),
+    # more units of work than multiprocessors: each takes several in turn, some without keys
+    ("bf16", 128, 3, 2000, 300, 20, 20, [300, 0, 130]),
+    ("fp16", 64, 5, 1100, 700, 16, 16, [1, 700, 0, 129, 640]),
 ]
 
 

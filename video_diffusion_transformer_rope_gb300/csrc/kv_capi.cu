@@ -242,8 +242,17 @@ vdx_status cross_problem(const vdx_cross_attn_args* a, bool size_only, Problem* 
 vdx_status launch(const Problem& pb, void* stream) {
   if (pb.nothing) return VDX_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = vdx::launch_attn_rows(pb.p, pb.d, pb.dtype, st);
-  if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
+  cudaError_t e;
+  const char* what = nullptr;
+  if (pb.p.rows_kernel) {
+    e = vdx::launch_attn_rows(pb.p, pb.d, pb.dtype, st);
+  } else {
+    vdx::EncodeTiledFn encode = nullptr;
+    if (!vdx::encode_tiled_fn(&encode)) return VDX_ERR_CUDA;
+    e = vdx::launch_attn_tiles(pb.p, pb.d, pb.dtype, encode, multiprocessors(), st, &what);
+  }
+  if (e != cudaSuccess)
+    return fail(VDX_ERR_CUDA, "attention kernel launch: %s%s%s", what ? what : "", what ? ": " : "", cudaGetErrorString(e));
   if (pb.p.nsplit > 1) {
     e = vdx::launch_attn_combine(pb.p, pb.d, pb.dtype, st);
     if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
@@ -257,22 +266,50 @@ namespace vdx {
 
 size_t plan_attention(KvParams* p, int d, int sms) {
   const long long rows = static_cast<long long>(p->max_q) * p->g;
-  p->rows_kernel = 1;
-  p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-  p->nblk = static_cast<int>((rows + p->block_rows - 1) / p->block_rows);
-  const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
-  // Two CTAs to a multiprocessor.  Splits of equal key counts keep ragged lengths balanced: about
-  // four waves of them, but no split below 512 keys (8 blocks per warp), whose start and join
-  // would cost more than its reads.
-  const long long want = static_cast<long long>(p->max_kv) * units / (8ll * sms);
-  long long keys = std::max<long long>(512, (want + 63) / 64 * 64);
-  p->nsplit = static_cast<int>((p->max_kv + keys - 1) / keys);
-  if (p->nsplit <= 1) {
+  p->rows_kernel = rows <= 32;
+  if (p->rows_kernel) {
+    p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+    p->nblk = 1;
+    const long long units = static_cast<long long>(p->S) * p->Hkv;
+    // Two CTAs to a multiprocessor.  Splits of equal key counts keep ragged lengths balanced: about
+    // four waves of them, but no split below 512 keys (8 blocks per warp), whose start and join
+    // would cost more than its reads.
+    const long long want = static_cast<long long>(p->max_kv) * units / (8ll * sms);
+    long long keys = std::max<long long>(512, (want + 63) / 64 * 64);
+    p->nsplit = static_cast<int>((p->max_kv + keys - 1) / keys);
+    if (p->nsplit <= 1) {
+      p->nsplit = 1;
+      keys = std::max(p->max_kv, 1);
+    }
+    p->split_keys = static_cast<int>(keys);
+  } else {
+    const int per = 2 * (128 / p->g);                 // tokens of a block
+    p->block_rows = per * p->g;
+    p->nblk = (p->max_q - 1) / per + 1;
+    const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
+    const bool small = p->table && p->P < 128;
+    long long tiles = 1;
+    if (p->max_kv > 0)
+      tiles = small ? (p->max_kv + 127) / 128
+                    : static_cast<long long>(p->max_kv / p->P) * ((p->P + 127) / 128) + (p->max_kv % p->P + 127) / 128;
+    // Splits: the persistent CTAs take ceil(units * splits / sms) units each, a unit costs its
+    // tiles and about two tiles' time to start and finish; a split call also writes and joins
+    // partial results (about a tile's time per unit).
+    long long best = 0;
     p->nsplit = 1;
-    keys = std::max(p->max_kv, 1);
+    for (int n = 1; n <= 32 && n <= tiles; ++n) {
+      const long long per_split = (tiles + n - 1) / n;
+      const long long cost = (units * n + sms - 1) / sms * (per_split + (n > 1 ? 3 : 2));
+      if (n == 1 || cost < best) {
+        best = cost;
+        p->nsplit = n;
+      }
+    }
+    p->split_keys = static_cast<int>((tiles + p->nsplit - 1) / p->nsplit);
+    p->nsplit = static_cast<int>((tiles + p->split_keys - 1) / p->split_keys);
   }
-  p->split_keys = static_cast<int>(keys);
   if (p->nsplit == 1) return 0;
+  const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
   return static_cast<size_t>(units) * p->nsplit * p->block_rows * (static_cast<size_t>(d) * 4 + 8);
 }
 

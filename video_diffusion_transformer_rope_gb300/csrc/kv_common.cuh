@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv_internal.h"
 #include "sm103_ptx.cuh"

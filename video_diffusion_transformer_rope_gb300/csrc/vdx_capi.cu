@@ -438,7 +438,8 @@ vdx_status vdx_sync_check(void* stream) {
   if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "cudaStreamSynchronize: %s", cudaGetErrorString(e));
   unsigned int word = 0;
   e = vdx::read_and_clear_error_word_sm103(&word);
-  for (auto read : {vdx::read_and_clear_error_word_append, vdx::read_and_clear_error_word_rows}) {
+  for (auto read : {vdx::read_and_clear_error_word_append, vdx::read_and_clear_error_word_rows,
+                    vdx::read_and_clear_error_word_tiles}) {
     unsigned int more = 0;
     if (e == cudaSuccess) e = read(&more);
     word |= more;
