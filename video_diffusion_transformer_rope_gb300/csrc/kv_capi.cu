@@ -283,23 +283,26 @@ size_t plan_attention(KvParams* p, int d, int sms) {
     }
     p->split_keys = static_cast<int>(keys);
   } else {
-    const int per = 2 * (128 / p->g);                 // tokens of a block
+    const int per = 4 * (128 / p->g);                 // tokens of a block: two Q tiles of two CTAs
     p->block_rows = per * p->g;
     p->nblk = (p->max_q - 1) / per + 1;
     const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
-    const bool small = p->table && p->P < 128;
+    // Tiles cross page ends where a page is a multiple of 8 keys (a swizzle atom of the copies); the
+    // largest power of two up to 64 that divides it is the box.  Dense keys are one page.
+    p->box_rows = 0;
+    if (p->table && p->P % 8 == 0) p->box_rows = std::min(64, p->P & -p->P);
     long long tiles = 1;
     if (p->max_kv > 0)
-      tiles = small ? (p->max_kv + 127) / 128
+      tiles = p->box_rows ? (p->max_kv + 127) / 128
                     : static_cast<long long>(p->max_kv / p->P) * ((p->P + 127) / 128) + (p->max_kv % p->P + 127) / 128;
-    // Splits: the persistent CTAs take ceil(units * splits / sms) units each, a unit costs its
+    // Splits: the sms / 2 CTA pairs take ceil(units * splits / pairs) units each, a unit costs its
     // tiles and about two tiles' time to start and finish; a split call also writes and joins
     // partial results (about a tile's time per unit).
     long long best = 0;
     p->nsplit = 1;
     for (int n = 1; n <= 32 && n <= tiles; ++n) {
       const long long per_split = (tiles + n - 1) / n;
-      const long long cost = (units * n + sms - 1) / sms * (per_split + (n > 1 ? 3 : 2));
+      const long long cost = (units * n + sms / 2 - 1) / (sms / 2) * (per_split + (n > 1 ? 3 : 2));
       if (n == 1 || cost < best) {
         best = cost;
         p->nsplit = n;
