@@ -11,8 +11,20 @@ from . import _binding as B
 from ._binding import VDX_ERR_ARG, VDX_ERR_UNSUPPORTED, VdxError
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported on first use (the library itself loads without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dtype(t):
-    import torch
+    torch = _t()
     if t.dtype == torch.bfloat16:
         return B.DTYPE_BF16
     if t.dtype == torch.float16:
@@ -20,26 +32,35 @@ def _dtype(t):
     raise VdxError(VDX_ERR_UNSUPPORTED, f"dtype {t.dtype} (use bfloat16 or float16)")
 
 
-def _tensor(name, t, like, dims, writable=False):
-    """A CUDA tensor of `dims` dimensions on like's device with like's dtype and dense channels."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device or t.dtype != like.dtype:
+def _tensor(name, t, like, dims):
+    """A CUDA tensor of `dims` dimensions on like's device with like's dtype and dense channels; its
+    shape and strides."""
+    torch = _torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != like.get_device() or t.dtype != like.dtype:
         raise VdxError(VDX_ERR_ARG, f"{name} must be a CUDA tensor of dtype {like.dtype} on {like.device}")
-    if t.dim() != dims:
-        raise VdxError(VDX_ERR_ARG, f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise VdxError(VDX_ERR_ARG, f"{name} must have {dims} dimensions, got {tuple(shape)}")
+    if stride[-1] != 1 and shape[-1] > 1:
         raise VdxError(VDX_ERR_ARG, f"{name}: the channels of a head must be contiguous")
     if t.requires_grad and torch.is_grad_enabled():
         raise VdxError(VDX_ERR_UNSUPPORTED, f"{name} requires a gradient: these calls are forward only "
                                             "(use torch.no_grad() or detach())")
+    return shape, stride
+
+
+def _cuda(name, t):
+    torch = _t()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise VdxError(VDX_ERR_ARG, f"{name} must be a CUDA tensor")
 
 
 def _int32(name, t, like, length):
-    import torch
     if t is None:
         return 0
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device or t.dtype != torch.int32
-            or t.dim() != 1 or t.shape[0] != length or (length > 1 and t.stride(0) != 1)):
+    torch = _torch
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.get_device() != like.get_device()
+            or tuple(t.shape) != (length,) or not t.is_contiguous()):
         raise VdxError(VDX_ERR_ARG, f"{name} must be a contiguous int32 CUDA tensor of {length} values on {like.device}")
     return t.data_ptr()
 
@@ -52,22 +73,29 @@ def _int(name, x, least=0):
 
 
 class _On:
-    """The tensors' device and the call's stream are current inside; .handle is the stream."""
+    """The tensors' device and the call's stream are current inside; .handle is the stream.  Where they
+    are already, which is the usual call, nothing is switched (the switch and back costs more host
+    time than the launch)."""
 
     def __init__(self, like, stream):
-        import torch
-        self.stream = torch.cuda.current_stream(like.device) if stream is None else stream
-        if self.stream.device != like.device:
-            raise VdxError(VDX_ERR_ARG, f"the stream is on {self.stream.device}, the tensors on {like.device}")
-        self.ctx = torch.cuda.stream(self.stream)       # also makes the stream's device current
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+        torch = _torch
+        dev = like.get_device()
+        if stream is None:
+            self.handle = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+            self.ctx = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+            return
+        if stream.device != like.device:
+            raise VdxError(VDX_ERR_ARG, f"the stream is on {stream.device}, the tensors on {like.device}")
+        self.handle = ctypes.c_void_p(stream.cuda_stream)
+        self.ctx = torch.cuda.stream(stream)            # also makes the stream's device current
 
     def __enter__(self):
-        self.ctx.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
         return self
 
     def __exit__(self, *a):
-        return self.ctx.__exit__(*a)
+        return None if self.ctx is None else self.ctx.__exit__(*a)
 
 
 @dataclass
@@ -81,20 +109,19 @@ class PagedKV:
     page_table: Any
 
     def _struct(self):
-        import torch
         k, v, t = self.k, self.v, self.page_table
-        if not isinstance(k, torch.Tensor) or not k.is_cuda:
-            raise VdxError(VDX_ERR_ARG, "the key cache must be a CUDA tensor")
-        _tensor("the key cache", k, k, 4)
-        _tensor("the value cache", v, k, 4)
-        if k.shape != v.shape:
-            raise VdxError(VDX_ERR_ARG, f"the key and value caches differ in shape: {tuple(k.shape)}, {tuple(v.shape)}")
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != k.device or t.dim() != 2
-                or (t.shape[1] > 1 and t.stride(1) != 1)):
+        _cuda("the key cache", k)
+        ks, kst = _tensor("the key cache", k, k, 4)
+        vs, vst = _tensor("the value cache", v, k, 4)
+        if ks != vs:
+            raise VdxError(VDX_ERR_ARG, f"the key and value caches differ in shape: {tuple(ks)}, {tuple(vs)}")
+        torch = _torch
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.get_device() != k.get_device()
+                or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
             raise VdxError(VDX_ERR_ARG, f"page_table must be an int32 [seqs, max_pages] tensor on {k.device} with contiguous rows")
-        return B.PagedKvStruct(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1),
-                               v.stride(2), t.data_ptr(), t.stride(0), k.shape[0], k.shape[1], t.shape[1], k.shape[2],
-                               k.shape[3], _dtype(k), t.shape[0])
+        seqs, width = t.shape
+        return B.PagedKvStruct(k.data_ptr(), v.data_ptr(), kst[0], kst[1], kst[2], vst[0], vst[1], vst[2], t.data_ptr(),
+                               t.stride(0), ks[0], ks[1], width, ks[2], ks[3], _dtype(k), seqs)
 
 
 def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10000.0, pos_offset=None, q_norm=None,
@@ -109,39 +136,37 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
     the rotation.  Slices of a fused projection are taken as they are."""
     sc = cache._struct()
     like = cache.k
-    for name, t, h in (("q", q, None), ("k", k, sc.Hkv), ("v", v, sc.Hkv)):
-        if t is None and name == "q":
-            continue
-        _tensor(name, t, like, 3)
-        if t.shape[0] != k.shape[0] or t.shape[2] != sc.d or (h is not None and t.shape[1] != h):
-            raise VdxError(VDX_ERR_ARG, f"{name} {tuple(t.shape)} does not match [rows, heads, d] of k {tuple(k.shape)} and "
-                                        f"the cache's {sc.Hkv} heads of {sc.d}")
+    ks, kst = _tensor("k", k, like, 3)
+    vs, vst = _tensor("v", v, like, 3)
+    rows, d = ks[0], sc.d
+    if ks[1] != sc.Hkv or ks[2] != d or vs != ks:
+        raise VdxError(VDX_ERR_ARG, f"k {tuple(ks)} and v {tuple(vs)} must be [rows, {sc.Hkv}, {d}], as the cache's heads")
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            _tensor(name, w, like, 1)
-            if w.shape[0] != sc.d:
-                raise VdxError(VDX_ERR_ARG, f"{name} must hold {sc.d} weights")
+        if w is not None and _tensor(name, w, like, 1)[0][0] != d:
+            raise VdxError(VDX_ERR_ARG, f"{name} must hold {d} weights")
     T, Hg, Wg = (_int("grid", x) for x in grid)
     st, sh, sw = (_int("sections", x) for x in sections)
+    Hq, qst, ost = 0, (0, 0), (0, 0)
+    if q is not None:
+        qs, qst = _tensor("q", q, like, 3)
+        Hq = qs[1]
+        if qs[0] != rows or qs[2] != d:
+            raise VdxError(VDX_ERR_ARG, f"q {tuple(qs)} does not match the {rows} rows of {d} channels of k")
+    elif q_out is not None:
+        raise VdxError(VDX_ERR_ARG, "q_out without q")
     with _On(like, stream) as on:
-        import torch
-        if q is None:
-            if q_out is not None:
-                raise VdxError(VDX_ERR_ARG, "q_out without q")
-        elif q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            _tensor("q_out", q_out, like, 3)
-            if q_out.shape != q.shape:
-                raise VdxError(VDX_ERR_ARG, f"q_out must be shaped like q {tuple(q.shape)}")
-        qs = (q.stride(0), q.stride(1)) if q is not None else (0, 0)
-        os_ = (q_out.stride(0), q_out.stride(1)) if q is not None else (0, 0)
+        if q is not None:
+            if q_out is None:
+                q_out = _torch.empty(qs, dtype=q.dtype, device=q.device)
+            os_, ost = _tensor("q_out", q_out, like, 3)
+            if os_ != qs:
+                raise VdxError(VDX_ERR_ARG, f"q_out must be shaped like q {tuple(qs)}")
         a = B.AppendArgs(q.data_ptr() if q is not None else 0, k.data_ptr(), v.data_ptr(),
-                         q_out.data_ptr() if q is not None else 0, *qs, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                         *os_, k.shape[0], q.shape[1] if q is not None else 0, _int32("cu", cu, like, sc.seqs + 1),
+                         q_out.data_ptr() if q is not None else 0, qst[0], qst[1], kst[0], kst[1], vst[0], vst[1],
+                         ost[0], ost[1], rows, Hq, _int32("cu", cu, like, sc.seqs + 1),
                          _int32("kv_len", kv_len, like, sc.seqs), _int32("pos_offset", pos_offset, like, sc.seqs), T, Hg, Wg,
-                         st, sh, sw, float(theta), q_norm.data_ptr() if q_norm is not None else 0,
-                         k_norm.data_ptr() if k_norm is not None else 0, float(eps))
+                         st, sh, sw, theta, q_norm.data_ptr() if q_norm is not None else 0,
+                         k_norm.data_ptr() if k_norm is not None else 0, eps)
         if q is not None and q.numel() == 0:            # no rows: empty tensors have no address
             return q_out
         B._check(B.lib().vdx_rope3d_append(ctypes.byref(sc), ctypes.byref(a), on.handle))
@@ -149,7 +174,7 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
 
 
 def _outputs(q, lse_shape, out, lse, return_lse):
-    import torch
+    torch = _torch
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
@@ -159,34 +184,40 @@ def _outputs(q, lse_shape, out, lse, return_lse):
     if lse is None:
         if return_lse:
             lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-    elif (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(lse_shape) or not lse.is_contiguous()
-          or lse.device != q.device):
+    elif (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != tuple(lse_shape)
+          or not lse.is_contiguous() or lse.device != q.device):
         raise VdxError(VDX_ERR_ARG, f"lse must be a contiguous float32 tensor of shape {tuple(lse_shape)} on {q.device}")
     return out, lse
 
 
-def _with_workspace(args, size_fn, run_fn, workspace, like, on):
+def _with_workspace(args, size_fn, run_fn, first, workspace, like, on):
     """Fill args.workspace (the caller's tensor, or one taken from torch's allocator for this call on
     its stream) and run."""
-    import torch
+    torch = _torch
+    ref = ctypes.byref(args)
     if workspace is not None:
         if (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.device != like.device
                 or not workspace.is_contiguous()):
             raise VdxError(VDX_ERR_ARG, f"workspace must be a contiguous CUDA tensor on {like.device}")
     else:
-        need = size_fn()
+        need = size_fn(*first, ref)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     if workspace is not None:
         args.workspace = workspace.data_ptr()
         args.workspace_bytes = workspace.numel() * workspace.element_size()
-    B._check(run_fn(on.handle))
+    B._check(run_fn(*first, ref, on.handle))
 
 
-def _paged_args(q, sc, cu, kv_len, max_q, max_kv, causal_block, scale):
-    return B.PagedAttnArgs(q.data_ptr(), 0, 0, q.stride(0), q.stride(1), q.shape[0], q.shape[1],
-                           _int32("cu", cu, q, sc.seqs + 1), _int32("kv_len", kv_len, q, sc.seqs), _int("max_q", max_q or 0),
-                           _int("max_kv", max_kv or 0), _int("causal_block", causal_block), float(scale), 0, 0)
+def _paged_args(q, cache, cu, kv_len, max_q, max_kv, causal_block, scale):
+    sc = cache._struct()
+    shape, stride = _tensor("q", q, cache.k, 3)
+    if shape[2] != sc.d:
+        raise VdxError(VDX_ERR_ARG, f"q {tuple(shape)} does not match the cache's head dimension {sc.d}")
+    return sc, B.PagedAttnArgs(q.data_ptr(), 0, 0, stride[0], stride[1], shape[0], shape[1],
+                               _int32("cu", cu, q, sc.seqs + 1), _int32("kv_len", kv_len, q, sc.seqs),
+                               _int("max_q", max_q or 0), _int("max_kv", max_kv or 0), _int("causal_block", causal_block),
+                               scale, 0, 0)
 
 
 def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, scale=0.0, out=None, lse=None,
@@ -201,42 +232,34 @@ def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, sc
 
     Returns (out [rows, Hq, d], lse [Hq, rows] float32 or None); rows outside every sequence are left
     as they were in out / lse."""
-    sc = cache._struct()
-    _tensor("q", q, cache.k, 3)
-    if q.shape[2] != sc.d:
-        raise VdxError(VDX_ERR_ARG, f"q {tuple(q.shape)} does not match the cache's head dimension {sc.d}")
-    a = _paged_args(q, sc, cu, kv_len, max_q, max_kv, causal_block, scale)
+    sc, a = _paged_args(q, cache, cu, kv_len, max_q, max_kv, causal_block, scale)
     L = B.lib()
     with _On(q, stream) as on:
-        out, lse = _outputs(q, (q.shape[1], q.shape[0]), out, lse, return_lse)
-        a.out, a.lse = out.data_ptr(), lse.data_ptr() if lse is not None else 0
-        _with_workspace(a, lambda: L.vdx_paged_attn_workspace_bytes(ctypes.byref(sc), ctypes.byref(a)),
-                        lambda h: L.vdx_paged_attn(ctypes.byref(sc), ctypes.byref(a), h), workspace, q, on)
+        out, lse = _outputs(q, (a.Hq, a.rows), out, lse, return_lse)
+        a.out = out.data_ptr()
+        if lse is not None:
+            a.lse = lse.data_ptr()
+        _with_workspace(a, L.vdx_paged_attn_workspace_bytes, L.vdx_paged_attn, (ctypes.byref(sc),), workspace, q, on)
     return out, lse
 
 
 def paged_attn_workspace_bytes(q, cache, cu, kv_len, max_q=None, max_kv=None):
     """Bytes of scratch that paged_attn needs for these arguments."""
-    import torch
-    sc = cache._struct()
-    a = _paged_args(q, sc, cu, kv_len, max_q, max_kv, 0, 0.0)
-    with torch.cuda.device(q.device):
+    sc, a = _paged_args(q, cache, cu, kv_len, max_q, max_kv, 0, 0.0)
+    with _t().cuda.device(q.device):
         return B.lib().vdx_paged_attn_workspace_bytes(ctypes.byref(sc), ctypes.byref(a))
 
 
 def _cross_args(q, k, v, kv_len, scale):
-    import torch
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise VdxError(VDX_ERR_ARG, "q must be a CUDA tensor")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _tensor(name, t, q, 4)
-    Bn, N, Hq, d = q.shape
-    if k.shape != v.shape or k.shape[0] != Bn or k.shape[3] != d:
-        raise VdxError(VDX_ERR_ARG, f"q [B, N, Hq, d], k and v [B, M, Hkv, d]: got {tuple(q.shape)}, {tuple(k.shape)}, "
-                                    f"{tuple(v.shape)}")
-    return B.CrossAttnArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), 0, 0, *q.stride()[:3], *k.stride()[:3],
-                           *v.stride()[:3], Bn, N, k.shape[1], Hq, k.shape[2], d, _dtype(q),
-                           _int32("kv_len", kv_len, q, Bn), float(scale), 0, 0)
+    _cuda("q", q)
+    qs, qst = _tensor("q", q, q, 4)
+    ks, kst = _tensor("k", k, q, 4)
+    vs, vst = _tensor("v", v, q, 4)
+    if ks != vs or ks[0] != qs[0] or ks[3] != qs[3]:
+        raise VdxError(VDX_ERR_ARG, f"q [B, N, Hq, d], k and v [B, M, Hkv, d]: got {tuple(qs)}, {tuple(ks)}, {tuple(vs)}")
+    return B.CrossAttnArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), 0, 0, qst[0], qst[1], qst[2], kst[0], kst[1], kst[2],
+                           vst[0], vst[1], vst[2], qs[0], qs[1], ks[1], qs[2], ks[2], qs[3], _dtype(q),
+                           _int32("kv_len", kv_len, q, qs[0]), scale, 0, 0)
 
 
 def cross_attn(q, k, v, kv_len=None, scale=0.0, out=None, lse=None, return_lse=True, stream=None, workspace=None):
@@ -248,16 +271,16 @@ def cross_attn(q, k, v, kv_len=None, scale=0.0, out=None, lse=None, return_lse=T
     a = _cross_args(q, k, v, kv_len, scale)
     L = B.lib()
     with _On(q, stream) as on:
-        out, lse = _outputs(q, (q.shape[0], q.shape[2], q.shape[1]), out, lse, return_lse)
-        a.out, a.lse = out.data_ptr(), lse.data_ptr() if lse is not None else 0
-        _with_workspace(a, lambda: L.vdx_cross_attn_workspace_bytes(ctypes.byref(a)),
-                        lambda h: L.vdx_cross_attn(ctypes.byref(a), h), workspace, q, on)
+        out, lse = _outputs(q, (a.B, a.Hq, a.N), out, lse, return_lse)
+        a.out = out.data_ptr()
+        if lse is not None:
+            a.lse = lse.data_ptr()
+        _with_workspace(a, L.vdx_cross_attn_workspace_bytes, L.vdx_cross_attn, (), workspace, q, on)
     return out, lse
 
 
 def cross_attn_workspace_bytes(q, k, v, kv_len=None):
     """Bytes of scratch that cross_attn needs for these arguments."""
-    import torch
     a = _cross_args(q, k, v, kv_len, 0.0)
-    with torch.cuda.device(q.device):
+    with _t().cuda.device(q.device):
         return B.lib().vdx_cross_attn_workspace_bytes(ctypes.byref(a))
