@@ -9,8 +9,10 @@
 // padding, and a warp needs no other warp: it streams its own 16-key blocks through its own
 // ring of cp.async stages (any page size, stride or token order; rows past the end are filled
 // with zeros, so what the cache holds there is never used), and keeps its own running maximum,
-// sum and accumulator.  The warps of a CTA join through shared memory at the end, the splits of a
-// long cache through the workspace and the join kernel below.
+// sum and accumulator.  The warps of a CTA join through shared memory at the end.  Splits of the keys,
+// up to 8 of them, are the CTAs of a cluster and join through one another's shared memory (no second
+// launch, no scratch: 16 to 9 us for 4 sequences of up to 1000 keys); more, for a few heads over a
+// long cache, join through the workspace and the kernel below.
 //
 // The running maximum moves only when a score exceeds it by more than 8 (log2 units): until then
 // weights stay below 2^8, exact in the fp32 sums, and no lane has to talk to another.
@@ -61,6 +63,18 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // kNT tiles of 8 query rows.
 template <typename T, int D, int kNT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
@@ -87,12 +101,14 @@ attn_rows(const __grid_constant__ KvParams p) {
   if (first_row >= all_rows) return;
   const int live = static_cast<int>(min(static_cast<long long>(kRows), all_rows - first_row));
 
-  // Keys of this split, up to the last row's limit.
+  // Keys of this split, up to the last row's limit: an equal part for each CTA of a cluster, which
+  // wait for one another; fixed ranges otherwise (a CTA past a short sequence's end leaves).
   const int last_tok = static_cast<int>((first_row + live - 1) / p.g);
   const int len = visible_limit(p, sq, last_tok);
-  const long long lo64 = static_cast<long long>(z) * p.split_keys;
+  const long long keys = p.cluster ? (len / (kKeys * kWarps) / p.nsplit + 1) * (kKeys * kWarps) : p.split_keys;
+  const long long lo64 = z * keys;
   const int lo = static_cast<int>(min(lo64, static_cast<long long>(len)));
-  const int hi = static_cast<int>(min(lo64 + p.split_keys, static_cast<long long>(len)));
+  const int hi = static_cast<int>(min(lo64 + keys, static_cast<long long>(len)));
 
   // Query fragments (B operand: k = channel, n = row): row 8*nt + gq, channels 16*ks + 2*c4 (+8).
   uint32_t qf[kNT][D / 16][2];
@@ -305,6 +321,19 @@ attn_rows(const __grid_constant__ KvParams p) {
   __syncthreads();
   // Four channels per thread.
   const long long slot = static_cast<long long>(unit) * p.nsplit + z;
+  float* cm = sl + kWarps * kRows;                                  // [kRows]: this CTA's maximum and sum
+  float* cl = cm + kRows;
+  auto store = [&](int r, int dq, float mx, float lt, const float4& acc) {
+    const long long R = first_row + r;
+    const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
+    const float inv = mx == -INFINITY ? 0.f : 1.f / lt;
+    uint2 w2;
+    w2.x = pack2<T>(acc.x * inv, acc.y * inv);
+    w2.y = pack2<T>(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D + dq) = w2;
+    if (dq == 0 && p.lse)
+      p.lse[lse_index(p, s, sq, h, tok)] = mx == -INFINITY ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
+  };
   for (int i = threadIdx.x; i < live * (D / 4); i += kWarps * 32) {
     const int r = i / (D / 4), dq = (i % (D / 4)) * 4;
     float mx = -INFINITY;
@@ -320,21 +349,38 @@ attn_rows(const __grid_constant__ KvParams p) {
       lt += wt * sl[w * kRows + r];
       acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
     }
-    if (p.nsplit > 1) {
+    if (p.cluster) {
+      *reinterpret_cast<float4*>(so + r * kPad + dq) = acc;          // over warp 0's, which only this thread reads
+      if (dq == 0) {
+        cm[r] = mx;
+        cl[r] = lt;
+      }
+    } else if (p.nsplit > 1) {
       *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + dq) = acc;
       if (dq == 0) p.part_ml[slot * kRows + r] = make_float2(mx, lt);
-      continue;
+    } else {
+      store(r, dq, mx, lt, acc);
     }
-    const long long R = first_row + r;
-    const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
-    const float inv = mx == -INFINITY ? 0.f : 1.f / lt;
-    uint2 w2;
-    w2.x = pack2<T>(acc.x * inv, acc.y * inv);
-    w2.y = pack2<T>(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D + dq) = w2;
-    if (dq == 0 && p.lse)
-      p.lse[lse_index(p, s, sq, h, tok)] = mx == -INFINITY ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
   }
+  if (!p.cluster) return;
+  cluster_sync_all();                   // every CTA's part is in its shared memory
+  for (int i = threadIdx.x + z * kWarps * 32; i < live * (D / 4); i += p.nsplit * kWarps * 32) {
+    const int r = i / (D / 4), dq = (i % (D / 4)) * 4;
+    const uint32_t am = smem_addr(cm + r), al = smem_addr(cl + r), ao = smem_addr(so + r * kPad + dq);
+    float mx = -INFINITY;
+    for (int w = 0; w < p.nsplit; ++w) mx = fmaxf(mx, ld_cluster_f32(mapa_shared(am, w)));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float lt = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < p.nsplit; ++w) {
+      const float wt = ex2_approx(ld_cluster_f32(mapa_shared(am, w)) - base);
+      const float4 v = ld_cluster_f32x4(mapa_shared(ao, w));
+      lt += wt * ld_cluster_f32(mapa_shared(al, w));
+      acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
+    }
+    store(r, dq, mx, lt, acc);
+  }
+  cluster_sync_all();                   // no CTA leaves while another reads its part
 }
 
 // Join the key splits of every row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.  One warp
@@ -382,14 +428,25 @@ attn_join(const __grid_constant__ KvParams p) {
 template <typename T, int D, int kNT>
 cudaError_t launch_nt(const KvParams& p, cudaStream_t stream) {
   const int ring = kWarps * kStages * 2 * kKeys * D * 2;
-  const int join = kWarps * 8 * kNT * (D + 4 + 2) * 4;
+  const int join = (kWarps * (D + 4 + 2) + 2) * 8 * kNT * 4;
   const int smem = ring > join ? ring : join;
   cudaError_t e = cudaFuncSetAttribute(attn_rows<T, D, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  attn_rows<T, D, kNT><<<static_cast<unsigned>(blocks), kWarps * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster ? static_cast<unsigned>(p.nsplit) : 1u;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_rows<T, D, kNT>, p);
 }
 template <typename T, int D>
 cudaError_t launch(const KvParams& p, cudaStream_t stream) {

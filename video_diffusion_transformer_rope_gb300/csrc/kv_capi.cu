@@ -253,7 +253,7 @@ vdx_status launch(const Problem& pb, void* stream) {
   }
   if (e != cudaSuccess)
     return fail(VDX_ERR_CUDA, "attention kernel launch: %s%s%s", what ? what : "", what ? ": " : "", cudaGetErrorString(e));
-  if (pb.p.nsplit > 1) {
+  if (pb.p.nsplit > 1 && !pb.p.cluster) {
     e = vdx::launch_attn_combine(pb.p, pb.d, pb.dtype, st);
     if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
   }
@@ -271,17 +271,24 @@ size_t plan_attention(KvParams* p, int d, int sms) {
     p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
     p->nblk = 1;
     const long long units = static_cast<long long>(p->S) * p->Hkv;
-    // Two CTAs to a multiprocessor.  Splits of equal key counts keep ragged lengths balanced: about
-    // four waves of them, but no split below 512 keys (8 blocks per warp), whose start and join
-    // would cost more than its reads.
-    const long long want = static_cast<long long>(p->max_kv) * units / (8ll * sms);
-    long long keys = std::max<long long>(512, (want + 63) / 64 * 64);
-    p->nsplit = static_cast<int>((p->max_kv + keys - 1) / keys);
-    if (p->nsplit <= 1) {
-      p->nsplit = 1;
-      keys = std::max(p->max_kv, 1);
+    // Two CTAs to a multiprocessor.  About four waves of splits keep ragged lengths balanced, and no
+    // split is below 256 keys (four blocks per warp), whose start would cost more than its reads.
+    const long long slots = 2ll * sms;
+    const long long want = static_cast<long long>(p->max_kv) * units / (4 * slots);
+    long long keys = std::max<long long>(256, (want + 63) / 64 * 64);
+    long long n = (p->max_kv + keys - 1) / keys;
+    // Short caches of few sequences: one wave at most.  Up to 8 splits are a cluster and join in it,
+    // also where more are wanted but 8 occupy the device; else they join through the workspace.
+    if (units * n > slots && units * n < 2 * slots) n = std::max<long long>(1, slots / units);
+    if (n > 8 && units * 8 >= slots) n = 8;
+    p->cluster = n > 1 && n <= 8;
+    if (!p->cluster && n > 1) {
+      keys = std::max<long long>(512, keys);
+      n = (p->max_kv + keys - 1) / keys;
     }
-    p->split_keys = static_cast<int>(keys);
+    p->nsplit = static_cast<int>(std::max<long long>(1, n));
+    p->split_keys = static_cast<int>(p->nsplit > 1 ? keys : std::max(p->max_kv, 1));
+    if (p->cluster) return 0;
   } else {
     const int per = 4 * (128 / p->g);                 // tokens of a block: two Q tiles of two CTAs
     p->block_rows = per * p->g;

@@ -66,6 +66,7 @@ struct KvParams {
   // row R is token R / g, head hk * g + R % g.  Block blk owns rows blk * block_rows and up.
   int block_rows;
   int nblk, nsplit;
+  int cluster;                // rows kernel: the splits are the CTAs of a cluster, which join them themselves
   int box_rows;               // tile kernel: keys of a partial copy box (8 to 64); 0: tiles end with their page
   int split_keys;             // keys (rows kernel) or key tiles (tile kernel) per split
   float* part_o;              // [unit][split][block_rows][d], unit = (s * Hkv + hk) * nblk + blk
