@@ -218,6 +218,31 @@ def test_rows_before_the_first_key_see_nothing(n, block):
     _check_paged(c, q, out, lse, [n], [length], block, dt)
 
 
+def test_a_busy_sequence_among_many_idle_ones():
+    # most units of work have no rows or no keys: a multiprocessor meets long runs of them between two with work
+    S, dt = 700, torch.bfloat16
+    news = [0] * S
+    for s in (0, 1, 333, 334, 699):
+        news[s] = 300
+    lens = [n + 50 if n else (16 if s % 3 else 0) for s, n in enumerate(news)]
+    lens[334] = 300
+    dt, c, q, out, lse = _paged_case("bf16", 128, 4, 2, 16, news, lens, 1)
+    vdx.paged_attn(q, vdx.PagedKV(c.k, c.v, c.table), cu_of(news), c.kv_len, max_q=300, max_kv=350, causal_block=1, out=out, lse=lse)
+    vdx.sync_check()
+    _check_paged(c, q, out, lse, news, lens, 1, dt)
+
+
+def test_cross_attention_with_whole_batch_entries_without_keys():
+    q = _rand((6, 9000, 4, 128), torch.bfloat16, 90, 1.5)
+    k, v = (_rand((6, 200, 4, 128), torch.bfloat16, s) for s in (91, 92))
+    lens = [200, 0, 0, 0, 0, 70]
+    out, lse = vdx.cross_attn(q, k, v, kv_len=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    vdx.sync_check()
+    for b, n in enumerate(lens):
+        ref = attend(q[b], k[b, :n], v[b, :n], torch.full((9000,), n, device="cuda"))
+        check_attention(out[b], lse[b], ref, torch.bfloat16, f"entry {b}")
+
+
 @pytest.mark.parametrize("n", [2, 200])
 def test_rows_with_no_keys_at_all(n):
     dt, c, q, out, lse = _paged_case("fp16", 64, 4, 4, 16, [n, n], [0, 30 if n < 30 else n], 0, width=20)

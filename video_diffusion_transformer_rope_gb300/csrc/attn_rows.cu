@@ -11,7 +11,7 @@
 // with zeros, so what the cache holds there is never used), and keeps its own running maximum,
 // sum and accumulator.  The warps of a CTA join through shared memory at the end.  Splits of the keys,
 // up to 8 of them, are the CTAs of a cluster and join through one another's shared memory (no second
-// launch, no scratch: 16 to 9 us for 4 sequences of up to 1000 keys); more, for a few heads over a
+// launch, no scratch: 15.6 to 9.9 us for 4 sequences of up to 1000 keys); more, for a few heads over a
 // long cache, join through the workspace and the kernel below.
 //
 // The running maximum moves only when a score exceeds it by more than 8 (log2 units): until then

@@ -534,7 +534,13 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       Unit u;
       for (int it = cluster; ok && it < units; it += clusters) {
         if (!(ok = units_in.next(sCtl, &u))) break;
-        if (u.t0 >= u.t1) continue;
+        if (u.t0 >= u.t1) {
+          // The pending product must not wait for a unit with tiles: until it is issued the softmax and
+          // store warps do not get to the units after theirs, and with every slot of the ring taken by
+          // such units none would follow.
+          if (have) finish_second();
+          continue;
+        }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
         const uint32_t q_full = sCtl + kBarQFull + 8 * (2 * (n & 1));
         const bool two = u.ntok > 2 * per_tile;
