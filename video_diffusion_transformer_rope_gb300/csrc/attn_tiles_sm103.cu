@@ -167,21 +167,28 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 // a multiple of box_rows >= 8 keys (whole swizzle atoms): a tile inside one page is one box of 128
 // rows, another is 128 / box_rows boxes, a lane looking up the page of each.  Other page sizes
 // (p.box_rows = 0): a tile ends with its page.
+// Dense keys (kPaged = false) are one page.
+template <bool kPaged>
 struct TileGeom {
   int tiles_per_page;      // of the second kind
   __device__ __forceinline__ explicit TileGeom(const KvParams& p) { tiles_per_page = (p.P + kBN - 1) / kBN; }
   __device__ __forceinline__ int tiles(const KvParams& p, int len) const {
     if (len <= 0) return 0;
-    if (p.box_rows) return (len + kBN - 1) / kBN;
+    if (!kPaged || p.box_rows) return (len + kBN - 1) / kBN;
     const int full = len / p.P;
     return full * tiles_per_page + (len - full * p.P + kBN - 1) / kBN;
   }
 };
+template <bool kPaged>
 struct TileCursor {
   int page, off;           // entry of the page table and token in the page of the first key
   int key0, keys;          // first key, keys the tile can hold
-  __device__ __forceinline__ void seek(const KvParams& p, const TileGeom& g, int t) {
-    if (p.box_rows) {
+  __device__ __forceinline__ void seek(const KvParams& p, const TileGeom<kPaged>& g, int t) {
+    if (!kPaged) {
+      page = 0;
+      off = key0 = t * kBN;
+      keys = min(kBN, p.P - off);
+    } else if (p.box_rows) {
       key0 = t * kBN;
       page = key0 / p.P;
       off = key0 - page * p.P;
@@ -196,7 +203,9 @@ struct TileCursor {
   __device__ __forceinline__ void next(const KvParams& p) {
     key0 += keys;
     off += keys;
-    if (p.box_rows) {
+    if (!kPaged) {
+      keys = min(kBN, p.P - off);
+    } else if (p.box_rows) {
       while (off >= p.P) {
         off -= p.P;
         ++page;
@@ -211,7 +220,8 @@ struct TileCursor {
   }
 };
 
-__device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom& g, int it, bool report) {
+template <bool kPaged>
+__device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom<kPaged>& g, int it, bool report) {
   Unit u;
   const int blk = it % p.nblk;
   int r = it / p.nblk;
@@ -234,7 +244,7 @@ __device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom& g, 
   u.t1 = static_cast<int>(min(a + p.split_keys, static_cast<long long>(nt)));
   u.tail = kBN;
   if (u.t0 < u.t1 && u.t1 == nt) {
-    TileCursor c;
+    TileCursor<kPaged> c;
     c.seek(p, g, nt - 1);
     if (c.key0 + c.keys > u.len) u.tail = u.len - c.key0;
   }
@@ -359,7 +369,9 @@ __device__ __noinline__ void zero_v_rows(uint32_t v_smem, int from, int lane) {
   __syncwarp();
 }
 
-template <typename T, int D>
+// One instance per kind of keys and of results, so that none carries the others' code: in this
+// kernel, whose roles' code does not fit the instruction caches, that is time.
+template <typename T, int D, bool kPaged, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kbox,
@@ -415,7 +427,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
   const uint32_t sCtl = smem_addr(ctl);
-  const TileGeom geom(p);
+  const TileGeom<kPaged> geom(p);
   const int per_tile = kBM / p.g;     // tokens of one Q tile
   auto wait = [&](uint32_t bar, int parity, int site) {      // the whole warp, which gives up as one
     return warp_wait(bar, parity & 1, sCtl + kOffAbort, site);
@@ -436,8 +448,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       for (int it = cluster; ok && it < units; it += clusters) {
         if (!(ok = units_in.next(sCtl, &u))) break;
         if (u.t0 >= u.t1) continue;
-        const int* table = p.table ? p.table + static_cast<long long>(u.s) * p.table_stride : nullptr;
-        TileCursor c;
+        const int* table = kPaged ? p.table + static_cast<long long>(u.s) * p.table_stride : nullptr;
+        TileCursor<kPaged> c;
         c.seek(p, geom, u.t0);
         for (int t = u.t0; ok && t < u.t1; ++t, c.next(p)) {
           const int st = kv % kS;
@@ -448,14 +460,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           for (int which = 0; which < 2; ++which) {
             const int first = which == 0 ? static_cast<int>(rank) * (kBN / 2) : 0;
             const int rows = which == 0 ? kBN / 2 : kBN;
-            const bool whole = !table || !p.box_rows || c.off + kBN <= p.P;
+            const bool whole = !kPaged || !p.box_rows || c.off + kBN <= p.P;
             int boxes = 1, page = u.s, tok = c.off + first;
             if (!whole) {
               const int seen = min(rows, max(0, u.len - c.key0 - first));
               boxes = (seen + p.box_rows - 1) / p.box_rows;
               tok += lane * p.box_rows;
             }
-            if (table && lane < boxes) {
+            if (kPaged && lane < boxes) {
               int e = c.page;
               if (!whole)
                 while (tok >= p.P) {
@@ -467,7 +479,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 atomicOr(&g_error_word, kErrPage);
                 page = -1;                              // out of the map's range: filled with zeros
               }
-            } else if (!table && (which == 0 ? p.k_p : p.v_p) == 0) {
+            } else if (!kPaged && (which == 0 ? p.k_p : p.v_p) == 0) {
               page = 0;                                 // one set of keys for the whole batch
             }
             const uint32_t bytes = whole ? Lo::kStageBytes
@@ -646,7 +658,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       for (int it = cluster; ok && it < units; it += clusters, ++k) {
         const int slot = k % kUnitSlots;
         if (k >= kUnitSlots && !(ok = wait(sCtl + kBarUnitEmpty + 8 * slot, k / kUnitSlots - 1, kSiteUnitEmpty))) break;
-        const Unit u = make_unit(p, geom, it, leader && lane == 0);
+        const Unit u = make_unit<kPaged>(p, geom, it, leader && lane == 0);
         if (lane == 0) {
           ctl->unit[slot] = u;
           mbar_arrive(sCtl + kBarUnitFull + 8 * slot);
@@ -662,7 +674,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 #pragma unroll
             for (int h = 0; h < Lo::kParts; ++h)
               tma_load_4d(sQ + b * Lo::kQBytes + h * Lo::kQPart, &tm_q, bar, h * 64, u.hk * p.g,
-                          u.row0 + u.tok0 + (2 * i + static_cast<int>(rank)) * per_tile, p.cu || p.q_b == 0 ? 0 : u.s);
+                          u.row0 + u.tok0 + (2 * i + static_cast<int>(rank)) * per_tile, kPaged || p.q_b == 0 ? 0 : u.s);
           }
           __syncwarp();
         }
@@ -674,7 +686,6 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ output tiles
-      const bool split = p.nsplit > 1;
       bool ok = true;
       int n = 0, n1 = 0;
       UnitReader units_in;
@@ -691,13 +702,13 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             ok = wait(sCtl + kBarStaged + 8 * i, i == 0 ? n : n1, kSiteStaged);
             if (!ok) break;
             const uint32_t src = sQ + b * Lo::kQBytes;
-            if (split || live <= 0) {
+            if (kSplit || live <= 0) {
               // partial results leave from the registers; a tile without rows has none
-            } else if (!p.cu || live == per_tile) {
+            } else if (!kPaged || live == per_tile) {
               if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < Lo::kParts; ++h)
-                  tma_store_4d(&tm_out, src + h * Lo::kQPart, h * 64, u.hk * p.g, u.row0 + u.tok0 + tok, p.cu ? 0 : u.s);
+                  tma_store_4d(&tm_out, src + h * Lo::kQPart, h * 64, u.hk * p.g, u.row0 + u.tok0 + tok, kPaged ? 0 : u.s);
                 bulk_commit_group();
                 bulk_wait_group_read0();
               }
@@ -769,10 +780,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         continue;
       }
       const bool live = in_tile && tok < u.ntok;
-      const int limit = live ? visible_limit(p, SeqInfo{u.row0, u.n, u.keys}, u.tok0 + tok) : 0;
+      const int limit = !live ? 0 : (kPaged ? visible_limit(p, SeqInfo{u.row0, u.n, u.keys}, u.tok0 + tok) : u.len);
       const bool any_live = __any_sync(0xffffffffu, live);
       // tiles below this one are whole for every live row of the warp
-      const int whole_to = p.table && !p.box_rows ? 0 : __reduce_min_sync(0xffffffffu, live ? limit : 0x7fffffff) / kBN;
+      const int whole_to = kPaged && !p.box_rows ? 0 : __reduce_min_sync(0xffffffffu, live ? limit : 0x7fffffff) / kBN;
       float m = -INFINITY, l = 0.f;
       bool fresh = true;                       // no tile of this unit has been weighed yet
       bool scaled = false;                     // O holds earlier tiles' sums (not before the second one)
@@ -783,7 +794,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         int valid = kBN;
         bool seen = any_live;
         if (t >= whole_to) {
-          TileCursor cur;
+          TileCursor<kPaged> cur;
           cur.seek(p, geom, t);
           valid = min(limit - cur.key0, cur.keys);
           seen = __any_sync(0xffffffffu, live && valid > 0);
@@ -845,17 +856,16 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         arrive(kBarPReady + 8 * qi);
       }
       if (!ok) break;
-      const bool split = p.nsplit > 1;
       const bool empty = !(m > -INFINITY) && !(l != l);  // saw no key (a NaN sum is an answer)
       const int h = u.hk * p.g + my_head;
       const long long prow = (static_cast<long long>(u.unit) * p.nsplit + u.z) * p.block_rows + tok * p.g + my_head;
       if (live) {
         const SeqInfo sq{u.row0, u.n, u.keys};
-        if (split)
+        if (kSplit)
           p.part_ml[prow] = make_float2(empty ? -INFINITY : m, l);
         else if (p.lse)
           p.lse[lse_index(p, u.s, sq, h, u.tok0 + tok)] = empty ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
-        if (!scaled && !split) {
+        if (!scaled && !kSplit) {
           // the block sees no key at all (a split without keys is not read)
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (out_row(p, u.s, sq, u.tok0 + tok) * p.Hq + h) * D);
 #pragma unroll
@@ -879,7 +889,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
           }
-          if (split) {
+          if (kSplit) {
             if (live && !empty) {                          // the join does not read an empty row
 #pragma unroll
               for (int e = 0; e < 32; e += 8) store32(dst + ch * 32 + e, r + e, al);
@@ -953,7 +963,9 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
     return cudaErrorInvalidValue;
   }
   const int smem = Layout<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(attn_tiles<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* kernel = p.table ? (p.nsplit > 1 ? attn_tiles<T, D, true, true> : attn_tiles<T, D, true, false>)
+                         : (p.nsplit > 1 ? attn_tiles<T, D, false, true> : attn_tiles<T, D, false, false>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (units > 0x7fffffffLL - sms) return cudaErrorInvalidConfiguration;
@@ -970,7 +982,7 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tiles<T, D>, mq, mk, mv, mkb, mvb, mo, p, static_cast<int>(units));
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mkb, mvb, mo, p, static_cast<int>(units));
 }
 
 }  // namespace
