@@ -251,25 +251,25 @@ __device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom<kPag
   return u;
 }
 
-// A role's walk along the ring of units: next() waits for the following one and copies it; the
-// slot is free again when every role's warps have done so.
+// A role's walk along the ring of units: wait() for the following one, read the fields it needs (broadcast
+// from one lane, so that what follows from them, such as loop counts, stages and MMA descriptors, is
+// warp-uniform to the compiler too), and release() its slot, which is free when every role has.
 struct UnitReader {
+  uint32_t ctl;
   int k = 0;
-  __device__ __forceinline__ bool next(uint32_t ctl, Unit* u) {
-    const int slot = k % kUnitSlots;
-    if (!warp_wait(ctl + kBarUnitFull + 8 * slot, (k / kUnitSlots) & 1, ctl + kOffAbort, kSiteUnitFull)) return false;
-    // broadcast from one lane, so that what follows from it (loop counts, stages, descriptors) is
-    // warp-uniform to the compiler too: MMA descriptors live in uniform registers, and per-lane
-    // ones cost a move each (82 instead of 64 cycles an MMA)
-    const uint32_t src = ctl + kOffUnit + slot * static_cast<uint32_t>(sizeof(Unit));
-    int* dst = reinterpret_cast<int*>(u);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Unit) / 4); ++i) dst[i] = __shfl_sync(0xffffffffu, ld_shared_flag(src + 4 * i), 0);
-    if ((threadIdx.x & 31) == 0) mbar_arrive(ctl + kBarUnitEmpty + 8 * slot);
+  __device__ __forceinline__ bool wait() const {
+    return warp_wait(ctl + kBarUnitFull + 8 * (k % kUnitSlots), (k / kUnitSlots) & 1, ctl + kOffAbort, kSiteUnitFull);
+  }
+  __device__ __forceinline__ int get(uint32_t offset) const {
+    return __shfl_sync(0xffffffffu, ld_shared_flag(ctl + kOffUnit + (k % kUnitSlots) * static_cast<uint32_t>(sizeof(Unit)) + offset), 0);
+  }
+  __device__ __forceinline__ void release() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(ctl + kBarUnitEmpty + 8 * (k % kUnitSlots));
     ++k;
-    return true;
   }
 };
+#define VDX_UNIT(reader, field) (reader).get(offsetof(Unit, field))
 constexpr int kUnitReaders = 8 + 3;     // softmax warps, producer, MMA / relay, store
 
 // S = Q K^T over the pair (M = 256, N = 128): A = each CTA's Q tile, B = 64 keys from each CTA.
@@ -443,15 +443,17 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       }
       int kv = 0;                                       // key tiles so far
       bool ok = true;
-      UnitReader units_in;
-      Unit u;
+      UnitReader in{sCtl};
       for (int it = cluster; ok && it < units; it += clusters) {
-        if (!(ok = units_in.next(sCtl, &u))) break;
-        if (u.t0 >= u.t1) continue;
-        const int* table = kPaged ? p.table + static_cast<long long>(u.s) * p.table_stride : nullptr;
+        if (!(ok = in.wait())) break;
+        const int t0 = VDX_UNIT(in, t0), t1 = VDX_UNIT(in, t1), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk);
+        const int len = kPaged ? VDX_UNIT(in, len) : 0;
+        in.release();
+        if (t0 >= t1) continue;
+        const int* table = kPaged ? p.table + static_cast<long long>(s) * p.table_stride : nullptr;
         TileCursor<kPaged> c;
-        c.seek(p, geom, u.t0);
-        for (int t = u.t0; ok && t < u.t1; ++t, c.next(p)) {
+        c.seek(p, geom, t0);
+        for (int t = t0; ok && t < t1; ++t, c.next(p)) {
           const int st = kv % kS;
           // K: this CTA's 64 keys; V: all 128 of its channels.  Each is one box where it lies inside one
           // page (always, for dense keys and for tiles that end with their page), else the boxes
@@ -461,9 +463,9 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             const int first = which == 0 ? static_cast<int>(rank) * (kBN / 2) : 0;
             const int rows = which == 0 ? kBN / 2 : kBN;
             const bool whole = !kPaged || !p.box_rows || c.off + kBN <= p.P;
-            int boxes = 1, page = u.s, tok = c.off + first;
+            int boxes = 1, page = s, tok = c.off + first;
             if (!whole) {
-              const int seen = min(rows, max(0, u.len - c.key0 - first));
+              const int seen = min(rows, max(0, len - c.key0 - first));
               boxes = (seen + p.box_rows - 1) / p.box_rows;
               tok += lane * p.box_rows;
             }
@@ -495,10 +497,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 #pragma unroll
                 for (int h = 0; h < Lo::kParts; ++h)
                   tma_load_4d(sK + st * Lo::kStageBytes + h * Lo::kKPart + row * 128, whole ? &tm_k : &tm_kbox, bar, h * 64,
-                              tok, u.hk, page);
+                              tok, hk, page);
               } else {
                 tma_load_4d(sV + st * Lo::kStageBytes + row * Lo::kVRow, whole ? &tm_v : &tm_vbox, bar,
-                            static_cast<int>(rank) * (D / 2), tok, u.hk, page);
+                            static_cast<int>(rank) * (D / 2), tok, hk, page);
               }
             }
             __syncwarp();
@@ -509,10 +511,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // every copy lands before the CTA can retire (rank 0's barriers also need rank 1's relay, which
       // an abort may have stopped: its own copies are waited for by the bounded drain)
       if (lane == 0) {
-        for (int s = 0; s < kS; ++s) {
-          if (kv > s) {
-            drain_wait(sCtl + kBarKFull + 8 * s, ((kv - 1 - s) / kS) & 1);
-            drain_wait(sCtl + kBarVFull + 8 * s, ((kv - 1 - s) / kS) & 1);
+        for (int st = 0; st < kS; ++st) {
+          if (kv > st) {
+            drain_wait(sCtl + kBarKFull + 8 * st, ((kv - 1 - st) / kS) & 1);
+            drain_wait(sCtl + kBarVFull + 8 * st, ((kv - 1 - st) / kS) & 1);
           }
         }
       }
@@ -542,11 +544,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         if (last) mma_commit_pair_warp(sCtl + kBarOFull + 8);
         have = false;
       };
-      UnitReader units_in;
-      Unit u;
+      UnitReader in{sCtl};
       for (int it = cluster; ok && it < units; it += clusters) {
-        if (!(ok = units_in.next(sCtl, &u))) break;
-        if (u.t0 >= u.t1) {
+        if (!(ok = in.wait())) break;
+        int left = VDX_UNIT(in, t1) - VDX_UNIT(in, t0);
+        const int tail = VDX_UNIT(in, tail);
+        const bool two = VDX_UNIT(in, ntok) > 2 * per_tile;
+        in.release();
+        if (left <= 0) {
           // The pending product must not wait for a unit with tiles: until it is issued the softmax and
           // store warps do not get to the units after theirs, and with every slot of the ring taken by
           // such units none would follow.
@@ -555,9 +560,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
         const uint32_t q_full = sCtl + kBarQFull + 8 * (2 * (n & 1));
-        const bool two = u.ntok > 2 * per_tile;
         if (!(ok = wait(q_full, qph, kSiteQFull) && wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
-        int left = u.t1 - u.t0;
         bool fresh = true;
         while (true) {
           const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
@@ -580,7 +583,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             mma_commit_pair_warp(sCtl + kBarKEmpty + 8 * st);
           }
           ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
-          if (end && u.tail < kBN) zero_v_rows<D>(vt, u.tail, lane);
+          if (end && tail < kBN) zero_v_rows<D>(vt, tail, lane);
           // the next tile's keys are waited for here, so that its product follows this one's without a
           // wait in between
           const int st_was = st;
@@ -618,22 +621,24 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // that this CTA's Q tiles and halves of K and V have landed
       int st = 0, ph = 0, n = 0;
       bool ok = true;
-      UnitReader units_in;
-      Unit u;
+      UnitReader in{sCtl};
       for (int it = cluster; ok && it < units; it += clusters) {
-        if (!(ok = units_in.next(sCtl, &u))) break;
-        if (u.t0 >= u.t1) continue;
+        if (!(ok = in.wait())) break;
+        int left = VDX_UNIT(in, t1) - VDX_UNIT(in, t0);
+        const int tail = VDX_UNIT(in, tail);
+        in.release();
+        if (left <= 0) continue;
         for (int i = 0; ok && i < 2; ++i) {
           const int b = 2 * (n & 1) + i;
           ok = wait(sCtl + kBarQFull + 8 * b, n >> 1, kSiteRelay);
           if (ok && lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarQFull + 8 * b, 0));
         }
-        for (int t = u.t0; ok && t < u.t1; ++t) {
+        for (; ok && left > 0; --left) {
           if (!(ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteRelay))) break;
           if (lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarKFull + 8 * st, 0));
           if (!(ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteRelay))) break;
-          if (t == u.t1 - 1 && u.tail < kBN) {
-            zero_v_rows<D>(sV + st * Lo::kStageBytes, u.tail, lane);
+          if (left == 1 && tail < kBN) {
+            zero_v_rows<D>(sV + st * Lo::kStageBytes, tail, lane);
             if (lane == 0) mbar_arrive_remote_cluster(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
           } else if (lane == 0) {
             mbar_arrive_remote(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
@@ -688,16 +693,19 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // ------------------------------------------------------------------ output tiles
       bool ok = true;
       int n = 0, n1 = 0;
-      UnitReader units_in;
-      Unit u;
+      UnitReader in{sCtl};
       for (int it = cluster; ok && it < units; it += clusters) {
-        if (!(ok = units_in.next(sCtl, &u))) break;
-        if (u.t0 >= u.t1) continue;
-        const bool two = u.ntok > 2 * per_tile;
+        if (!(ok = in.wait())) break;
+        const bool tiles = VDX_UNIT(in, t0) < VDX_UNIT(in, t1);
+        const int ntok = VDX_UNIT(in, ntok), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk);
+        const int tok0 = VDX_UNIT(in, tok0) + (kPaged ? VDX_UNIT(in, row0) : 0);
+        in.release();
+        if (!tiles) continue;
+        const bool two = ntok > 2 * per_tile;
         for (int i = 0; ok && i < 2; ++i) {
           const int b = 2 * (n & 1) + i;
           const int tok = (2 * i + static_cast<int>(rank)) * per_tile;      // within the block
-          const int live = min(per_tile, u.ntok - tok);
+          const int live = min(per_tile, ntok - tok);
           if (i == 0 || two) {
             ok = wait(sCtl + kBarStaged + 8 * i, i == 0 ? n : n1, kSiteStaged);
             if (!ok) break;
@@ -708,7 +716,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
               if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < Lo::kParts; ++h)
-                  tma_store_4d(&tm_out, src + h * Lo::kQPart, h * 64, u.hk * p.g, u.row0 + u.tok0 + tok, kPaged ? 0 : u.s);
+                  tma_store_4d(&tm_out, src + h * Lo::kQPart, h * 64, hk * p.g, tok0 + tok, kPaged ? 0 : s);
                 bulk_commit_group();
                 bulk_wait_group_read0();
               }
@@ -720,7 +728,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 const uint4 x = ld_shared_v4(src + (ch >> 3) * Lo::kQPart + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
                 const int tk = row / p.g, hd = row - tk * p.g;
                 T* dst = static_cast<T*>(p.out) +
-                         ((static_cast<long long>(u.row0) + u.tok0 + tok + tk) * p.Hq + u.hk * p.g + hd) * D + ch * 8;
+                         ((static_cast<long long>(tok0) + tok + tk) * p.Hq + hk * p.g + hd) * D + ch * 8;
                 *reinterpret_cast<uint4*>(dst) = x;
               }
             }
@@ -783,7 +791,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const int limit = !live ? 0 : (kPaged ? visible_limit(p, SeqInfo{u.row0, u.n, u.keys}, u.tok0 + tok) : u.len);
       const bool any_live = __any_sync(0xffffffffu, live);
       // tiles below this one are whole for every live row of the warp
-      const int whole_to = kPaged && !p.box_rows ? 0 : __reduce_min_sync(0xffffffffu, live ? limit : 0x7fffffff) / kBN;
+      const int whole_to = !kPaged ? u.len / kBN
+                           : !p.box_rows ? 0 : __reduce_min_sync(0xffffffffu, live ? limit : 0x7fffffff) / kBN;
       float m = -INFINITY, l = 0.f;
       bool fresh = true;                       // no tile of this unit has been weighed yet
       bool scaled = false;                     // O holds earlier tiles' sums (not before the second one)
