@@ -453,54 +453,63 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         const int* table = kPaged ? p.table + static_cast<long long>(s) * p.table_stride : nullptr;
         TileCursor<kPaged> c;
         c.seek(p, geom, t0);
-        for (int t = t0; ok && t < t1; ++t, c.next(p)) {
+        // K: this CTA's 64 keys; V: all 128 of its channels.  A tile is one box of each where it lies inside
+        // one page (always, for dense keys and for tiles that end with their page), else box_rows-key
+        // boxes, one to a lane, of the keys that some row sees.
+        const int box = kPaged ? p.box_rows : 0;
+        bool whole;
+        int seen, page, tok;                            // of the tile: keys in boxes; of this lane's box
+        auto look_up = [&](const TileCursor<kPaged>& c) {
+          whole = !kPaged || !box || c.off + kBN <= p.P;
+          seen = whole ? kBN : min(kBN, len - c.key0);
+          page = !kPaged ? s : 0;
+          tok = c.off + lane * box;
+          if (kPaged && (lane == 0 || (!whole && lane * box < seen))) {
+            int e = c.page;
+            if (!whole)
+              while (tok >= p.P) {
+                tok -= p.P;
+                ++e;
+              }
+            page = __ldg(table + e);
+          }
+        };
+        look_up(c);
+        for (int t = t0; ok && t < t1; ++t) {
+          const bool one = whole;
+          const int keys = seen, tok0 = kPaged ? tok : c.key0;
+          int pg = page;
+          if (kPaged && static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
+            atomicOr(&g_error_word, kErrPage);
+            pg = -1;                                    // out of the map's range: filled with zeros
+          }
+          c.next(p);
+          if (kPaged && t + 1 < t1) look_up(c);         // the next tile's pages, while this one waits for its stages
           const int st = kv % kS;
-          // K: this CTA's 64 keys; V: all 128 of its channels.  Each is one box where it lies inside one
-          // page (always, for dense keys and for tiles that end with their page), else the boxes
-          // of keys that some row sees, one to a lane.
+          const int k_box0 = one ? 0 : static_cast<int>(rank) * (kBN / 2 / max(box, 1));   // first box of this CTA's keys
+          const int k_rows = one ? kBN / 2 : max(0, min(kBN / 2, keys - static_cast<int>(rank) * (kBN / 2)));
 #pragma unroll 1
           for (int which = 0; which < 2; ++which) {
-            const int first = which == 0 ? static_cast<int>(rank) * (kBN / 2) : 0;
-            const int rows = which == 0 ? kBN / 2 : kBN;
-            const bool whole = !kPaged || !p.box_rows || c.off + kBN <= p.P;
-            int boxes = 1, page = s, tok = c.off + first;
-            if (!whole) {
-              const int seen = min(rows, max(0, len - c.key0 - first));
-              boxes = (seen + p.box_rows - 1) / p.box_rows;
-              tok += lane * p.box_rows;
-            }
-            if (kPaged && lane < boxes) {
-              int e = c.page;
-              if (!whole)
-                while (tok >= p.P) {
-                  tok -= p.P;
-                  ++e;
-                }
-              page = __ldg(table + e);
-              if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-                atomicOr(&g_error_word, kErrPage);
-                page = -1;                              // out of the map's range: filled with zeros
-              }
-            } else if (!kPaged && (which == 0 ? p.k_p : p.v_p) == 0) {
-              page = 0;                                 // one set of keys for the whole batch
-            }
-            const uint32_t bytes = whole ? Lo::kStageBytes
-                                         : static_cast<uint32_t>(boxes * p.box_rows) * (which == 0 ? D * 2 : D);
-            const uint32_t empty = which == 0 ? sCtl + kBarKEmpty + 8 * st : sCtl + kBarVEmpty + 8 * st;
+            // boxes [b0, b0 + n) of the tile, in rows of this stage from 0
+            const int b0 = which == 0 ? k_box0 : 0;
+            const int n = one ? 1 : ((which == 0 ? k_rows : keys) + box - 1) / box;
+            const uint32_t bytes = one ? Lo::kStageBytes : static_cast<uint32_t>(n * box) * (which == 0 ? D * 2 : D);
+            const uint32_t empty = (which == 0 ? sCtl + kBarKEmpty : sCtl + kBarVEmpty) + 8 * st;
             if (kv >= kS && !(ok = wait(empty, kv / kS - 1, which == 0 ? kSiteKEmpty : kSiteVEmpty))) break;
-            const uint32_t bar = (which == 0 ? sCtl + kBarKFull + 8 * st : sCtl + kBarVFull + 8 * st);
+            const uint32_t bar = (which == 0 ? sCtl + kBarKFull : sCtl + kBarVFull) + 8 * st;
             if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
-            if (lane < boxes) {
-              const uint32_t row = whole ? 0u : static_cast<uint32_t>(lane * p.box_rows);
+            if (lane >= b0 && lane < b0 + n) {
+              const uint32_t row = one ? 0u : static_cast<uint32_t>((lane - b0) * box);
               if (which == 0) {
+                const int kp = !kPaged && p.k_p == 0 ? 0 : pg;       // one set of keys for the whole batch
 #pragma unroll
                 for (int h = 0; h < Lo::kParts; ++h)
-                  tma_load_4d(sK + st * Lo::kStageBytes + h * Lo::kKPart + row * 128, whole ? &tm_k : &tm_kbox, bar, h * 64,
-                              tok, hk, page);
+                  tma_load_4d(sK + st * Lo::kStageBytes + h * Lo::kKPart + row * 128, one ? &tm_k : &tm_kbox, bar, h * 64,
+                              tok0 + (one ? static_cast<int>(rank) * (kBN / 2) : 0), hk, kp);
               } else {
-                tma_load_4d(sV + st * Lo::kStageBytes + row * Lo::kVRow, whole ? &tm_v : &tm_vbox, bar,
-                            static_cast<int>(rank) * (D / 2), tok, hk, page);
+                tma_load_4d(sV + st * Lo::kStageBytes + row * Lo::kVRow, one ? &tm_v : &tm_vbox, bar,
+                            static_cast<int>(rank) * (D / 2), tok0, hk, !kPaged && p.v_p == 0 ? 0 : pg);
               }
             }
             __syncwarp();
