@@ -156,6 +156,9 @@ PAGED = [
     ("fp16", 64, 12, 1, 32, [1, 1, 0], [777, 33, 0], 0),
     ("fp16", 128, 4, 4, 200, [1, 1], [199, 4001], 1),
     ("bf16", 64, 33, 1, 16, [1, 2], [100, 50], 1),
+    # few heads over long caches: many splits, joined through the workspace
+    ("bf16", 128, 4, 1, 64, [1, 2, 1], [20000, 9001, 3], 1),
+    ("fp16", 64, 2, 2, 200, [3, 0, 1], [30011, 5, 0], 0),
     # short chunks
     ("bf16", 128, 6, 2, 128, [5, 3, 8], [5, 300, 1029], 1),
     ("fp16", 64, 8, 8, 16, [16, 7], [16, 100], 3),

@@ -383,46 +383,105 @@ attn_rows(const __grid_constant__ KvParams p) {
   cluster_sync_all();                   // no CTA leaves while another reads its part
 }
 
-// Join the key splits of every row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.  One warp
-// per row; it reads each split's row once, D * 4 bytes coalesced.  Bound by those reads (L2).
-template <typename T, int D>
+// Join the key splits of every row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.  kPer warps per
+// row (8 where there are few rows with many splits, 1 where there are many rows), each taking every
+// kPer-th split: first the maxima, a split to a lane, then the rows of O, whose loads do not depend on one
+// another (read one after another, 195 splits of one row took 60 us).  Bound by reading O (L2).
+template <typename T, int D, int kPer>
 __global__ void __launch_bounds__(256)
 attn_join(const __grid_constant__ KvParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long idx = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  constexpr int kVals = D / 32;
+  __shared__ float s_m[8], s_l[8], s_o[8][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
+  const long long idx = static_cast<long long>(blockIdx.x) * (8 / kPer) + warp / kPer;
   const long long unit = idx / p.block_rows;
   const int r = static_cast<int>(idx - unit * p.block_rows);
-  if (unit >= static_cast<long long>(p.S) * p.Hkv * p.nblk) return;
-  const int blk = static_cast<int>(unit % p.nblk);
-  const int hk = static_cast<int>(unit / p.nblk % p.Hkv);
-  const int s = static_cast<int>(unit / p.nblk / p.Hkv);
-  const SeqInfo sq = sequence_info(p, s, false);
-  const long long R = static_cast<long long>(blk) * p.block_rows + r;
-  if (R >= static_cast<long long>(min(sq.n, p.max_q)) * p.g) return;
-  const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
-
-  float mx = -INFINITY, lt = 0.f;
-  constexpr int kPer = D / 32;
-  float acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int z = 0; z < p.nsplit; ++z) mx = fmaxf(mx, p.part_ml[(unit * p.nsplit + z) * p.block_rows + r].x);
-  for (int z = 0; z < p.nsplit; ++z) {
-    const long long at = (unit * p.nsplit + z) * p.block_rows + r;
-    const float2 ml = p.part_ml[at];
-    if (ml.x == -INFINITY) continue;           // a split without keys for this row
-    const float w = ex2_approx(ml.x - mx);
-    lt += w * ml.y;
-    const float* src = p.part_o + at * D + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += w * src[e];
+  bool live = unit < static_cast<long long>(p.S) * p.Hkv * p.nblk;
+  int hk = 0, s = 0, tok = 0, h = 0;
+  SeqInfo sq{0, 0, 0};
+  if (live) {
+    hk = static_cast<int>(unit / p.nblk % p.Hkv);
+    s = static_cast<int>(unit / p.nblk / p.Hkv);
+    sq = sequence_info(p, s, false);
+    const long long R = unit % p.nblk * p.block_rows + r;
+    live = R < static_cast<long long>(min(sq.n, p.max_q)) * p.g;
+    tok = static_cast<int>(R / p.g);
+    h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / lt;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D) + lane * (kPer / 2);
+  float m = -INFINITY, l = 0.f, acc[kVals];
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) dst[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
+  if (live) {
+    const long long base = unit * p.nsplit * p.block_rows + r;      // + z * block_rows
+    for (int z = part + kPer * lane; z < p.nsplit; z += kPer * 32)
+      m = fmaxf(m, p.part_ml[base + static_cast<long long>(z) * p.block_rows].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int z0 = part; z0 < p.nsplit; z0 += kPer * 32) {
+      // weights of up to 32 splits, a lane each; a split without keys for this row has none, and no O
+      const int z = z0 + kPer * lane;
+      float w = 0.f;
+      bool has = false;
+      if (z < p.nsplit) {
+        const float2 ml = p.part_ml[base + static_cast<long long>(z) * p.block_rows];
+        has = ml.x > -INFINITY || ml.y != ml.y;           // a NaN sum is an answer
+        w = ml.x > -INFINITY ? ex2_approx(ml.x - m) : 1.f;
+        if (has) l += w * ml.y;
+      }
+      unsigned todo = __ballot_sync(0xffffffffu, has);
+#pragma unroll 4
+      while (todo) {
+        const int i = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* src = p.part_o + (base + static_cast<long long>(z0 + kPer * i) * p.block_rows) * D + lane * kVals;
+        float v[kVals];
+        if constexpr (kVals == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[0] = x.x; v[1] = x.y;
+        }
+#pragma unroll
+        for (int e = 0; e < kVals; ++e) acc[e] += wi * v[e];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  }
+  if (kPer > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) s_o[warp][lane * kVals + e] = acc[e];
+    __syncthreads();
+    if (part != 0) return;
+    float top = m;
+#pragma unroll
+    for (int w = 1; w < kPer; ++w) top = fmaxf(top, s_m[warp + w]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+      const float f = s_m[warp + w] > -INFINITY ? ex2_approx(s_m[warp + w] - top) : 1.f;   // no keys: l and O are 0
+      l += f * s_l[warp + w];
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) acc[e] += f * s_o[warp + w][lane * kVals + e];
+    }
+    m = top;
+  }
+  if (!live) return;
+  const bool empty = !(m > -INFINITY) && !(l != l);
+  const float inv = empty ? 0.f : 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D) + lane * (kVals / 2);
+#pragma unroll
+  for (int e = 0; e < kVals / 2; ++e) dst[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   if (lane == 0 && p.lse)
-    p.lse[lse_index(p, s, sq, h, tok)] = mx == -INFINITY ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
+    p.lse[lse_index(p, s, sq, h, tok)] = empty ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
 }
 
 template <typename T, int D, int kNT>
@@ -457,7 +516,12 @@ cudaError_t launch(const KvParams& p, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t join(const KvParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.block_rows;
-  attn_join<T, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
+  const long long blocks = p.rows_kernel ? rows : (rows + 7) / 8;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (p.rows_kernel)
+    attn_join<T, D, 8><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+  else
+    attn_join<T, D, 1><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

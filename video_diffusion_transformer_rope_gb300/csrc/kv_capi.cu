@@ -271,22 +271,27 @@ size_t plan_attention(KvParams* p, int d, int sms) {
     p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
     p->nblk = 1;
     const long long units = static_cast<long long>(p->S) * p->Hkv;
-    // Two CTAs to a multiprocessor.  About four waves of splits keep ragged lengths balanced, and no
-    // split is below 256 keys (four blocks per warp), whose start would cost more than its reads.
-    const long long slots = 2ll * sms;
-    const long long want = static_cast<long long>(p->max_kv) * units / (4 * slots);
-    long long keys = std::max<long long>(256, (want + 63) / 64 * 64);
-    long long n = (p->max_kv + keys - 1) / keys;
-    // Short caches of few sequences: one wave at most.  Up to 8 splits are a cluster and join in it,
-    // also where more are wanted but 8 occupy the device; else they join through the workspace.
-    if (units * n > slots && units * n < 2 * slots) n = std::max<long long>(1, slots / units);
-    if (n > 8 && units * 8 >= slots) n = 8;
+    // Two CTAs to a multiprocessor, in one wave where the units leave room for splits: the most
+    // splits that fit with a tenth to spare (clusters do not fill every group of processors), of at
+    // least 192 keys.  16 x 8 heads over 8192 keys: 2 splits 84.7 us, 1 split 131, 4 (two waves) 93, 8
+    // 105; 4 x 12 over 1000: 5 splits 10.9, 1 split 20.7, 6 (all slots, did not fit) 17.6.  Units
+    // that fill the device by themselves are split only where they are long, to even out ragged
+    // lengths: 48 x 8 over 8-33 thousand keys: 4 splits 662 us, 1 split 856; 64 x 12 over 1000 keys: 1
+    // split 76.8, 2 splits 94.4.  Up to 8 splits are a cluster and join in it; a few heads over a long
+    // cache take more, joined through the workspace (8 heads over 16000 keys: 31 of 512 keys 19.7 us,
+    // 8 in a cluster 39.6).
+    const long long slots = 2ll * sms, room = slots * 9 / 10 / units;
+    long long n;
+    if (room < 2)
+      n = std::min<long long>(8, (p->max_kv + 8191) / 8192);
+    else if (room <= 8 || p->max_kv <= 8 * 1024)
+      n = std::min<long long>({room, 8, (p->max_kv + 191) / 192});
+    else
+      n = std::min<long long>(slots / units, p->max_kv / 512);
+    long long keys = n > 0 ? ((p->max_kv + n - 1) / n + 63) / 64 * 64 : 0;
     p->cluster = n > 1 && n <= 8;
-    if (!p->cluster && n > 1) {
-      keys = std::max<long long>(512, keys);
-      n = (p->max_kv + keys - 1) / keys;
-    }
     p->nsplit = static_cast<int>(std::max<long long>(1, n));
+    if (!p->cluster && n > 1) p->nsplit = static_cast<int>((p->max_kv + keys - 1) / keys);
     p->split_keys = static_cast<int>(p->nsplit > 1 ? keys : std::max(p->max_kv, 1));
     if (p->cluster) return 0;
   } else {
