@@ -489,7 +489,8 @@ cudaError_t launch_nt(const KvParams& p, cudaStream_t stream) {
   const int ring = kWarps * kStages * 2 * kKeys * D * 2;
   const int join = (kWarps * (D + 4 + 2) + 2) * 8 * kNT * 4;
   const int smem = ring > join ? ring : join;
-  cudaError_t e = cudaFuncSetAttribute(attn_rows<T, D, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(attn_rows<T, D, kNT>, smem, &done);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -960,9 +960,8 @@ bool encode_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, int D
 
 template <typename T, int D>
 cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_t stream, const char** what) {
-  CUtensorMap mq, mk, mv, mkb, mvb, mo;
+  CUtensorMap mq, mk, mv, mkb{}, mvb{}, mo;            // no boxes: their maps are never used
   const bool one_q = p.cu != nullptr || p.q_b == 0;
-  const int box = p.box_rows ? p.box_rows : kBN / 2;
   const bool has_keys = p.P > 0;
   // dimensions: q and out (d, head, token, batch), k and v (d, token, head, page)
   const long long kpages = !p.table && p.k_p == 0 ? 1 : p.num_pages, vpages = !p.table && p.v_p == 0 ? 1 : p.num_pages;
@@ -973,17 +972,18 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   if (!encode_rows<T>(encode, &mq, p.q, D, p.Hq, p.q_h, p.N, p.q_t, one_q ? 1 : p.S, p.q_b, 64, p.g, kBM / p.g) ||
       !encode_rows<T>(encode, &mk, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, kBN / 2, 1) ||
       !encode_rows<T>(encode, &mv, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, kBN, 1) ||
-      !encode_rows<T>(encode, &mkb, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, box, 1) ||
-      !encode_rows<T>(encode, &mvb, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, box, 1) ||
+      (p.box_rows && (!encode_rows<T>(encode, &mkb, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, p.box_rows, 1) ||
+                      !encode_rows<T>(encode, &mvb, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, p.box_rows, 1))) ||
       !encode_rows<T>(encode, &mo, p.out, D, p.Hq, D, p.N, static_cast<long long>(p.Hq) * D, p.cu ? 1 : p.S, ob, 64, p.g,
                       kBM / p.g)) {
     *what = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
   const int smem = Layout<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
+  static std::atomic<uint64_t> done[4] = {};
   auto* kernel = p.table ? (p.nsplit > 1 ? attn_tiles<T, D, true, true> : attn_tiles<T, D, true, false>)
                          : (p.nsplit > 1 ? attn_tiles<T, D, false, true> : attn_tiles<T, D, false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared(kernel, smem, &done[(p.table ? 2 : 0) + (p.nsplit > 1 ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (units > 0x7fffffffLL - sms) return cudaErrorInvalidConfiguration;

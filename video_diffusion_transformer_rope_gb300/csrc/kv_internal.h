@@ -2,6 +2,7 @@
 // (kv_capi.cu) and their kernels.  Not part of the public API.
 #pragma once
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "vdx_internal.h"
@@ -72,6 +73,20 @@ struct KvParams {
   float* part_o;              // [unit][split][block_rows][d], unit = (s * Hkv + hk) * nblk + blk
   float2* part_ml;            // [unit][split][block_rows]: running maximum (log2 units) and sum
 };
+
+// Opt a kernel in to `bytes` of dynamic shared memory, once per device (a process-wide property of the
+// function; asking again on every call costs a microsecond of host time).  `done`: the kernel's own flags.
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Fill the plan for `sms` multiprocessors; returns the workspace bytes it needs.
 size_t plan_attention(KvParams* p, int d, int sms);

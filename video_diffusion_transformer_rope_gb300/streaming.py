@@ -12,13 +12,16 @@ from ._binding import VDX_ERR_ARG, VDX_ERR_UNSUPPORTED, VdxError
 
 
 _torch = None
+_raw_stream = None
+_I32_MAX = 0x7fffffff
 
 
 def _t():
     """torch, imported on first use (the library itself loads without it)."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
         _torch = torch
     return _torch
 
@@ -34,16 +37,16 @@ def _dtype(t):
 
 def _tensor(name, t, like, dims):
     """A CUDA tensor of `dims` dimensions on like's device with like's dtype and dense channels; its
-    shape and strides."""
-    torch = _torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != like.get_device() or t.dtype != like.dtype:
+    shape and strides.  (The checks of these calls are host time of every launch: cheap ones first,
+    each attribute once.)"""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda or t.get_device() != like.get_device() or t.dtype != like.dtype:
         raise VdxError(VDX_ERR_ARG, f"{name} must be a CUDA tensor of dtype {like.dtype} on {like.device}")
     shape, stride = t.shape, t.stride()
     if len(shape) != dims:
         raise VdxError(VDX_ERR_ARG, f"{name} must have {dims} dimensions, got {tuple(shape)}")
     if stride[-1] != 1 and shape[-1] > 1:
         raise VdxError(VDX_ERR_ARG, f"{name}: the channels of a head must be contiguous")
-    if t.requires_grad and torch.is_grad_enabled():
+    if t.requires_grad and _torch.is_grad_enabled():
         raise VdxError(VDX_ERR_UNSUPPORTED, f"{name} requires a gradient: these calls are forward only "
                                             "(use torch.no_grad() or detach())")
     return shape, stride
@@ -58,44 +61,48 @@ def _cuda(name, t):
 def _int32(name, t, like, length):
     if t is None:
         return 0
-    torch = _torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.get_device() != like.get_device()
-            or tuple(t.shape) != (length,) or not t.is_contiguous()):
+    if (not isinstance(t, _torch.Tensor) or t.dtype != _torch.int32 or not t.is_cuda or t.get_device() != like.get_device()
+            or t.dim() != 1 or t.shape[0] != length or not t.is_contiguous()):
         raise VdxError(VDX_ERR_ARG, f"{name} must be a contiguous int32 CUDA tensor of {length} values on {like.device}")
     return t.data_ptr()
 
 
-def _int(name, x, least=0):
-    x = int(x)
-    if x < least or x > 0x7fffffff:
-        raise VdxError(VDX_ERR_ARG, f"{name} = {x} is outside [{least}, 2^31)")
-    return x
+def _ints(name, values, count):
+    """`count` integers that fit a C int."""
+    values = tuple(map(int, values))
+    if len(values) != count or min(values) < 0 or max(values) > _I32_MAX:
+        raise VdxError(VDX_ERR_ARG, f"{name} = {values}: {count} integers in [0, 2^31) are needed")
+    return values
 
 
 class _On:
-    """The tensors' device and the call's stream are current inside; .handle is the stream.  Where they
-    are already, which is the usual call, nothing is switched (the switch and back costs more host
-    time than the launch)."""
+    """The tensors' device and the call's stream, current inside; .handle is the stream."""
 
     def __init__(self, like, stream):
-        torch = _torch
-        dev = like.get_device()
-        if stream is None:
-            self.handle = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-            self.ctx = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-            return
         if stream.device != like.device:
             raise VdxError(VDX_ERR_ARG, f"the stream is on {stream.device}, the tensors on {like.device}")
-        self.handle = ctypes.c_void_p(stream.cuda_stream)
-        self.ctx = torch.cuda.stream(stream)            # also makes the stream's device current
+        self.handle = stream.cuda_stream
+        self.ctx = _torch.cuda.stream(stream)           # also makes the stream's device current
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self
+        self.ctx.__enter__()
+        return self.handle
 
     def __exit__(self, *a):
-        return None if self.ctx is None else self.ctx.__exit__(*a)
+        return self.ctx.__exit__(*a)
+
+
+def _run(call, like, stream, *args):
+    """call(stream handle, *args) with the tensors' device and the stream current.  Where they are
+    already, which is the usual call, nothing is switched: that costs more host time than a launch."""
+    if stream is None:
+        dev = like.get_device()
+        if _torch.cuda.current_device() == dev:
+            return call(_raw_stream(dev), *args)
+        with _torch.cuda.device(dev):
+            return call(_raw_stream(dev), *args)
+    with _On(like, stream) as handle:
+        return call(handle, *args)
 
 
 @dataclass
@@ -138,42 +145,51 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
     like = cache.k
     ks, kst = _tensor("k", k, like, 3)
     vs, vst = _tensor("v", v, like, 3)
-    rows, d = ks[0], sc.d
+    rows, d, seqs = ks[0], sc.d, sc.seqs
     if ks[1] != sc.Hkv or ks[2] != d or vs != ks:
         raise VdxError(VDX_ERR_ARG, f"k {tuple(ks)} and v {tuple(vs)} must be [rows, {sc.Hkv}, {d}], as the cache's heads")
+    qn = kn = Hq = q_ptr = 0
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
         if w is not None and _tensor(name, w, like, 1)[0][0] != d:
             raise VdxError(VDX_ERR_ARG, f"{name} must hold {d} weights")
-    T, Hg, Wg = (_int("grid", x) for x in grid)
-    st, sh, sw = (_int("sections", x) for x in sections)
-    Hq, qst, ost = 0, (0, 0), (0, 0)
+    if q_norm is not None:
+        qn = q_norm.data_ptr()
+    if k_norm is not None:
+        kn = k_norm.data_ptr()
+    qs, qst = None, (0, 0)
     if q is not None:
         qs, qst = _tensor("q", q, like, 3)
-        Hq = qs[1]
+        Hq, q_ptr = qs[1], q.data_ptr()
         if qs[0] != rows or qs[2] != d:
             raise VdxError(VDX_ERR_ARG, f"q {tuple(qs)} does not match the {rows} rows of {d} channels of k")
+        if rows == 0 or Hq == 0:                        # empty tensors have no address
+            return _torch.empty(qs, dtype=q.dtype, device=q.device) if q_out is None else q_out
     elif q_out is not None:
         raise VdxError(VDX_ERR_ARG, "q_out without q")
-    with _On(like, stream) as on:
-        if q is not None:
-            if q_out is None:
-                q_out = _torch.empty(qs, dtype=q.dtype, device=q.device)
-            os_, ost = _tensor("q_out", q_out, like, 3)
-            if os_ != qs:
-                raise VdxError(VDX_ERR_ARG, f"q_out must be shaped like q {tuple(qs)}")
-        a = B.AppendArgs(q.data_ptr() if q is not None else 0, k.data_ptr(), v.data_ptr(),
-                         q_out.data_ptr() if q is not None else 0, qst[0], qst[1], kst[0], kst[1], vst[0], vst[1],
-                         ost[0], ost[1], rows, Hq, _int32("cu", cu, like, sc.seqs + 1),
-                         _int32("kv_len", kv_len, like, sc.seqs), _int32("pos_offset", pos_offset, like, sc.seqs), T, Hg, Wg,
-                         st, sh, sw, theta, q_norm.data_ptr() if q_norm is not None else 0,
-                         k_norm.data_ptr() if k_norm is not None else 0, eps)
-        if q is not None and q.numel() == 0:            # no rows: empty tensors have no address
-            return q_out
-        B._check(B.lib().vdx_rope3d_append(ctypes.byref(sc), ctypes.byref(a), on.handle))
+    a = B.AppendArgs(q_ptr, k.data_ptr(), v.data_ptr(), 0, qst[0], qst[1], kst[0], kst[1], vst[0], vst[1], 0, 0, rows, Hq,
+                     _int32("cu", cu, like, seqs + 1), _int32("kv_len", kv_len, like, seqs),
+                     _int32("pos_offset", pos_offset, like, seqs), *_ints("grid", grid, 3), *_ints("sections", sections, 3), theta,
+                     qn, kn, eps)
+    return _run(_append, like, stream, sc, a, q, qs, q_out)
+
+
+def _append(handle, sc, a, q, qs, q_out):
+    if q is not None:
+        if q_out is None:
+            q_out = _torch.empty(qs, dtype=q.dtype, device=q.device)
+        os_, ost = _tensor("q_out", q_out, q, 3)
+        if os_ != qs:
+            raise VdxError(VDX_ERR_ARG, f"q_out must be shaped like q {tuple(qs)}")
+        a.q_out = q_out.data_ptr()
+        a.q_out_row, a.q_out_head = ost[0], ost[1]
+    status = B.lib().vdx_rope3d_append(ctypes.byref(sc), ctypes.byref(a), handle)
+    if status:
+        B._check(status)
     return q_out
 
 
-def _outputs(q, lse_shape, out, lse, return_lse):
+def _attention(handle, args, size_fn, run_fn, first, q, lse_shape, out, lse, return_lse, workspace):
+    """Outputs and scratch (the caller's, or torch's for this call on its stream), then the call."""
     torch = _torch
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -181,32 +197,31 @@ def _outputs(q, lse_shape, out, lse, return_lse):
         _tensor("out", out, q, q.dim())
         if out.shape != q.shape or not out.is_contiguous():
             raise VdxError(VDX_ERR_ARG, f"out must be contiguous and shaped like q {tuple(q.shape)}")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-    elif (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != tuple(lse_shape)
-          or not lse.is_contiguous() or lse.device != q.device):
-        raise VdxError(VDX_ERR_ARG, f"lse must be a contiguous float32 tensor of shape {tuple(lse_shape)} on {q.device}")
-    return out, lse
-
-
-def _with_workspace(args, size_fn, run_fn, first, workspace, like, on):
-    """Fill args.workspace (the caller's tensor, or one taken from torch's allocator for this call on
-    its stream) and run."""
-    torch = _torch
+    args.out = out.data_ptr()
+    if lse is not None:
+        if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != lse_shape
+                or not lse.is_contiguous() or lse.device != q.device):
+            raise VdxError(VDX_ERR_ARG, f"lse must be a contiguous float32 tensor of shape {lse_shape} on {q.device}")
+        args.lse = lse.data_ptr()
+    elif return_lse:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        args.lse = lse.data_ptr()
     ref = ctypes.byref(args)
     if workspace is not None:
-        if (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.device != like.device
+        if (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.device != q.device
                 or not workspace.is_contiguous()):
-            raise VdxError(VDX_ERR_ARG, f"workspace must be a contiguous CUDA tensor on {like.device}")
+            raise VdxError(VDX_ERR_ARG, f"workspace must be a contiguous CUDA tensor on {q.device}")
     else:
         need = size_fn(*first, ref)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     if workspace is not None:
         args.workspace = workspace.data_ptr()
         args.workspace_bytes = workspace.numel() * workspace.element_size()
-    B._check(run_fn(*first, ref, on.handle))
+    status = run_fn(*first, ref, handle)
+    if status:
+        B._check(status)
+    return out, lse
 
 
 def _paged_args(q, cache, cu, kv_len, max_q, max_kv, causal_block, scale):
@@ -216,8 +231,7 @@ def _paged_args(q, cache, cu, kv_len, max_q, max_kv, causal_block, scale):
         raise VdxError(VDX_ERR_ARG, f"q {tuple(shape)} does not match the cache's head dimension {sc.d}")
     return sc, B.PagedAttnArgs(q.data_ptr(), 0, 0, stride[0], stride[1], shape[0], shape[1],
                                _int32("cu", cu, q, sc.seqs + 1), _int32("kv_len", kv_len, q, sc.seqs),
-                               _int("max_q", max_q or 0), _int("max_kv", max_kv or 0), _int("causal_block", causal_block),
-                               scale, 0, 0)
+                               *_ints("max_q, max_kv, causal_block", (max_q or 0, max_kv or 0, causal_block), 3), scale, 0, 0)
 
 
 def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, scale=0.0, out=None, lse=None,
@@ -234,13 +248,8 @@ def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, sc
     as they were in out / lse."""
     sc, a = _paged_args(q, cache, cu, kv_len, max_q, max_kv, causal_block, scale)
     L = B.lib()
-    with _On(q, stream) as on:
-        out, lse = _outputs(q, (a.Hq, a.rows), out, lse, return_lse)
-        a.out = out.data_ptr()
-        if lse is not None:
-            a.lse = lse.data_ptr()
-        _with_workspace(a, L.vdx_paged_attn_workspace_bytes, L.vdx_paged_attn, (ctypes.byref(sc),), workspace, q, on)
-    return out, lse
+    return _run(_attention, q, stream, a, L.vdx_paged_attn_workspace_bytes, L.vdx_paged_attn, (ctypes.byref(sc),), q,
+                (a.Hq, a.rows), out, lse, return_lse, workspace)
 
 
 def paged_attn_workspace_bytes(q, cache, cu, kv_len, max_q=None, max_kv=None):
@@ -270,13 +279,8 @@ def cross_attn(q, k, v, kv_len=None, scale=0.0, out=None, lse=None, return_lse=T
     Returns (out [B, N, Hq, d], lse [B, Hq, N] float32 or None)."""
     a = _cross_args(q, k, v, kv_len, scale)
     L = B.lib()
-    with _On(q, stream) as on:
-        out, lse = _outputs(q, (a.B, a.Hq, a.N), out, lse, return_lse)
-        a.out = out.data_ptr()
-        if lse is not None:
-            a.lse = lse.data_ptr()
-        _with_workspace(a, L.vdx_cross_attn_workspace_bytes, L.vdx_cross_attn, (), workspace, q, on)
-    return out, lse
+    return _run(_attention, q, stream, a, L.vdx_cross_attn_workspace_bytes, L.vdx_cross_attn, (), q, (a.B, a.Hq, a.N), out,
+                lse, return_lse, workspace)
 
 
 def cross_attn_workspace_bytes(q, k, v, kv_len=None):
