@@ -520,6 +520,42 @@ def test_a_captured_step_replays_with_new_lengths():
             assert torch.equal(a, b)
 
 
+def test_a_captured_chunk_replays_with_new_lengths():
+    # the tile kernel and its joined splits in a graph: chunk lengths, cached lengths and inputs change between replays
+    dt, H, d, page, S = torch.bfloat16, 4, 128, 64, 3
+    c = Paged(dt, d, H, page, [3000, 2500, 700], seed=95, width=64)
+    cache = vdx.PagedKV(c.k, c.v, c.table)
+    q = _rand((600, H, d), dt, 96)
+    text = _rand((S, 150, H, d), dt, 97)
+    cu = cu_of([200, 200, 200])
+    out, lse = torch.full_like(q, 9.0), torch.full((H, 600), 7.0, device="cuda")
+
+    def step():
+        vdx.paged_attn(q, cache, cu, c.kv_len, max_q=300, max_kv=3000, causal_block=1, out=out, lse=lse)
+        return vdx.cross_attn(q.view(S, 200, H, d), text, text)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, ly = step()
+    for news, lens in (([200, 200, 200], [3000, 2500, 700]), ([300, 0, 150], [2999, 40, 150]), ([1, 299, 300], [64, 299, 700])):
+        cu.copy_(cu_of(news))
+        c.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(_rand((600, H, d), dt, sum(news)))
+        out.fill_(9.0)
+        lse.fill_(7.0)
+        g.replay()
+        vdx.sync_check()
+        _check_paged(c, q, out, lse, news, lens, 1, dt)
+        for b in range(S):
+            ref = attend(q.view(S, 200, H, d)[b], text[b], text[b], torch.full((200,), 150, device="cuda"))
+            check_attention(y[b], ly[b], ref, dt, f"text {b}")
+
+
 @pytest.mark.parametrize("n", [1, 300])
 def test_calls_on_a_side_stream_and_repeated_calls_are_bit_identical(n):
     dt, c, q, out, lse = _paged_case("bf16", 128, 4, 4, 64, [n, n], [3000, 777], 0)

@@ -393,26 +393,18 @@ attn_join(const __grid_constant__ KvParams p) {
   constexpr int kVals = D / 32;
   __shared__ float s_m[8], s_l[8], s_o[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
-  const long long idx = static_cast<long long>(blockIdx.x) * (8 / kPer) + warp / kPer;
-  const long long unit = idx / p.block_rows;
-  const int r = static_cast<int>(idx - unit * p.block_rows);
-  bool live = unit < static_cast<long long>(p.S) * p.Hkv * p.nblk;
-  int hk = 0, s = 0, tok = 0, h = 0;
-  SeqInfo sq{0, 0, 0};
-  if (live) {
-    hk = static_cast<int>(unit / p.nblk % p.Hkv);
-    s = static_cast<int>(unit / p.nblk / p.Hkv);
-    sq = sequence_info(p, s, false);
-    const long long R = unit % p.nblk * p.block_rows + r;
-    live = R < static_cast<long long>(min(sq.n, p.max_q)) * p.g;
-    tok = static_cast<int>(R / p.g);
-    h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
-  }
+  const unsigned unit = blockIdx.x, sh = unit / p.nblk;               // a block stays within one unit
+  const int r = blockIdx.y * (8 / kPer) + warp / kPer;
+  const int hk = static_cast<int>(sh % p.Hkv), s = static_cast<int>(sh / p.Hkv);
+  const SeqInfo sq = sequence_info(p, s, false);
+  const int R = static_cast<int>(unit - sh * p.nblk) * p.block_rows + r;      // rows of a kv head are < 2^31
+  const bool live = r < p.block_rows && R < min(sq.n, p.max_q) * p.g;
+  const int tok = R / p.g, h = hk * p.g + (R - tok * p.g);
   float m = -INFINITY, l = 0.f, acc[kVals];
 #pragma unroll
   for (int e = 0; e < kVals; ++e) acc[e] = 0.f;
   if (live) {
-    const long long base = unit * p.nsplit * p.block_rows + r;      // + z * block_rows
+    const long long base = static_cast<long long>(unit) * p.nsplit * p.block_rows + r;      // + z * block_rows
     for (int z = part + kPer * lane; z < p.nsplit; z += kPer * 32)
       m = fmaxf(m, p.part_ml[base + static_cast<long long>(z) * p.block_rows].x);
 #pragma unroll
@@ -516,13 +508,12 @@ cudaError_t launch(const KvParams& p, cudaStream_t stream) {
 }
 template <typename T, int D>
 cudaError_t join(const KvParams& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.block_rows;
-  const long long blocks = p.rows_kernel ? rows : (rows + 7) / 8;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (p.rows_kernel)
-    attn_join<T, D, 8><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+    attn_join<T, D, 8><<<dim3(static_cast<unsigned>(units), p.block_rows), 256, 0, stream>>>(p);
   else
-    attn_join<T, D, 1><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+    attn_join<T, D, 1><<<dim3(static_cast<unsigned>(units), (p.block_rows + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -108,6 +108,11 @@ __device__ __forceinline__ void st_shared_flag(uint32_t addr) {
   asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(1) : "memory");
 }
 
+// Latch a wait that gave up, and the first site that did, beside whatever else has been reported.
+__device__ __forceinline__ void report_timeout(int site) {
+  if ((atomicOr(&g_error_word, 1u) & 1u) == 0) atomicOr(&g_error_word, static_cast<unsigned>(site & 0xff) << 8);
+}
+
 // The rest of a warp's wait for a barrier phase whose first look (mbar_try_wait, which itself blocks for
 // a while) failed.  Kept out of line: a dozen inlined copies would spread the roles' loops over so
 // much code that they miss the instruction caches.  The warp gives up as one, when the CTA's abort
@@ -119,7 +124,7 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t a
     if (__any_sync(0xffffffffu, ld_shared_flag(abort_flag) != 0)) return false;
     if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) {
       st_shared_flag(abort_flag);
-      atomicCAS(&g_error_word, 0u, 1u | (static_cast<unsigned>(site & 0xff) << 8));
+      if ((threadIdx.x & 31) == 0) report_timeout(site);
       return false;
     }
   }
@@ -135,7 +140,7 @@ __device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, 
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
     if (__any_sync(0xffffffffu, ld_shared_flag(abort_flag) != 0 || global_timer_ns() - t0 > kWaitLimitNs)) {
       st_shared_flag(abort_flag);
-      atomicCAS(&g_error_word, 0u, 1u | (static_cast<unsigned>(site & 0xff) << 8));
+      if ((threadIdx.x & 31) == 0) report_timeout(site);
       return false;
     }
   }
@@ -157,7 +162,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicCAS(&g_error_word, 0u, 1u | (static_cast<unsigned>(kSiteDrain) << 8));
+      report_timeout(kSiteDrain);
       return;
     }
   }

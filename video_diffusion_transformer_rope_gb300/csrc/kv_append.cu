@@ -122,7 +122,7 @@ template <typename T, int D, int kTok, int kKind>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
   __shared__ __align__(16) float2 cs[kTok][D / 2];
   __shared__ long long s_at[kTok];    // where each token goes: cache offset, or grid token for q; < 0: nowhere
-  __shared__ long long s_pos[kTok];   // grid token; < 0: row skipped
+  __shared__ int s_axis[kTok][3];     // its (t, h, w)
   const int tid = threadIdx.x;
   RowWalk<T, D, kTok, kKind> rows;
   rows.init(p, row0);
@@ -130,20 +130,27 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
 
   for (int j = tid >> 5; j < kTok; j += kThreads / 32) {     // one warp per token
     const int r = row0 + j;
-    long long pos = -1, at = -1;
+    long long at = -1;
+    int frame = 0, row = 0, col = 0;
     if (r < p.rows) {
       const int s = find_sequence(p.cu, p.S, r);
       const int begin = __ldg(p.cu + s), end = __ldg(p.cu + s + 1);
       if (r >= begin && r < end) {
         const long long c = static_cast<long long>(__ldg(p.kv_len + s)) - (end - begin) + (r - begin);
-        pos = c + (p.pos_offset ? __ldg(p.pos_offset + s) : 0);
+        const long long pos = c + (p.pos_offset ? __ldg(p.pos_offset + s) : 0);
         if (c < 0 || c >= static_cast<long long>(p.max_pages) * p.P || pos < 0 ||
             pos >= static_cast<long long>(p.T) * p.Hg * p.Wg) {
           if ((tid & 31) == 0) atomicOr(&g_error_word, kErrPosition);
-          pos = -1;
-        } else if (kKind == 0) {
-          at = pos;
         } else {
+          const int area = p.Hg * p.Wg;
+          frame = static_cast<int>(pos / area);
+          const int rest = static_cast<int>(pos - static_cast<long long>(frame) * area);
+          row = rest / p.Wg;
+          col = rest - row * p.Wg;
+          at = pos;
+        }
+        if (kKind != 0 && at >= 0) {
+          at = -1;
           const int pg = static_cast<int>(c / p.P), slot = static_cast<int>(c - static_cast<long long>(pg) * p.P);
           const int page = __ldg(p.table + s * p.table_stride + pg);
           if (page < 0 || page >= p.num_pages) {
@@ -155,22 +162,17 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
       }
     }
     if ((tid & 31) == 0) {
-      s_pos[j] = pos;
       s_at[j] = at;
+      s_axis[j][0] = frame;
+      s_axis[j][1] = row;
+      s_axis[j][2] = col;
     }
   }
   __syncthreads();
   if (kKind < 2) {
     for (int i = tid; i < kTok * (D / 2); i += kThreads) {
       const int j = i / (D / 2), pr = i % (D / 2);
-      const long long pos = s_pos[j];
-      if (pos < 0) continue;
-      const unsigned area = static_cast<unsigned>(p.Hg) * static_cast<unsigned>(p.Wg);
-      const unsigned long long frame = static_cast<unsigned long long>(pos) / area;
-      const unsigned rest = static_cast<unsigned>(pos - frame * area);
-      const unsigned long long x = pr < p.half_t ? frame
-                                   : (pr < p.half_t + p.half_h ? rest / static_cast<unsigned>(p.Wg)
-                                                               : rest % static_cast<unsigned>(p.Wg));
+      const unsigned long long x = static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]);
       const int hi = static_cast<int>((x * p.turn[pr]) >> 32);        // turns in [-1/2, 1/2) * 2^32
       float sn, cn;
       sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);

@@ -146,7 +146,7 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
   p.scale_log2 = static_cast<float>((scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(pb->d))) * 1.4426950408889634);
   pb->nothing = q.empty();
   if (pb->nothing) return VDX_OK;
-  if (static_cast<long long>(p.max_q) * p.g > 0x7fffffffll)
+  if (static_cast<long long>(p.max_q) * p.g > 0x7ffff000ll)     // row numbers of padded blocks stay in an int
     return fail(VDX_ERR_ARG, "%d rows of %d heads per kv head are too many", p.max_q, p.g);
   if (vdx_status s = check_tensor("q", q, true)) return s;
   if (vdx_status s = check_tensor("k", k, true)) return s;
@@ -251,11 +251,16 @@ vdx_status launch(const Problem& pb, void* stream) {
     if (!vdx::encode_tiled_fn(&encode)) return VDX_ERR_CUDA;
     e = vdx::launch_attn_tiles(pb.p, pb.d, pb.dtype, encode, multiprocessors(), st, &what);
   }
-  if (e != cudaSuccess)
+  if (e != cudaSuccess) {
+    cudaGetLastError();          // reported here; not left for the process's next CUDA call
     return fail(VDX_ERR_CUDA, "attention kernel launch: %s%s%s", what ? what : "", what ? ": " : "", cudaGetErrorString(e));
+  }
   if (pb.p.nsplit > 1 && !pb.p.cluster) {
     e = vdx::launch_attn_combine(pb.p, pb.d, pb.dtype, st);
-    if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(VDX_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
+    }
   }
   return VDX_OK;
 }
@@ -320,6 +325,8 @@ size_t plan_attention(KvParams* p, int d, int sms) {
         p->nsplit = n;
       }
     }
+    // a unit of 2^17 tiles takes about 0.2 s, well inside the limit of the kernel's waits for it
+    p->nsplit = static_cast<int>(std::max<long long>(p->nsplit, (tiles + (1 << 17) - 1) >> 17));
     p->split_keys = static_cast<int>((tiles + p->nsplit - 1) / p->nsplit);
     p->nsplit = static_cast<int>((tiles + p->split_keys - 1) / p->split_keys);
   }
@@ -398,7 +405,10 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
       p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
     }
   const cudaError_t e = vdx::launch_append(p, d, c->dtype, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
+  }
   return VDX_OK;
 }
 
