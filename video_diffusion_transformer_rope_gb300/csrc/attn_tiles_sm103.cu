@@ -446,7 +446,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      int kv = 0;                                       // key tiles so far
+      int kv = 0, k_issued = 0;                         // key tiles so far; tiles of K (an abort may fall between)
       bool ok = true;
       UnitReader in{sCtl};
       for (int it = cluster; ok && it < units; it += clusters) {
@@ -503,6 +503,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             if (kv >= kS && !(ok = wait(empty, kv / kS - 1, which == 0 ? kSiteKEmpty : kSiteVEmpty))) break;
             const uint32_t bar = (which == 0 ? sCtl + kBarKFull : sCtl + kBarVFull) + 8 * st;
             if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            if (which == 0) ++k_issued;
             __syncwarp();
             if (lane >= b0 && lane < b0 + n) {
               const uint32_t row = one ? 0u : static_cast<uint32_t>((lane - b0) * box);
@@ -526,10 +527,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // an abort may have stopped: its own copies are waited for by the bounded drain)
       if (lane == 0) {
         for (int st = 0; st < kS; ++st) {
-          if (kv > st) {
-            drain_wait(sCtl + kBarKFull + 8 * st, ((kv - 1 - st) / kS) & 1);
-            drain_wait(sCtl + kBarVFull + 8 * st, ((kv - 1 - st) / kS) & 1);
-          }
+          if (k_issued > st) drain_wait(sCtl + kBarKFull + 8 * st, ((k_issued - 1 - st) / kS) & 1);
+          if (kv > st) drain_wait(sCtl + kBarVFull + 8 * st, ((kv - 1 - st) / kS) & 1);
         }
       }
       __syncwarp();
@@ -673,7 +672,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (lane == 0) tma_prefetch_desc(&tm_q);
       const uint32_t q_bytes = static_cast<uint32_t>(per_tile * p.g) * D * 2;
       bool ok = true;
-      int k = 0, n = 0;                                 // units, units with key tiles
+      int k = 0, n = 0, q_issued = 0;                   // units, units with key tiles, Q tiles
       for (int it = cluster; ok && it < units; it += clusters, ++k) {
         const int slot = k % kUnitSlots;
         if (k >= kUnitSlots && !(ok = wait(sCtl + kBarUnitEmpty + 8 * slot, k / kUnitSlots - 1, kSiteUnitEmpty))) break;
@@ -695,13 +694,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
               tma_load_4d(sQ + b * Lo::kQBytes + h * Lo::kQPart, &tm_q, bar, h * 64, u.hk * p.g,
                           u.row0 + u.tok0 + (2 * i + static_cast<int>(rank)) * per_tile, kPaged || p.q_b == 0 ? 0 : u.s);
           }
+          ++q_issued;
           __syncwarp();
         }
         if (ok) ++n;
       }
       if (lane == 0)
         for (int b = 0; b < kQBufs; ++b)
-          if (n > (b >> 1)) drain_wait(sCtl + kBarQFull + 8 * b, ((n - 1 - (b >> 1)) >> 1) & 1);
+          if (q_issued > b) drain_wait(sCtl + kBarQFull + 8 * b, ((q_issued - 1 - b) / kQBufs) & 1);
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ output tiles
