@@ -73,11 +73,12 @@ struct Layout {
 
 enum : int {
   kSiteQFull = 32, kSiteQEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePReady,
-  kSiteOFull, kSiteOEmpty, kSiteDrain, kSiteUnitFull, kSiteUnitEmpty, kSiteStaged, kSiteRelay
+  kSiteOFull, kSiteOEmpty, kSiteDrain, kSiteUnitFull, kSiteUnitEmpty, kSiteStaged, kSiteRelay, kSiteClaim
 };
 
 // One unit of work, as warp 10 hands it to the other roles.
 struct Unit {
+  int end;                 // no unit: none is left
   int s, hk, unit, z;      // sequence, kv head, index among (sequence, head, block), split
   int row0, n, keys;       // the sequence's first row, rows and keys (SeqInfo)
   int tok0, ntok;          // first token of the block and live tokens in it (<= 0: none)
@@ -93,7 +94,9 @@ struct Ctl {
   uint64_t s_full[2], p_ready[2];
   uint64_t o_full[2], o_empty[2], staged[2];
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+  uint64_t claim_full, claim_ready;
   uint64_t done;
+  alignas(16) uint32_t claim[4];     // answer to the claim of a further cluster's work
   Unit unit[kUnitSlots];
   uint32_t tmem_base;
   int abort_flag;
@@ -153,7 +156,8 @@ constexpr uint32_t kBarQFull = offsetof(Ctl, q_full), kBarQEmpty = offsetof(Ctl,
                    kBarSFull = offsetof(Ctl, s_full), kBarPReady = offsetof(Ctl, p_ready), kBarOFull = offsetof(Ctl, o_full),
                    kBarOEmpty = offsetof(Ctl, o_empty), kBarStaged = offsetof(Ctl, staged),
                    kBarUnitFull = offsetof(Ctl, unit_full), kBarUnitEmpty = offsetof(Ctl, unit_empty),
-                   kBarDone = offsetof(Ctl, done), kOffUnit = offsetof(Ctl, unit), kOffAbort = offsetof(Ctl, abort_flag);
+                   kBarClaimFull = offsetof(Ctl, claim_full), kBarClaimReady = offsetof(Ctl, claim_ready),
+                   kOffClaim = offsetof(Ctl, claim), kBarDone = offsetof(Ctl, done), kOffUnit = offsetof(Ctl, unit), kOffAbort = offsetof(Ctl, abort_flag);
 
 // Bounded wait on the way out, whatever the abort flag says: copies and MMAs in flight finish
 // before shared or tensor memory is released.
@@ -228,6 +232,7 @@ struct TileCursor {
 template <bool kPaged>
 __device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom<kPaged>& g, int it, bool report) {
   Unit u;
+  u.end = 0;
   const int blk = it % p.nblk;
   int r = it / p.nblk;
   u.z = r % p.nsplit;
@@ -365,6 +370,27 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* r, bool align
   }
 }
 
+// Ask for a cluster of the grid that has not been launched: the 16-byte answer goes to this offset of every CTA
+// of this cluster, counted on its barrier.  Not to be asked again once an answer was "none".
+__device__ __forceinline__ void claim_cluster(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];"
+      ::"r"(answer), "r"(bar) : "memory");
+}
+// The unit of the claimed cluster (its index in the grid), or `none`.
+__device__ __forceinline__ int claimed_cluster(uint32_t answer, int none) {
+  const uint4 a = ld_shared_v4(answer);
+  const uint64_t lo = a.x | (static_cast<uint64_t>(a.y) << 32), hi = a.z | (static_cast<uint64_t>(a.w) << 32);
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tmov.b128 r, {%2, %3};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x) : "l"(lo), "l"(hi) : "memory");
+  fence_proxy_async_smem();          // the next answer is written by the async proxy, after this read
+  return got && static_cast<int>(x >> 1) < none ? static_cast<int>(x >> 1) : none;
+}
+
 // Rows of V past the last visible key become zeros (this CTA's half of the tile; whole warp).
 template <int D>
 __device__ __noinline__ void zero_v_rows(uint32_t v_smem, int from, int lane) {
@@ -381,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kbox,
            const __grid_constant__ CUtensorMap tm_vbox, const __grid_constant__ CUtensorMap tm_out,
-           const __grid_constant__ KvParams p, const int units) {
+           const __grid_constant__ KvParams p, const int units, const int claim) {
   using Lo = Layout<D>;
   constexpr int kS = Lo::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -391,7 +417,6 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   const uint32_t sQ = smem_addr(smem), sK = smem_addr(smem + Lo::kOffK), sV = smem_addr(smem + Lo::kOffV);
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
   if (tid == 0) {
     // rank 0's full barriers also count one relayed arrival from rank 1, its P-ready and O-empty
@@ -418,6 +443,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       mbar_init(smem_addr(&ctl->unit_full[i]), 1);
       mbar_init(smem_addr(&ctl->unit_empty[i]), kUnitReaders);
     }
+    mbar_init(smem_addr(&ctl->claim_full), 1);
+    mbar_init(smem_addr(&ctl->claim_ready), 2);          // both CTAs' (used on rank 0)
     mbar_init(smem_addr(&ctl->done), 1);
     ctl->abort_flag = 0;
     fence_barrier_init();
@@ -449,8 +476,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       int kv = 0, k_issued = 0;                         // key tiles so far; tiles of K (an abort may fall between)
       bool ok = true;
       UnitReader in{sCtl};
-      for (int it = cluster; ok && it < units; it += clusters) {
+      while (ok) {
         if (!(ok = in.wait())) break;
+        if (VDX_UNIT(in, end)) {
+          in.release();
+          break;
+        }
         const int t0 = VDX_UNIT(in, t0), t1 = VDX_UNIT(in, t1), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk);
         const int len = kPaged ? VDX_UNIT(in, len) : 0;
         in.release();
@@ -558,8 +589,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         have = false;
       };
       UnitReader in{sCtl};
-      for (int it = cluster; ok && it < units; it += clusters) {
+      while (ok) {
         if (!(ok = in.wait())) break;
+        if (VDX_UNIT(in, end)) {
+          in.release();
+          break;
+        }
         int left = VDX_UNIT(in, t1) - VDX_UNIT(in, t0);
         const int tail = VDX_UNIT(in, tail);
         const bool two = VDX_UNIT(in, ntok) > 2 * per_tile;
@@ -635,8 +670,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       int st = 0, ph = 0, n = 0;
       bool ok = true;
       UnitReader in{sCtl};
-      for (int it = cluster; ok && it < units; it += clusters) {
+      while (ok) {
         if (!(ok = in.wait())) break;
+        if (VDX_UNIT(in, end)) {
+          in.release();
+          break;
+        }
         int left = VDX_UNIT(in, t1) - VDX_UNIT(in, t0);
         const int tail = VDX_UNIT(in, tail);
         in.release();
@@ -672,33 +711,63 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (lane == 0) tma_prefetch_desc(&tm_q);
       const uint32_t q_bytes = static_cast<uint32_t>(per_tile * p.g) * D * 2;
       bool ok = true;
-      int k = 0, n = 0, q_issued = 0;                   // units, units with key tiles, Q tiles
-      for (int it = cluster; ok && it < units; it += clusters, ++k) {
+      int n = 0, q_issued = 0;                          // units with key tiles, Q tiles
+      int it = static_cast<int>(blockIdx.x >> 1), claims = 0;
+      const uint32_t remote = mapa_shared(sCtl, 0);
+      for (int k = 0;; ++k) {
+        // slot k is free: its last unit, k - 4, was released before unit k - 1 was claimed
         const int slot = k % kUnitSlots;
-        if (k >= kUnitSlots && !(ok = wait(sCtl + kBarUnitEmpty + 8 * slot, k / kUnitSlots - 1, kSiteUnitEmpty))) break;
-        const Unit u = make_unit<kPaged>(p, geom, it, leader && lane == 0);
+        Unit u;
+        u.end = 1;
+        u.t0 = u.t1 = u.ntok = 0;
+        const bool more = it < units;
+        if (more) u = make_unit<kPaged>(p, geom, it, leader && lane == 0);
         if (lane == 0) {
           ctl->unit[slot] = u;
           mbar_arrive(sCtl + kBarUnitFull + 8 * slot);
         }
         __syncwarp();
-        if (u.t0 >= u.t1) continue;
-        for (int i = 0; i < 2; ++i) {
-          const int b = 2 * (n & 1) + i;
-          if (n >= 2 && !(ok = wait(sCtl + kBarQEmpty + 8 * b, (n >> 1) - 1, kSiteQEmpty))) break;
-          if (lane == 0) {
-            const uint32_t bar = sCtl + kBarQFull + 8 * b;
-            mbar_arrive_expect_tx(bar, q_bytes);
+        if (!more) break;
+        if (u.t0 < u.t1) {
+          for (int i = 0; i < 2; ++i) {
+            const int b = 2 * (n & 1) + i;
+            if (n >= 2 && !(ok = wait(sCtl + kBarQEmpty + 8 * b, (n >> 1) - 1, kSiteQEmpty))) break;
+            if (lane == 0) {
+              const uint32_t bar = sCtl + kBarQFull + 8 * b;
+              mbar_arrive_expect_tx(bar, q_bytes);
 #pragma unroll
-            for (int h = 0; h < Lo::kParts; ++h)
-              tma_load_4d(sQ + b * Lo::kQBytes + h * Lo::kQPart, &tm_q, bar, h * 64, u.hk * p.g,
-                          u.row0 + u.tok0 + (2 * i + static_cast<int>(rank)) * per_tile, kPaged || p.q_b == 0 ? 0 : u.s);
+              for (int h = 0; h < Lo::kParts; ++h)
+                tma_load_4d(sQ + b * Lo::kQBytes + h * Lo::kQPart, &tm_q, bar, h * 64, u.hk * p.g,
+                            u.row0 + u.tok0 + (2 * i + static_cast<int>(rank)) * per_tile, kPaged || p.q_b == 0 ? 0 : u.s);
+            }
+            ++q_issued;
+            __syncwarp();
           }
-          ++q_issued;
+          if (!ok) break;
+          ++n;
+        }
+        it = units;
+        if (!claim) continue;                           // every cluster of the grid runs at once
+        // When the unit before this one is done, claim the work of a cluster that has not started yet as the
+        // next: rank 0 asks once both CTAs expect the answer and have read the one before; it comes to
+        // both.  Claimed any earlier, the units of a short call would be dealt out before their lengths tell.
+        if (k > 0 && !(ok = wait(sCtl + kBarUnitEmpty + 8 * ((k - 1) % kUnitSlots), (k - 1) / kUnitSlots, kSiteUnitEmpty))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(sCtl + kBarClaimFull, 16);
+          mbar_arrive_remote_cluster(remote + kBarClaimReady);
+        }
+        __syncwarp();
+        if (leader) {
+          if (!(ok = wait(sCtl + kBarClaimReady, claims, kSiteClaim))) break;
+          if (lane == 0) claim_cluster(sCtl + kOffClaim, sCtl + kBarClaimFull);
           __syncwarp();
         }
-        if (ok) ++n;
+        ++claims;
+        if (!(ok = wait(sCtl + kBarClaimFull, claims - 1, kSiteClaim))) break;
+        it = claimed_cluster(sCtl + kOffClaim, units);
+        __syncwarp();
       }
+      if (lane == 0 && claims > 0) drain_wait(sCtl + kBarClaimFull, (claims - 1) & 1);
       if (lane == 0)
         for (int b = 0; b < kQBufs; ++b)
           if (q_issued > b) drain_wait(sCtl + kBarQFull + 8 * b, ((q_issued - 1 - b) / kQBufs) & 1);
@@ -708,8 +777,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       bool ok = true;
       int n = 0, n1 = 0;
       UnitReader in{sCtl};
-      for (int it = cluster; ok && it < units; it += clusters) {
+      while (ok) {
         if (!(ok = in.wait())) break;
+        if (VDX_UNIT(in, end)) {
+          in.release();
+          break;
+        }
         const bool tiles = VDX_UNIT(in, t0) < VDX_UNIT(in, t1);
         const int ntok = VDX_UNIT(in, ntok), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk);
         const int tok0 = VDX_UNIT(in, tok0) + (kPaged ? VDX_UNIT(in, row0) : 0);
@@ -784,7 +857,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         if (lane == 0) mbar_arrive_remote(remote + bar);
       }
     };
-    for (int it = cluster, k = 0; ok && it < units; it += clusters, ++k) {
+    for (int k = 0; ok; ++k) {
       // The unit's fields are read from its slot where they are needed (the score row leaves no
       // registers to keep them in); the slot is free when the unit is done.
       const int slot = k % kUnitSlots;
@@ -794,6 +867,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) mbar_arrive(sCtl + kBarUnitEmpty + 8 * slot);
       };
+      if (u.end) {
+        release();
+        break;
+      }
       int t = u.t0;
       const int t1 = u.t1;
       if (t < t1) ++nq;
@@ -991,10 +1068,9 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   const cudaError_t e = allow_shared(kernel, smem, &done[(p.table ? 2 : 0) + (p.nsplit > 1 ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
-  if (units > 0x7fffffffLL - sms) return cudaErrorInvalidConfiguration;
-  const int clusters = static_cast<int>(units < sms / 2 ? units : sms / 2);
+  if (units > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * units));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
@@ -1005,7 +1081,7 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mkb, mvb, mo, p, static_cast<int>(units));
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mkb, mvb, mo, p, static_cast<int>(units), units > sms / 2 ? 1 : 0);
 }
 
 }  // namespace
