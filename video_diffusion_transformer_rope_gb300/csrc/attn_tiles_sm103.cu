@@ -10,7 +10,9 @@
 //
 // A unit of work is (sequence, kv head, block of 4 x 128 query rows, range of 128-key tiles); the
 // rows of a block are (token, query head of the group) pairs, so grouped heads share every key
-// they read.  Clusters of two CTAs, one CTA per multiprocessor, walk units c, c + clusters, ...
+// they read.  The grid has a cluster of two CTAs per unit, of which one per two multiprocessors run: each
+// takes its own unit and then claims those of clusters that have not started (launch control answers
+// with their index), one ahead of its work, so units of uneven length even out.
 // Each CTA holds two Q tiles of 128 rows (tile i of rank r: rows 256 i + 128 r and up of the block)
 // and half of every key tile (64 keys of K, half the channels of V); rank 0 issues cta_group::2
 // MMAs over both CTAs' rows and halves.  The halves leave room for the Q tiles of two units, so

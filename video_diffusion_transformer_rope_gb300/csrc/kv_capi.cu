@@ -312,14 +312,18 @@ size_t plan_attention(KvParams* p, int d, int sms) {
     if (p->max_kv > 0)
       tiles = p->box_rows ? (p->max_kv + 127) / 128
                     : static_cast<long long>(p->max_kv / p->P) * ((p->P + 127) / 128) + (p->max_kv % p->P + 127) / 128;
-    // Splits: the sms / 2 CTA pairs take ceil(units * splits / pairs) units each, a unit costs its
-    // tiles and about two tiles' time to start and finish; a split call also writes and joins
-    // partial results (about a tile's time per unit).
+    // Splits: the sms / 2 CTA pairs take ceil(units * splits / pairs) units each; a unit costs its
+    // tiles and about two tiles' time to start and finish, a split one up to two more for its partial
+    // results, as its rows fill a block, and their join two to six in all (tile time: 1.4 us).  480p
+    // frame of 96 units of 256 tiles: 3 splits 514 us, 1 split 706, 4 557; 40 units of 32 tiles: 512
+    // rows each 1 split 54 us, 3 splits 60; 33 rows each 53 and 44.
+    const long long fill = std::min<long long>(16, rows * 16 / p->block_rows);      // of a block, in sixteenths
     long long best = 0;
     p->nsplit = 1;
     for (int n = 1; n <= 32 && n <= tiles; ++n) {
       const long long per_split = (tiles + n - 1) / n;
-      const long long cost = (units * n + sms / 2 - 1) / (sms / 2) * (per_split + (n > 1 ? 3 : 2));
+      const long long rounds = (units * n + sms / 2 - 1) / (sms / 2);
+      const long long cost = n == 1 ? rounds * 16 * (per_split + 2) : rounds * (16 * (per_split + 2) + 2 * fill) + 32 + 4 * fill;
       if (n == 1 || cost < best) {
         best = cost;
         p->nsplit = n;
