@@ -715,10 +715,11 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       bool ok = true;
       int n = 0, q_issued = 0;                          // units with key tiles, Q tiles
       int it = static_cast<int>(blockIdx.x >> 1), claims = 0;
+      int busy = -1;                                    // the last unit with key tiles
       const uint32_t remote = mapa_shared(sCtl, 0);
       for (int k = 0;; ++k) {
-        // slot k is free: its last unit, k - 4, was released before unit k - 1 was claimed
         const int slot = k % kUnitSlots;
+        if (k >= kUnitSlots && !(ok = wait(sCtl + kBarUnitEmpty + 8 * slot, k / kUnitSlots - 1, kSiteUnitEmpty))) break;
         Unit u;
         u.end = 1;
         u.t0 = u.t1 = u.ntok = 0;
@@ -747,13 +748,17 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           if (!ok) break;
           ++n;
+          // When the unit with tiles before this one is done, claim a further one.  Claimed any earlier, the units
+          // of a short call would be dealt out before their lengths tell.  (Its slot, taken again, says so.)
+          if (claim && busy >= 0 && k - busy < kUnitSlots &&
+              !(ok = wait(sCtl + kBarUnitEmpty + 8 * (busy % kUnitSlots), busy / kUnitSlots, kSiteUnitEmpty)))
+            break;
+          busy = k;
         }
         it = units;
         if (!claim) continue;                           // every cluster of the grid runs at once
-        // When the unit before this one is done, claim the work of a cluster that has not started yet as the
-        // next: rank 0 asks once both CTAs expect the answer and have read the one before; it comes to
-        // both.  Claimed any earlier, the units of a short call would be dealt out before their lengths tell.
-        if (k > 0 && !(ok = wait(sCtl + kBarUnitEmpty + 8 * ((k - 1) % kUnitSlots), (k - 1) / kUnitSlots, kSiteUnitEmpty))) break;
+        // Claim the work of a cluster that has not started yet: rank 0 asks once both CTAs expect the answer
+        // and have read the one before; it comes to both.
         if (lane == 0) {
           mbar_arrive_expect_tx(sCtl + kBarClaimFull, 16);
           mbar_arrive_remote_cluster(remote + kBarClaimReady);
