@@ -240,8 +240,8 @@ typedef struct vdx_paged_kv {
  * dropped from its table).  With q_norm / k_norm (d values of the call's type, shared by the
  * heads) x * rsqrt(mean(x^2) + eps) * weight is applied to each head before the rotation.
  * fp32 arithmetic, angles reduced exactly, one rounding at the end; v is copied bit for bit.
- * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place);
- * otherwise the outputs must not overlap an input.  A token outside the grid's T*Hgrid*Wgrid
+ * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place),
+ * also inside a fused projection; otherwise the outputs must not overlap an input, nor each other.  A token outside the grid's T*Hgrid*Wgrid
  * positions, or with a cache index below 0 or past its page table, is skipped and reported.
  * Two rows of one call that land in the same cache slot leave one of them there. */
 typedef struct vdx_append_args {

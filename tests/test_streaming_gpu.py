@@ -90,6 +90,28 @@ def test_append_in_place_and_without_queries():
     assert torch.equal(q, want) and torch.equal(qkv[:, 2:], before)
 
 
+@pytest.mark.parametrize("layout", ["kinds", "kinds_of_a_head", "padded"])
+def test_append_in_place_within_a_fused_projection(layout):
+    dt, d, H, n, grid = torch.bfloat16, 128, 3, 40, (40, 1, 1)
+    if layout == "kinds":                                            # [rows, 3, H, d]
+        x = _rand((n, 3, H, d), dt, 60)
+        q, k, v = x.unbind(1)
+    elif layout == "kinds_of_a_head":                                # [rows, H, 3, d]
+        x = _rand((n, H, 3, d), dt, 61)
+        q, k, v = x.unbind(2)
+    else:                                                            # v, q, k and a gap
+        x = _rand((n, 3 * H + 1, d), dt, 62)
+        v, q, k = x[:, :H], x[:, H:2 * H], x[:, 2 * H:3 * H]
+    before = [t.clone() for t in (q, k, v)]
+    c = Paged(dt, d, H, 16, [n], seed=63)
+    r = vdx.rope3d_append(q, k, v, vdx.PagedKV(c.k, c.v, c.table), cu_of([n]), c.kv_len, grid, SECTIONS[d], q_out=q)
+    vdx.sync_check()
+    pos = torch.arange(n, device="cuda")
+    ref = rotate(before[0], pos, grid, SECTIONS[d], 10000.0, None, 1e-6)
+    assert r is q and bool(((q.double() - ref).abs() <= rotate_bound(ref, dt)).all())
+    assert torch.equal(k, before[1]) and torch.equal(v, before[2]) and torch.equal(c.v[c.slots(0, pos)], v)
+
+
 def test_append_skips_and_reports_what_has_no_place():
     c = Paged(torch.bfloat16, 64, 1, 16, [20, 4], seed=11)
     k0 = c.k.clone()

@@ -160,6 +160,25 @@ def test_cross_refusals(L, kw, status, msg):
     assert r == status and msg in L.vdx_last_error().decode(), L.vdx_last_error()
 
 
+@pytest.mark.parametrize("ckw,kw,msg", [
+    # rows or slots that lie over one another: two rows of the call would write one place
+    (dict(), dict(q_out_row=384), "q_out"),
+    (dict(), dict(q_out_row=128, q_out_head=128 * 6), "q_out"),
+    (dict(k_token=384), dict(), "key cache"),
+    (dict(v_page=15 * 512), dict(), "value cache"),
+    (dict(v=FAKE), dict(), "same memory"),
+    # q in place, and k or v in the rows that it turns
+    (dict(), dict(q_out=FAKE + 3 * G, k=FAKE + 3 * G), "q_out overlaps"),
+    (dict(), dict(q_out=FAKE + 3 * G, v=FAKE + 3 * G + 256), "q_out overlaps"),
+    (dict(), dict(q_out=FAKE + 3 * G, q_row=1536, q_out_row=1536, k_row=1536, k=FAKE + 3 * G + 1024 - 256), "q_out overlaps"),
+    (dict(), dict(q_out=FAKE + 3 * G, q_row=1536, q_out_row=1536, v_row=1536, v=FAKE + 3 * G - 768), "q_out overlaps"),
+    (dict(), dict(q_out=FAKE + 3 * G, q_row=384, q_out_row=384), "q_out"),
+])
+def test_append_refuses_outputs_over_other_tensors(L, ckw, kw, msg):
+    r = L.vdx_rope3d_append(ctypes.byref(_cache(**ckw)), ctypes.byref(_append(**kw)), None)
+    assert r == B.VDX_ERR_ARG and msg in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
 def test_null_structures(L):
     assert L.vdx_rope3d_append(None, ctypes.byref(_append()), None) == B.VDX_ERR_ARG
     assert L.vdx_rope3d_append(ctypes.byref(_cache()), None, None) == B.VDX_ERR_ARG

@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <numeric>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -63,6 +64,42 @@ bool overlap(const Tensor& a, const Tensor& b) {
 bool overlap(const Tensor& a, const void* p, size_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(p);
   return p && bytes && !a.empty() && a.begin() < x + bytes && x < a.end();
+}
+
+// Whether no row of `a` shares an element with a row of `b`, also where their spans interleave (slices of one
+// fused projection): true if, with some of the dimensions walked inside a window, the windows of both
+// repeat by steps with a common divisor and lie apart within it.
+bool rows_apart(const Tensor& a, const Tensor& b) {
+  if (!overlap(a, b)) return true;
+  const long long delta = (static_cast<long long>(b.begin()) - static_cast<long long>(a.begin())) / 2;
+  for (int inside = 0; inside < 7; ++inside) {
+    long long wa = a.d, wb = b.d, step = 0;
+    for (int i = 0; i < 3; ++i)
+      if (inside >> i & 1) {
+        wa += (a.n[i] - 1) * a.stride[i];
+        wb += (b.n[i] - 1) * b.stride[i];
+      } else {
+        if (a.n[i] > 1) step = std::gcd(step, a.stride[i]);
+        if (b.n[i] > 1) step = std::gcd(step, b.stride[i]);
+      }
+    if (step == 0) continue;
+    const long long at = (delta % step + step) % step;
+    if (at >= wa && at + wb <= step) return true;
+  }
+  return false;
+}
+// Whether the rows of a tensor that is written lie apart from one another.
+bool rows_distinct(const Tensor& t) {
+  if (t.empty()) return true;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return t.stride[x] < t.stride[y]; });
+  long long span = t.d;
+  for (int i : order) {
+    if (t.n[i] <= 1) continue;
+    if (t.stride[i] < span) return false;
+    span += (t.n[i] - 1) * t.stride[i];
+  }
+  return true;
 }
 
 constexpr long long kMaxStride = 1ll << 38;   // elements: a tensor map's strides stay below 2^40 bytes
@@ -381,8 +418,12 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
     return fail(VDX_ERR_ALIGN, "q_norm or k_norm is not 16-byte aligned");
   const Tensor kc = cache_tensor(*c, false), vc = cache_tensor(*c, true);
   const bool in_place = a->q && a->q == a->q_out && a->q_row == a->q_out_row && a->q_head == a->q_out_head;
-  if (a->q && !in_place && (overlap(qo, q) || overlap(qo, k) || overlap(qo, v)))
+  if (a->q && ((!in_place && !rows_apart(qo, q)) || !rows_apart(qo, k) || !rows_apart(qo, v)))
     return fail(VDX_ERR_ARG, "q_out overlaps q, k or v");
+  if (!rows_distinct(qo)) return fail(VDX_ERR_ARG, "rows of q_out overlap one another");
+  if (!rows_distinct(kc)) return fail(VDX_ERR_ARG, "tokens of the key cache overlap one another");
+  if (!rows_distinct(vc)) return fail(VDX_ERR_ARG, "tokens of the value cache overlap one another");
+  if (c->k == c->v) return fail(VDX_ERR_ARG, "the key and value caches are the same memory");
   for (const Tensor* t : {&kc, &vc})
     if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
       return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
