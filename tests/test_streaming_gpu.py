@@ -112,6 +112,30 @@ def test_append_in_place_within_a_fused_projection(layout):
     assert torch.equal(k, before[1]) and torch.equal(v, before[2]) and torch.equal(c.v[c.slots(0, pos)], v)
 
 
+def test_append_of_queries_without_heads_is_refused():
+    c = Paged(torch.bfloat16, 128, 2, 16, [5], seed=64)
+    x = _rand((5, 2, 128), torch.bfloat16, 65)
+    with pytest.raises(vdx.VdxError):
+        vdx.rope3d_append(x[:, :0], x, x, vdx.PagedKV(c.k, c.v, c.table), cu_of([5]), c.kv_len, (5, 1, 1))
+
+
+def test_sizes_past_32_bits_are_refused():
+    # broadcast views: nothing of this size is in memory
+    n, dt = 2 ** 32 + 1, torch.bfloat16
+    x = torch.zeros(1, 1, 1, 128, dtype=dt, device="cuda")
+    long = x.expand(1, n, 1, 128)
+    out = torch.empty(1, 1, 1, 128, dtype=dt, device="cuda")
+    with pytest.raises(vdx.VdxError):
+        vdx.cross_attn(x, long, long, out=out)
+    pages = torch.zeros(1, 16, 1, 128, dtype=dt, device="cuda")
+    cu, one = cu_of([1]), torch.ones(1, dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for cache in (vdx.PagedKV(pages.expand(n, -1, -1, -1), pages.expand(n, -1, -1, -1), table),
+                  vdx.PagedKV(pages, pages.clone(), table.expand(n, 1))):
+        with pytest.raises(vdx.VdxError):
+            vdx.paged_attn(x[0], cache, cu, one)
+
+
 def test_append_skips_and_reports_what_has_no_place():
     c = Paged(torch.bfloat16, 64, 1, 16, [20, 4], seed=11)
     k0 = c.k.clone()

@@ -44,6 +44,8 @@ def _tensor(name, t, like, dims):
     shape, stride = t.shape, t.stride()
     if len(shape) != dims:
         raise VdxError(VDX_ERR_ARG, f"{name} must have {dims} dimensions, got {tuple(shape)}")
+    if max(shape) > _I32_MAX:
+        raise VdxError(VDX_ERR_ARG, f"{name}: {tuple(shape)} is too large")
     if stride[-1] != 1 and shape[-1] > 1:
         raise VdxError(VDX_ERR_ARG, f"{name}: the channels of a head must be contiguous")
     if t.requires_grad and _torch.is_grad_enabled():
@@ -124,7 +126,7 @@ class PagedKV:
             raise VdxError(VDX_ERR_ARG, f"the key and value caches differ in shape: {tuple(ks)}, {tuple(vs)}")
         torch = _torch
         if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.get_device() != k.get_device()
-                or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
+                or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or max(t.shape) > _I32_MAX):
             raise VdxError(VDX_ERR_ARG, f"page_table must be an int32 [seqs, max_pages] tensor on {k.device} with contiguous rows")
         seqs, width = t.shape
         return B.PagedKvStruct(k.data_ptr(), v.data_ptr(), kst[0], kst[1], kst[2], vst[0], vst[1], vst[2], t.data_ptr(),
@@ -162,7 +164,9 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
         Hq, q_ptr = qs[1], q.data_ptr()
         if qs[0] != rows or qs[2] != d:
             raise VdxError(VDX_ERR_ARG, f"q {tuple(qs)} does not match the {rows} rows of {d} channels of k")
-        if rows == 0 or Hq == 0:                        # empty tensors have no address
+        if Hq == 0:
+            raise VdxError(VDX_ERR_ARG, "q has no heads (q=None appends keys and values only)")
+        if rows == 0:                                   # empty tensors have no address
             return _torch.empty(qs, dtype=q.dtype, device=q.device) if q_out is None else q_out
     elif q_out is not None:
         raise VdxError(VDX_ERR_ARG, "q_out without q")
