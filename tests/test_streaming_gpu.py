@@ -619,6 +619,89 @@ def test_calls_on_a_side_stream_and_repeated_calls_are_bit_identical(n):
     assert torch.equal(own[0][:2 * n], a[:2 * n])
 
 
+def test_calls_keep_no_references_and_no_memory():
+    import sys
+    dt = torch.bfloat16
+    c = Paged(dt, 128, 2, 16, [40, 9], seed=66)
+    cache, x, w = vdx.PagedKV(c.k, c.v, c.table), _rand((2, 2, 128), dt, 67), _rand((128,), dt, 68)
+    cu, text = cu_of([1, 1]), _rand((1, 50, 2, 128), dt, 69)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    grid, q_out, out = (50, 1, 1), torch.empty_like(x), torch.empty_like(x)
+    kept = [c.k, c.v, c.table, c.kv_len, x, w, cu, text, none, grid, q_out, out]
+
+    def calls():
+        vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, grid, q_norm=w, k_norm=w)
+        vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, list(grid), q_out=q_out)
+        assert vdx.rope3d_append(None, x, x, cache, cu, c.kv_len, grid) is None
+        assert vdx.paged_attn(x, cache, cu, c.kv_len, out=out)[0] is out
+        assert vdx.paged_attn(x, cache, cu, c.kv_len, return_lse=False)[1] is None
+        vdx.cross_attn(text, text, text, kv_len=none)
+        with pytest.raises(vdx.VdxError):
+            vdx.paged_attn(x, cache, cu[:2], c.kv_len)
+        with pytest.raises(vdx.VdxError):
+            vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1))
+        with pytest.raises(TypeError):
+            vdx.cross_attn(text, text, text, scale="x")
+        with pytest.raises(vdx.VdxError):
+            vdx.cross_attn(text, text, text, out=text[:, :9])
+
+    calls()
+    torch.cuda.synchronize()
+    before, memory = [sys.getrefcount(t) for t in kept], torch.cuda.memory_allocated()
+    for _ in range(20):
+        calls()
+    torch.cuda.synchronize()
+    assert [sys.getrefcount(t) for t in kept] == before and torch.cuda.memory_allocated() == memory
+
+
+def test_what_the_calls_refuse_of_tensors():
+    dt = torch.bfloat16
+    c = Paged(dt, 128, 2, 16, [40, 9], seed=70)
+    cache, x, cu = vdx.PagedKV(c.k, c.v, c.table), _rand((2, 2, 128), dt, 71), cu_of([1, 1])
+    text = _rand((1, 50, 2, 128), dt, 72)
+    grad = x.clone().requires_grad_()
+    refused = [
+        lambda: vdx.paged_attn(grad, cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(x.float(), cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(x.cpu(), cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(None, cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(x[0], cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(x[..., ::2], cache, cu, c.kv_len),
+        lambda: vdx.paged_attn(x, cache, None, c.kv_len),
+        lambda: vdx.paged_attn(x, cache, cu.long(), c.kv_len),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len.cpu()),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, max_q=-1),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, max_kv=2 ** 31),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, out=x),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, lse=torch.empty(2, 2, device="cuda", dtype=torch.float64)),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, lse=torch.empty(3, 2, device="cuda")),
+        lambda: vdx.paged_attn(x, cache, cu, c.kv_len, workspace=torch.empty(64)),
+        lambda: vdx.paged_attn(x, vdx.PagedKV(c.k, c.v[:1], c.table), cu, c.kv_len),
+        lambda: vdx.paged_attn(x, vdx.PagedKV(c.k, c.v.half(), c.table), cu, c.kv_len),
+        lambda: vdx.paged_attn(x, vdx.PagedKV(c.k, c.v, c.table.long()), cu, c.kv_len),
+        lambda: vdx.paged_attn(x, vdx.PagedKV(c.k, c.v, c.table[0]), cu, c.kv_len),
+        lambda: vdx.paged_attn_workspace_bytes(x, vdx.PagedKV(c.k, c.v, None), cu, c.kv_len),
+        lambda: vdx.rope3d_append(x, x, x[:1], cache, cu, c.kv_len, (50, 1, 1)),
+        lambda: vdx.rope3d_append(x[:1], x, x, cache, cu, c.kv_len, (50, 1, 1)),
+        lambda: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1, 1), q_norm=x[0, 0, :64]),
+        lambda: vdx.rope3d_append(None, x, x, cache, cu, c.kv_len, (50, 1, 1), q_out=x),
+        lambda: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1, 1), q_out=torch.empty_like(x)[:1]),
+        lambda: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, -1, 1)),
+        lambda: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1, 1), sections=(0, 0)),
+        lambda: vdx.cross_attn(text, text[..., :64], text[..., :64]),
+        lambda: vdx.cross_attn(text, text, text[:, :9]),
+        lambda: vdx.cross_attn(text.double(), text.double(), text.double()),
+        lambda: vdx.cross_attn(text.to_sparse(), text, text),
+        lambda: vdx.cross_attn_workspace_bytes(text, text, text.half()),
+    ]
+    for i, f in enumerate(refused):
+        with pytest.raises(vdx.VdxError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    with torch.no_grad():
+        vdx.paged_attn(grad, cache, cu, c.kv_len)
+
+
 def test_cache_offsets_past_32_bits():
     # pages far enough apart that element offsets pass 2^31
     page, H, d = 1024, 8, 128

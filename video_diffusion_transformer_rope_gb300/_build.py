@@ -1,4 +1,5 @@
-"""Build libvdx.so in-tree with nvcc for sm_103a (GB300).
+"""Build libvdx.so in-tree with nvcc for sm_103a (GB300), and with the host compiler the Python entry of
+the streaming calls (_streaming_py.so, where PyTorch is installed).
 
 Each .cu file is compiled to an object in parallel, then linked into one shared library with
 the CUDA runtime linked statically (so the library loads on machines without the NVIDIA driver;
@@ -6,10 +7,13 @@ libcuda is reached only when a call is made).  Run `python -m
 video_diffusion_transformer_rope_gb300._build` or call build().
 """
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvdx.so")
 SOURCES = ["vdx_capi.cu", "attn_fwd_sm103.cu", "attn_fwd_f32.cu", "vdx_noalloc.cu", "kv_capi.cu",
            "kv_append.cu", "attn_rows.cu", "attn_tiles_sm103.cu"]
+EXT = os.path.join(PKG, "_streaming_py.so")
+EXT_STAMP = os.path.join(OUT_DIR, "streaming_py.torch")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,15 +42,50 @@ def _deps():
     return files
 
 
+def _torch():
+    """PyTorch's folder and version, without importing it; None where it is not installed."""
+    spec = importlib.util.find_spec("torch")
+    return (os.path.dirname(spec.origin), importlib.metadata.version("torch")) if spec else None
+
+
+def _ext_stale(torch):
+    """The Python entry is bound to the interpreter and the PyTorch that it was compiled against."""
+    if torch is None:
+        return False
+    if not os.path.exists(EXT) or not os.path.exists(EXT_STAMP):
+        return True
+    return open(EXT_STAMP).read() != f"{torch[1]} {sys.version}"
+
+
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or _ext_stale(_torch()):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
+def _build_ext(torch):
+    base, version = torch
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("g++ not found: a C++ compiler is required to build the Python entry of the streaming calls")
+    include = [INCLUDE, base + "/include", base + "/include/torch/csrc/api/include", sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *("-I" + i for i in include),
+           os.path.join(CSRC, "streaming_py.cpp"), "-o", EXT + ".tmp", "-L" + base + "/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on streaming_py.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(EXT + ".tmp", EXT)
+    with open(EXT_STAMP, "w") as f:
+        f.write(f"{version} {sys.version}")
+    return EXT
+
+
 def build(force=False, verbose=False):
-    """Compile and link libvdx.so if any source is newer than it.  Returns the library path."""
+    """Compile and link libvdx.so, and the Python entry of the streaming calls, if any source is newer.
+    Returns the library path."""
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()
@@ -60,8 +101,12 @@ def build(force=False, verbose=False):
             f.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch = _torch()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_build_ext, torch) if torch else None
         objs = list(ex.map(compile_one, SOURCES))
+        if ext:
+            ext.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
