@@ -702,6 +702,22 @@ def test_what_the_calls_refuse_of_tensors():
         vdx.paged_attn(grad, cache, cu, c.kv_len)
 
 
+def test_a_row_of_nan_is_its_own_answer_only():
+    # in each kernel: few rows, few rows over a long cache (joined), many rows
+    dt = torch.float16
+    for rows, keys, bad in ((3, 50, 1), (2, 9000, 0), (300, 400, 170)):
+        q, k = _rand((1, rows, 2, 64), dt, 73), _rand((1, keys, 2, 64), dt, 74)
+        # (the rows of a warp raise their running maxima together, by up to 2^8 late, so the other rows' last bits
+        # may depend on this one; the bounds against the formula cover that)
+        ref = attend(q[0], k[0], k[0], limits(rows, keys, 0))
+        q2 = q.clone()
+        q2[0, bad, 1, 5] = float("nan")
+        got, gl = vdx.cross_attn(q2, k, k)
+        assert bool(got[0, bad, 1].isnan().all()) and bool(gl[0, 1, bad].isnan())
+        got[0, bad, 1], gl[0, 1, bad] = ref[0][bad, 1].to(dt), ref[1][1, bad].float()
+        check_attention(got[0], gl[0], ref, dt, str(rows))
+
+
 def test_cache_offsets_past_32_bits():
     # pages far enough apart that element offsets pass 2^31
     page, H, d = 1024, 8, 128

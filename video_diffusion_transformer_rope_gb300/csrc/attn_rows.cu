@@ -326,13 +326,14 @@ attn_rows(const __grid_constant__ KvParams p) {
   auto store = [&](int r, int dq, float mx, float lt, const float4& acc) {
     const long long R = first_row + r;
     const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
-    const float inv = mx == -INFINITY ? 0.f : 1.f / lt;
+    const bool none = mx == -INFINITY && lt == lt;                  // no key seen; a NaN sum is an answer
+    const float inv = none ? 0.f : 1.f / lt;
     uint2 w2;
     w2.x = pack2<T>(acc.x * inv, acc.y * inv);
     w2.y = pack2<T>(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D + dq) = w2;
     if (dq == 0 && p.lse)
-      p.lse[lse_index(p, s, sq, h, tok)] = mx == -INFINITY ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
+      p.lse[lse_index(p, s, sq, h, tok)] = none ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
   };
   for (int i = threadIdx.x; i < live * (D / 4); i += kWarps * 32) {
     const int r = i / (D / 4), dq = (i % (D / 4)) * 4;
