@@ -10,7 +10,8 @@
 // Bound: DRAM (each element is read once and written once; ~10 flops).  A block takes kTok
 // tokens.  The cosines and sines of a token are shared by all its heads, so the block's threads
 // first work them out once per (token, pair) into shared memory, with the token's destination;
-// then the (token, head) rows are walked by groups of d/8 lanes, kUnroll rows in flight per lane.
+// then the (token, head) rows are walked by groups of d/8 lanes, kUnroll rows in flight per lane (5.0 to 6.2 TB/s
+// of reads and writes: 21600 tokens of 3 x 40 heads, 1.33 GB, 215 us).
 //
 // Angles: a double product loses nothing here but FP64 units are scarce; instead the turn per
 // position, omega / 2 pi mod 1, is a 64-bit fixed-point fraction, so pos * turn mod 2^64 is the
@@ -24,8 +25,13 @@
 namespace vdx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kThreads = 128;
+// Rows that each group has in flight in a block of kTok tokens.  Small blocks and few rows in flight waste
+// little where the heads do not divide by a batch of rows, and leave registers for more blocks: 3 rows of
+// 128 threads and 4 tokens a block take 14.0 us for 3120 tokens of 3 x 12 heads and 215 us for 21600 of
+// 3 x 40; 4 rows of 256 threads and 8 tokens 17.5 and 220 us; 8 rows 24 and 303 us.
+template <int kTok>
+constexpr int kRowsInFlight = kTok > 2 ? 3 : 1;
 
 // The (token, head) rows of one tensor of a block's tokens, walked by groups of d/8 lanes, kUnroll
 // loads in flight per lane.  One instance per kind (0 q, 1 k, 2 v), so a row carries no choices: with
@@ -33,6 +39,7 @@ constexpr int kUnroll = 4;
 // takes (281 against 240 us for 21600 tokens of 3 x 40 heads).
 template <typename T, int D, int kTok, int kKind>
 struct RowWalk {
+  static constexpr int kUnroll = kRowsInFlight<kTok>;
   const T* src;
   T* dst;                      // base of q_out or the cache
   long long src_row, src_head, dst_head, dst_row;
@@ -70,7 +77,7 @@ struct RowWalk {
       tok[e] = j < rows ? j : -1;
       head[e] = h;
       x[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < rows) x[e] = __ldcs(reinterpret_cast<const uint4*>(src + j * src_row + h * src_head));
+      if (j < rows) x[e] = __ldcg(reinterpret_cast<const uint4*>(src + j * src_row + h * src_head));
       h += step;
       wrap();
     }
@@ -113,7 +120,7 @@ struct RowWalk {
       }
       if (tok[e] < 0 || at[t] < 0) continue;
       T* to = dst + (kKind == 0 ? t * dst_row : at[t]) + head[e] * dst_head;
-      *reinterpret_cast<uint4*>(to) = y;
+      *reinterpret_cast<uint4*>(to) = y;      // the next call reads it: no streaming hint
     }
   }
 };
@@ -202,8 +209,9 @@ template <typename T, int D, int kTok>
 cudaError_t launch_tok(const AppendParams& p, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
   const int heads = p.Hq > p.Hkv ? p.Hq : p.Hkv;
-  // Few tokens: split the heads over blocks too, until the device is covered or a block's
-  // groups have one row each.
+  // Few tokens: split the heads over blocks too, until the device is covered (four blocks to a
+  // multiprocessor; with twice that 700 tokens of 12 heads take 10.8 us, not 8.3) or a block's groups have
+  // one row each.
   const int blocks = (p.rows - 1) / kTok + 1;
   int ny = 1;
   const int most = (kTok * heads + kGroups - 1) / kGroups;
@@ -214,9 +222,9 @@ cudaError_t launch_tok(const AppendParams& p, cudaStream_t stream) {
 }
 template <typename T, int D>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-  // 8 tokens share a block's look-ups; a handful of tokens is spread wider (8 tokens of 12 heads: 5.3 against
-  // 5.8 us; 3120 of them: 30.9 against 18.3 us, 16 to a block 23.1 us).
-  return p.rows >= 256 ? launch_tok<T, D, 8>(p, stream) : launch_tok<T, D, 2>(p, stream);
+  // 4 tokens share a block's look-ups; few tokens are spread wider (12 heads, 2 and 4 to a
+  // block: 128 tokens 4.2 and 5.2 us, 400 5.2 and 6.4, 600 5.7 each, 3120 15.4 and 13.9).
+  return p.rows >= 512 ? launch_tok<T, D, 4>(p, stream) : launch_tok<T, D, 2>(p, stream);
 }
 
 }  // namespace
