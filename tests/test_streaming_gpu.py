@@ -619,6 +619,40 @@ def test_calls_on_a_side_stream_and_repeated_calls_are_bit_identical(n):
     assert torch.equal(own[0][:2 * n], a[:2 * n])
 
 
+def test_two_threads_on_two_streams_at_once():
+    import threading
+    dt, rows, keys = torch.bfloat16, (1, 40), (9000, 700)             # joined splits; tiles
+    cases = [(_rand((1, n, 4, 128), dt, 80 + n), _rand((1, m, 4, 128), dt, 90 + n)) for n, m in zip(rows, keys)]
+    want = [vdx.cross_attn(q, k, k) for q, k in cases]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            q, k = cases[i]
+            for j in range(30):
+                if j % 3 == 2:
+                    with pytest.raises(vdx.VdxError, match="must have"):
+                        vdx.cross_attn(q, k[0], k, stream=stream)
+                got[i].append(vdx.cross_attn(q, k, k, stream=stream))
+            stream.synchronize()
+        except BaseException as e:                                     # a failed assertion must reach the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    vdx.sync_check()
+    assert not errors, errors
+    for i in range(2):
+        assert len(got[i]) == 30
+        assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
+
+
 def test_calls_keep_no_references_and_no_memory():
     import sys
     dt = torch.bfloat16

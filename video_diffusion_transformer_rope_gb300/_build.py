@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import importlib.metadata
 import importlib.util
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -48,13 +49,17 @@ def _torch():
     return (os.path.dirname(spec.origin), importlib.metadata.version("torch")) if spec else None
 
 
+def _ext_stamp(version):
+    """What the Python entry is bound to: the PyTorch and interpreter it was compiled against, the machine."""
+    return f"{version} {sys.version} {platform.machine()}"
+
+
 def _ext_stale(torch):
-    """The Python entry is bound to the interpreter and the PyTorch that it was compiled against."""
     if torch is None:
         return False
     if not os.path.exists(EXT) or not os.path.exists(EXT_STAMP):
         return True
-    return open(EXT_STAMP).read() != f"{torch[1]} {sys.version}"
+    return open(EXT_STAMP).read() != _ext_stamp(torch[1])
 
 
 def _stale():
@@ -79,7 +84,7 @@ def _build_ext(torch):
         raise RuntimeError(f"g++ failed on streaming_py.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(EXT + ".tmp", EXT)
     with open(EXT_STAMP, "w") as f:
-        f.write(f"{version} {sys.version}")
+        f.write(_ext_stamp(version))
     return EXT
 
 
