@@ -89,6 +89,7 @@ attn_rows(const __grid_constant__ KvParams p) {
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, c4 = lane & 3;
+  wait_for_earlier_work();
 
   const int z = blockIdx.x % p.nsplit;
   const int unit = blockIdx.x / p.nsplit;
@@ -394,6 +395,7 @@ attn_join(const __grid_constant__ KvParams p) {
   constexpr int kVals = D / 32;
   __shared__ float s_m[8], s_l[8], s_o[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
+  wait_for_earlier_work();
   const unsigned unit = blockIdx.x, sh = unit / p.nblk;               // a block stays within one unit
   const int r = blockIdx.y * (8 / kPer) + warp / kPer;
   const int hk = static_cast<int>(sh % p.Hkv), s = static_cast<int>(sh / p.Hkv);
@@ -492,13 +494,14 @@ cudaError_t launch_nt(const KvParams& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.cluster ? static_cast<unsigned>(p.nsplit) : 1u;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1] = launch_early();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, attn_rows<T, D, kNT>, p);
 }
 template <typename T, int D>
@@ -511,11 +514,14 @@ template <typename T, int D>
 cudaError_t join(const KvParams& p, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk;
   if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (p.rows_kernel)
-    attn_join<T, D, 8><<<dim3(static_cast<unsigned>(units), p.block_rows), 256, 0, stream>>>(p);
-  else
-    attn_join<T, D, 1><<<dim3(static_cast<unsigned>(units), (p.block_rows + 7) / 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units), p.rows_kernel ? p.block_rows : (p.block_rows + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = launch_early();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return p.rows_kernel ? cudaLaunchKernelEx(&cfg, attn_join<T, D, 8>, p) : cudaLaunchKernelEx(&cfg, attn_join<T, D, 1>, p);
 }
 
 }  // namespace

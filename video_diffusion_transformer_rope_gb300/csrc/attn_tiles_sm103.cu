@@ -459,6 +459,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   __syncthreads();
   cluster_sync_all();                 // both CTAs' barriers exist before any remote arrival
   tc_fence_after_sync();
+  wait_for_earlier_work();
   const uint32_t tmem = ctl->tmem_base;
   const uint32_t sCtl = smem_addr(ctl);
   const TileGeom<kPaged> geom(p);
@@ -1081,13 +1082,14 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1] = launch_early();
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, mkb, mvb, mo, p, static_cast<int>(units), units > sms / 2 ? 1 : 0);
 }
 

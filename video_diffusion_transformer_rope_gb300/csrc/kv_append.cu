@@ -194,6 +194,7 @@ template <typename T, int D, int kTok>
 __global__ void __launch_bounds__(kThreads)
 kv_append(const __grid_constant__ AppendParams p) {
   const int row0 = blockIdx.x * kTok;
+  wait_for_earlier_work();
   // One tensor per block, q, k and v side by side (gridDim.z = 3): walked one after another they would
   // wait for memory three times over.  What a row reads depends on its number alone, so the first batch
   // is under way before the block has looked up its tokens' sequences and pages.
@@ -217,8 +218,14 @@ cudaError_t launch_tok(const AppendParams& p, cudaStream_t stream) {
   const int most = (kTok * heads + kGroups - 1) / kGroups;
   while (ny < most && static_cast<long long>(blocks) * ny * 3 < 608) ny *= 2;
   if (ny > most) ny = most;
-  kv_append<T, D, kTok><<<dim3(blocks, ny, p.Hq > 0 ? 3 : 2), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, ny, p.Hq > 0 ? 3 : 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = launch_early();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_append<T, D, kTok>, p);
 }
 template <typename T, int D>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
