@@ -236,6 +236,20 @@ def test_structures_match_the_header(tmp_path):
         assert names == [f[0] for f in st._fields_]
 
 
+def test_the_compiled_entry_is_bound_to_its_torch(L, monkeypatch):
+    import torch
+    from video_diffusion_transformer_rope_gb300 import streaming
+    t = torch.zeros(1, 16, 1, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(streaming, "_native", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="build them again"):
+        vdx.cross_attn(t, t, t)
+    monkeypatch.undo()
+    with pytest.raises(vdx.VdxError, match="CUDA tensor"):
+        vdx.cross_attn(t, t, t)
+    assert not _build._ext_stale(_build._torch()) and _build._ext_stale((os.path.dirname(torch.__file__), "1.0.0"))
+
+
 def test_python_refuses_host_tensors_and_gradients():
     import torch
     t = torch.zeros(1, 16, 1, 64, dtype=torch.bfloat16)
