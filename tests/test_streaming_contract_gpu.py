@@ -1,0 +1,86 @@
+"""Promises of the paged-cache and cross-attention calls, on the GPU, beside the formulas that
+test_streaming_gpu.py checks: order in a stream, what is reported, and what is left alone."""
+import math
+
+import pytest
+import torch
+
+import video_diffusion_transformer_rope_gb300 as vdx
+from streaming_ref import (SECTIONS, Paged, attend, check_attention, cu_of, limits, rotate, rotate_bound)  # noqa: F401
+from test_streaming_gpu import _built, _rand  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------ order in a stream
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_bare_chain_of_calls_reads_what_the_call_before_wrote(n):
+    # append and attention alternate over the same q, cache and scratch with nothing between them and no
+    # synchronisation; the same steps one at a time are the reference
+    dt, H, d, page, S, steps = torch.bfloat16, 4, 128, 16, 3, 150
+    first = 64 if n == 1 else 0
+    width = -(-(first + n * steps) // page)
+    xs = _rand((steps, S * n, 3 * H, d), dt, 100)
+    lens = (first + n * torch.arange(1, steps + 1, device="cuda", dtype=torch.int32))[:, None].expand(-1, S).contiguous()
+    cu, grid = cu_of([n] * S), (first + n * steps, 1, 1)
+    results = []
+    for alone in (True, False):
+        k, v = (torch.zeros(S * width, page, H, d, dtype=dt, device="cuda") for _ in range(2))
+        cache = vdx.PagedKV(k, v, torch.arange(S * width, dtype=torch.int32, device="cuda").view(S, width))
+        q = torch.zeros(S * n, H, d, dtype=dt, device="cuda")
+        outs = torch.zeros(steps, S * n, H, d, dtype=dt, device="cuda")
+        lse = torch.zeros(steps, H, S * n, device="cuda")
+        top = first + n * steps
+        ws = torch.empty(vdx.paged_attn_workspace_bytes(q, cache, cu, lens[0], n, top) + 16, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            x = xs[i]
+            vdx.rope3d_append(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], cache, cu, lens[i], grid, q_out=q)
+            if alone:
+                torch.cuda.synchronize()
+            vdx.paged_attn(q, cache, cu, lens[i], max_q=n, max_kv=top, causal_block=1, out=outs[i], lse=lse[i], workspace=ws)
+            if alone:
+                torch.cuda.synchronize()
+        vdx.sync_check()
+        results.append((outs, lse, k, v))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_calls_right_behind_kernels_that_rewrite_their_inputs(n):
+    # lengths, page table, rows, norm weights and queries are overwritten by kernels queued just ahead of each call
+    dt, H, d, page, S, steps = torch.bfloat16, 4, 128, 16, 4, 100
+    width = 24
+    g = torch.Generator(device="cuda").manual_seed(101)
+    xs = _rand((2, S * n, 3 * H, d), dt, 102)
+    weights = _rand((2, d), dt, 103)
+    lens = torch.tensor([[60, 300, 41, 384], [384, 40, 200, 77]], dtype=torch.int32, device="cuda")
+    cus = torch.stack([cu_of([n] * S), cu_of([n - 1, n, n, n])])
+    tables = torch.stack([torch.randperm(S * width, generator=g, device="cuda").int().view(S, width) for _ in range(2)])
+    k0, v0 = _rand((S * width, page, H, d), dt, 104), _rand((S * width, page, H, d), dt, 105)
+    grid = (400, 1, 1)
+    results = []
+    for alone in (True, False):
+        x, w, kv_len, cu, table = (torch.empty_like(t[0]) for t in (xs, weights, lens, cus, tables))
+        k, v = k0.clone(), v0.clone()
+        cache = vdx.PagedKV(k, v, table)
+        outs = torch.zeros(steps, S * n, H, d, dtype=dt, device="cuda")
+        rot = torch.zeros(steps, S * n, H, d, dtype=dt, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for t, src in ((x, xs), (w, weights), (kv_len, lens), (cu, cus), (table, tables)):
+                torch.add(src[i & 1], 0, out=t)
+            if alone:
+                torch.cuda.synchronize()
+            vdx.rope3d_append(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], cache, cu, kv_len, grid, q_norm=w, k_norm=w, q_out=rot[i])
+            torch.add(lens[(i + 1) & 1], 0, out=kv_len)             # attention over other lengths than were appended to
+            if alone:
+                torch.cuda.synchronize()
+            vdx.paged_attn(rot[i], cache, cu, kv_len, max_q=n, max_kv=384, out=outs[i])
+            if alone:
+                torch.cuda.synchronize()
+        vdx.sync_check()
+        results.append((rot, outs, k, v))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

@@ -125,8 +125,8 @@ attn_rows(const __grid_constant__ KvParams p) {
     }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      qf[nt][ks][0] = src ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 2 * c4)) : 0u;
-      qf[nt][ks][1] = src ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + 2 * c4)) : 0u;
+      qf[nt][ks][0] = src ? load_b32(src + ks * 16 + 2 * c4) : 0u;
+      qf[nt][ks][1] = src ? load_b32(src + ks * 16 + 8 + 2 * c4) : 0u;
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -169,8 +169,8 @@ attn_rows(const __grid_constant__ KvParams p) {
   int e0 = s, e1 = s;
   auto fetch_pages = [&](int key) {
     if (table) {
-      e0 = key < hi ? __ldg(table + pg) : 0;
-      e1 = (off + kKeys > p.P && key + (p.P - off) < hi) ? __ldg(table + pg + 1) : 0;
+      e0 = key < hi ? load_i32(table + pg) : 0;
+      e1 = (off + kKeys > p.P && key + (p.P - off) < hi) ? load_i32(table + pg + 1) : 0;
       if (static_cast<unsigned>(e0) >= static_cast<unsigned>(p.num_pages) ||
           static_cast<unsigned>(e1) >= static_cast<unsigned>(p.num_pages)) {
         if (lane == 0) atomicOr(&g_error_word, kErrPage);

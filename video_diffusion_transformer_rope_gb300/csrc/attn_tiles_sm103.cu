@@ -510,7 +510,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 tok -= p.P;
                 ++e;
               }
-            page = __ldg(table + e);
+            page = load_i32(table + e);
           }
         };
         look_up(c);

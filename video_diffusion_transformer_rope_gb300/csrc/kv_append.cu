@@ -45,6 +45,7 @@ struct RowWalk {
   long long src_row, src_head, dst_head, dst_row;
   int heads, step, rows;
   int j, h;                    // token and head of the next row
+  uint4 weights;               // this lane's 8 of the norm's, if there is one
   uint4 x[kUnroll];
   int tok[kUnroll], head[kUnroll];      // tok < 0: past the block's rows
   __device__ __forceinline__ void init(const AppendParams& p, int row0) {
@@ -57,6 +58,9 @@ struct RowWalk {
     src_head = kKind == 0 ? p.q_head : (kKind == 1 ? p.k_head : p.v_head);
     dst_head = kKind == 0 ? p.q_out_head : (kKind == 1 ? p.kc_head : p.vc_head);
     dst_row = p.q_out_row;
+    const void* norm = kKind == 0 ? p.q_norm : p.k_norm;
+    weights = make_uint4(0u, 0u, 0u, 0u);
+    if (kKind < 2 && norm) weights = load_b128(static_cast<const T*>(norm) + lane * 8);
     src += row0 * src_row;
     if (kKind == 0) dst += row0 * dst_row;
     rows = heads > 0 ? min(kTok, p.rows - row0) : 0;
@@ -77,7 +81,7 @@ struct RowWalk {
       tok[e] = j < rows ? j : -1;
       head[e] = h;
       x[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < rows) x[e] = __ldcg(reinterpret_cast<const uint4*>(src + j * src_row + h * src_head));
+      if (j < rows) x[e] = load_b128(src + j * src_row + h * src_head);
       h += step;
       wrap();
     }
@@ -86,10 +90,10 @@ struct RowWalk {
   // take every lane.
   __device__ __forceinline__ bool more() const { return __any_sync(0xffffffffu, tok[0] >= 0); }
   // at[t]: where token t goes (an offset in the cache; q: a grid token), negative: nowhere.
-  __device__ __forceinline__ void finish(const AppendParams& p, const float2 (*cs)[D / 2], const long long* at, const void* norm) {
+  __device__ __forceinline__ void finish(const AppendParams& p, const float2 (*cs)[D / 2], const long long* at, bool norm) {
     const int lane = threadIdx.x % (D / 8);
     float w[8];
-    if (kKind < 2) load8<T>(norm, lane, w);
+    if (kKind < 2) unpack8<T>(weights, w);
 #pragma unroll
     for (int e = 0; e < kUnroll; ++e) {
       uint4 y = x[e];
@@ -141,10 +145,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
     int frame = 0, row = 0, col = 0;
     if (r < p.rows) {
       const int s = find_sequence(p.cu, p.S, r);
-      const int begin = __ldg(p.cu + s), end = __ldg(p.cu + s + 1);
+      const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
       if (r >= begin && r < end) {
-        const long long c = static_cast<long long>(__ldg(p.kv_len + s)) - (end - begin) + (r - begin);
-        const long long pos = c + (p.pos_offset ? __ldg(p.pos_offset + s) : 0);
+        const long long c = static_cast<long long>(load_i32(p.kv_len + s)) - (end - begin) + (r - begin);
+        const long long pos = c + (p.pos_offset ? load_i32(p.pos_offset + s) : 0);
         if (c < 0 || c >= static_cast<long long>(p.max_pages) * p.P || pos < 0 ||
             pos >= static_cast<long long>(p.T) * p.Hg * p.Wg) {
           if ((tid & 31) == 0) atomicOr(&g_error_word, kErrPosition);
@@ -159,7 +163,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
         if (kKind != 0 && at >= 0) {
           at = -1;
           const int pg = static_cast<int>(c / p.P), slot = static_cast<int>(c - static_cast<long long>(pg) * p.P);
-          const int page = __ldg(p.table + s * p.table_stride + pg);
+          const int page = load_i32(p.table + s * p.table_stride + pg);
           if (page < 0 || page >= p.num_pages) {
             if ((tid & 31) == 0) atomicOr(&g_error_word, kErrPage);
           } else {
@@ -187,11 +191,11 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
     }
     __syncthreads();
   }
-  for (; rows.more(); rows.load()) rows.finish(p, cs, s_at, kKind == 0 ? p.q_norm : p.k_norm);
+  for (; rows.more(); rows.load()) rows.finish(p, cs, s_at, (kKind == 0 ? p.q_norm : p.k_norm) != nullptr);
 }
 
 template <typename T, int D, int kTok>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 9)
 kv_append(const __grid_constant__ AppendParams p) {
   const int row0 = blockIdx.x * kTok;
   wait_for_earlier_work();

@@ -50,27 +50,37 @@ template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
 }
-// Chunk `lane` of 8 weights as floats (ones without weights).
-template <typename T>
-__device__ __forceinline__ void load8(const void* w, int lane, float (&f)[8]) {
-  if (w) {
-    unpack8<T>(__ldg(static_cast<const uint4*>(w) + lane), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-  }
+
+// Loads of what the work just ahead in the stream may have written (lengths, page tables, rows, weights):
+// coherent, through L2, and in order with wait_for_earlier_work(), since both are volatile.  The
+// read-only path (ld.global.nc) is for memory that nobody writes while the kernel runs, and a kernel
+// that starts early is running while the work before it still writes.
+__device__ __forceinline__ int load_i32(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_b32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_b128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
 // The last s in [0, S) with cu[s] <= r (0 if none), found by the whole warp: each step its lanes
 // probe 32 evenly spaced starts, so up to 32 sequences take one load.  With cu not decreasing it
 // is the sequence that owns row r, if any does; the caller checks cu[s] <= r < cu[s + 1].
-__device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int S, int r) {
+__device__ __forceinline__ int find_sequence(const int* cu, int S, int r) {
   int lo = 0, n = S;                      // the answer is in [lo, lo + n)
   const int lane = threadIdx.x & 31;
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int off = lane * step;
-    const bool le = off < n && __ldg(cu + lo + off) <= r;
+    const bool le = off < n && load_i32(cu + lo + off) <= r;
     // the highest probe at or below r; probes past a decreasing cu only make the result wrong,
     // not out of range
     const unsigned m = __ballot_sync(0xffffffffu, le);
@@ -91,7 +101,7 @@ __device__ __forceinline__ SeqInfo sequence_info(const KvParams& p, int s, bool 
   SeqInfo q;
   bool bad = false;
   if (p.cu) {
-    int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
+    int a = load_i32(p.cu + s), b = load_i32(p.cu + s + 1);
     bad = a < 0 || b < a || b > p.N;
     a = min(max(a, 0), p.N);
     b = min(max(b, a), p.N);
@@ -103,7 +113,7 @@ __device__ __forceinline__ SeqInfo sequence_info(const KvParams& p, int s, bool 
     q.n = p.N;
   }
   if (p.kv_len) {
-    const int len = __ldg(p.kv_len + s);
+    const int len = load_i32(p.kv_len + s);
     q.len = min(max(len, 0), p.max_kv);
     bad = bad || len != q.len;
   } else {
