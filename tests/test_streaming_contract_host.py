@@ -24,3 +24,13 @@ def test_kernels_that_start_early_read_through_the_coherent_path(name):
     # (also one that the compiler may choose, given const __restrict__) need not see them after the wait
     text = _source(name)
     assert not re.findall(r"__ldg|ld\.global\.nc|__restrict__|ld_nc", text)
+
+
+def test_arrivals_released_to_the_cluster_are_waited_for_at_cluster_scope():
+    # a barrier on which the other CTA arrives with a cluster-scope release (it announces plain stores or reads)
+    # has a wait whose acquire has that scope too; one of CTA scope does not pair with it
+    text = _source("attn_tiles_sm103.cu")
+    bars = set(re.findall(r"mbar_arrive_remote_cluster\((?:mapa_shared\(sCtl \+|remote \+) (kBar\w+)", text))
+    assert bars == {"kBarVFull", "kBarClaimReady"}
+    for bar in bars:
+        assert re.search(r"warp_wait<true>\(sCtl \+ %s\b" % bar, text), bar

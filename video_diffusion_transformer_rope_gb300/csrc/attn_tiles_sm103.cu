@@ -118,14 +118,29 @@ __device__ __forceinline__ void report_timeout(int site) {
   if ((atomicOr(&g_error_word, 1u) & 1u) == 0) atomicOr(&g_error_word, static_cast<unsigned>(site & 0xff) << 8);
 }
 
+// mbar_try_wait that pairs with another CTA's cluster-scope release: what that CTA wrote by plain stores (or
+// read) before it arrived lies before what follows here.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The rest of a warp's wait for a barrier phase whose first look (mbar_try_wait, which itself blocks for
 // a while) failed.  Kept out of line: a dozen inlined copies would spread the roles' loops over so
 // much code that they miss the instruction caches.  The warp gives up as one, when the CTA's abort
 // flag is raised or after kWaitLimitNs, and then raises the flag and records the site.
+template <bool kCluster>
 __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
   const unsigned long long t0 = global_timer_ns();
   while (true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, ld_shared_flag(abort_flag) != 0)) return false;
     if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) {
       st_shared_flag(abort_flag);
@@ -134,9 +149,12 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t a
     }
   }
 }
+// kCluster: for what the other CTA did by plain accesses.  Waits for copies, products and tensor memory need
+// CTA scope only (the copies' bytes, the commits and the tcgen05 fences order those).
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return wait_more(bar, parity, abort_flag, site);
+  if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+  return wait_more<kCluster>(bar, parity, abort_flag, site);
 }
 // The softmax warps' form: their registers are past what a function call leaves room for.
 __device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
@@ -634,7 +652,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             mma_commit_pair_warp(sCtl + kBarKEmpty + 8 * st);
           }
           ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
-          if (end && tail < kBN) zero_v_rows<D>(vt, tail, lane);
+          if (end && tail < kBN) {
+            // rank 1 zeroed rows of its half before it arrived: seen at cluster scope (the phase is complete,
+            // so this returns at once)
+            if (ok) ok = warp_wait<true>(sCtl + kBarVFull + 8 * st, ph, sCtl + kOffAbort, kSiteVFull);
+            zero_v_rows<D>(vt, tail, lane);
+          }
           // the next tile's keys are waited for here, so that its product follows this one's without a
           // wait in between
           const int st_was = st;
@@ -766,7 +789,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         __syncwarp();
         if (leader) {
-          if (!(ok = wait(sCtl + kBarClaimReady, claims, kSiteClaim))) break;
+          // the other CTA's read of the last answer lies before the next one is asked for
+          if (!(ok = warp_wait<true>(sCtl + kBarClaimReady, claims & 1, sCtl + kOffAbort, kSiteClaim))) break;
           if (lane == 0) claim_cluster(sCtl + kOffClaim, sCtl + kBarClaimFull);
           __syncwarp();
         }
