@@ -242,7 +242,8 @@ typedef struct vdx_paged_kv {
  * fp32 arithmetic, angles reduced exactly, one rounding at the end; v is copied bit for bit.
  * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place),
  * also inside a fused projection; otherwise the outputs must not overlap an input, nor each other.  A token outside the grid's T*Hgrid*Wgrid
- * positions, or with a cache index below 0 or past its page table, is skipped and reported.
+ * positions, or with a cache index below 0 or past its page table, is skipped and reported; so are the
+ * tokens of a sequence whose range in cu is no range of the call's rows.
  * Two rows of one call that land in the same cache slot leave one of them there. */
 typedef struct vdx_append_args {
   const void* q;            /* [rows, Hq, d] or NULL                                              */

@@ -84,3 +84,34 @@ def test_calls_right_behind_kernels_that_rewrite_their_inputs(n):
         results.append((rot, outs, k, v))
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------------ append: what is reported
+@pytest.mark.parametrize("rows", [8, 600])
+@pytest.mark.parametrize("bad", ["past the rows", "negative", "decreasing", "decreasing behind the rows"])
+def test_append_reports_ranges_that_are_none(rows, bad):
+    dt, H, d = torch.bfloat16, 2, 64
+    lens = [rows + 20, rows + 20]
+    cu = {"past the rows": [0, rows + 2, rows + 2], "negative": [-2, rows // 2, rows // 2],
+          "decreasing": [0, rows, rows // 2], "decreasing behind the rows": [0, 0, -1]}[bad]
+    # the first sequence of "decreasing" has a good range: its tokens go where they belong
+    good = rows if bad == "decreasing" else 0
+    c = Paged(dt, d, H, 16, lens, seed=110)
+    k0, v0 = c.k.clone(), c.v.clone()
+    q, k, v = (_rand((rows, H, d), dt, 111 + i) for i in range(3))
+    out = torch.full_like(q, 5.0)
+    cache, grid = vdx.PagedKV(c.k, c.v, c.table), (2000, 1, 1)
+    vdx.rope3d_append(q, k, v, cache, torch.tensor(cu, dtype=torch.int32, device="cuda"), c.kv_len, grid, q_out=out)
+    with pytest.raises(vdx.VdxError, match="cu or kv_len broke a bound"):
+        vdx.sync_check()
+    assert bool((out[good:] == 5.0).all())
+    written = torch.zeros(c.k.shape[:2], dtype=torch.bool, device="cuda")
+    pos = torch.arange(20, 20 + good, device="cuda")
+    if good:
+        written[c.slots(0, pos)] = True
+        assert torch.equal(c.v[c.slots(0, pos)], v)
+    for now, was in ((c.k, k0), (c.v, v0)):
+        assert torch.equal(now[~written].view(torch.int16), was[~written].view(torch.int16))
+    # rows behind the last sequence are no mistake
+    vdx.rope3d_append(q, k, v, cache, cu_of([3, 2]), c.kv_len, grid, q_out=out)
+    vdx.sync_check()

@@ -146,7 +146,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
     if (r < p.rows) {
       const int s = find_sequence(p.cu, p.S, r);
       const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
-      if (r >= begin && r < end) {
+      if (begin < 0 || end < begin || end > p.rows) {
+        // n would count rows that are not there, and the tokens would land on those before them
+        if ((tid & 31) == 0) atomicOr(&g_error_word, kErrLength);
+      } else if (r >= begin && r < end) {
         const long long c = static_cast<long long>(load_i32(p.kv_len + s)) - (end - begin) + (r - begin);
         const long long pos = c + (p.pos_offset ? load_i32(p.pos_offset + s) : 0);
         if (c < 0 || c >= static_cast<long long>(p.max_pages) * p.P || pos < 0 ||
@@ -178,6 +181,15 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
       s_axis[j][1] = row;
       s_axis[j][2] = col;
     }
+  }
+  // One warp of the call looks at every sequence's range (a row's look-up sees only its own).
+  if (kKind == 1 && blockIdx.x == 0 && blockIdx.y == 0 && tid >= kThreads - 32) {
+    bool bad = false;
+    for (int s = tid & 31; s < p.S; s += 32) {
+      const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
+      bad = bad || begin < 0 || end < begin || end > p.rows;
+    }
+    if (bad) atomicOr(&g_error_word, kErrLength);
   }
   __syncthreads();
   if (kKind < 2) {

@@ -455,7 +455,7 @@ vdx_status vdx_sync_check(void* stream) {
   if (word & vdx::kErrPage)
     return fail(VDX_ERR_ARG, "a page index was outside the cache; nothing was written there, and its keys read as zeros");
   if (word & vdx::kErrLength)
-    return fail(VDX_ERR_ARG, "cu or kv_len broke a bound of its call (rows, max_q, max_kv); it was clamped");
+    return fail(VDX_ERR_ARG, "cu or kv_len broke a bound of its call (rows, max_q, max_kv); it was clamped, or its tokens not appended");
   if (word & vdx::kErrPosition)
     return fail(VDX_ERR_ARG, "an appended token was outside the position grid or its page table; it was skipped");
   return VDX_OK;
