@@ -34,3 +34,29 @@ def test_arrivals_released_to_the_cluster_are_waited_for_at_cluster_scope():
     assert bars == {"kBarVFull", "kBarClaimReady"}
     for bar in bars:
         assert re.search(r"warp_wait<true>\(sCtl \+ %s\b" % bar, text), bar
+
+
+@pytest.mark.parametrize("ckw", [
+    dict(v=FAKE + 16),                                                         # shifted by some channels
+    dict(v=FAKE + 256),                                                        # by a head
+    dict(v=FAKE + 1024),                                                       # by a token
+    dict(v=FAKE + 16 * 1024),                                                  # by a page
+    dict(k=FAKE + 16 * 1024, v=FAKE),
+    dict(k_token=1024, k_page=16 * 1024, v_token=1024, v_page=16 * 1024, v=FAKE + 512),   # half a token's heads on
+    dict(v=FAKE + 512, Hkv=4, k_head=256, k_token=1024, k_page=16 * 1024),
+])
+def test_append_refuses_caches_that_overlap(L, ckw):
+    r = L.vdx_rope3d_append(ctypes.byref(_cache(**ckw)), ctypes.byref(_append()), None)
+    assert r == B.VDX_ERR_ARG and "caches overlap" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+@pytest.mark.parametrize("ckw", [
+    dict(v=FAKE + 1024, k_token=1024, k_page=16 * 1024, v_token=1024, v_page=16 * 1024),          # [pages, token, 2, H, d]
+    dict(v=FAKE + 256, k_head=256, k_token=1024, k_page=16 * 1024, v_head=256, v_token=1024, v_page=16 * 1024),   # [.., H, 2, d]
+    dict(v=FAKE + 16 * 1024, k_page=2 * 16 * 512, v_page=2 * 16 * 512),                           # [pages, 2, token, H, d]
+    dict(v=FAKE + 20 * 16 * 1024),                                             # one right behind the other
+])
+def test_append_takes_caches_side_by_side(L, ckw):
+    # refused only for what is checked after the caches: q and k of the call lie in the key cache
+    r = L.vdx_rope3d_append(ctypes.byref(_cache(**ckw)), ctypes.byref(_append(k=FAKE + 16)), None)
+    assert r == B.VDX_ERR_ARG and "the cache overlaps q, k, v or q_out" in L.vdx_last_error().decode(), L.vdx_last_error()

@@ -424,6 +424,7 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
   if (!rows_distinct(kc)) return fail(VDX_ERR_ARG, "tokens of the key cache overlap one another");
   if (!rows_distinct(vc)) return fail(VDX_ERR_ARG, "tokens of the value cache overlap one another");
   if (c->k == c->v) return fail(VDX_ERR_ARG, "the key and value caches are the same memory");
+  if (!rows_apart(kc, vc)) return fail(VDX_ERR_ARG, "the key and value caches overlap");
   for (const Tensor* t : {&kc, &vc})
     if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
       return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
