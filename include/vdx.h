@@ -244,7 +244,8 @@ typedef struct vdx_paged_kv {
  * also inside a fused projection; otherwise the outputs must not overlap an input, nor each other.  A token outside the grid's T*Hgrid*Wgrid
  * positions, or with a cache index below 0 or past its page table, is skipped and reported; so are the
  * tokens of a sequence whose range in cu is no range of the call's rows.
- * Two rows of one call that land in the same cache slot leave one of them there. */
+ * Two rows of one call that land in the same cache slot (sequences whose tables share a page that both
+ * write) race for it: what it holds then is a mixture of the two, each 16 bytes from either. */
 typedef struct vdx_append_args {
   const void* q;            /* [rows, Hq, d] or NULL                                              */
   const void* k;            /* [rows, Hkv, d]                                                     */

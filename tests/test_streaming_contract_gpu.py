@@ -115,3 +115,29 @@ def test_append_reports_ranges_that_are_none(rows, bad):
     # rows behind the last sequence are no mistake
     vdx.rope3d_append(q, k, v, cache, cu_of([3, 2]), c.kv_len, grid, q_out=out)
     vdx.sync_check()
+
+
+@pytest.mark.parametrize("n", [8, 700])
+def test_two_rows_for_one_slot_leave_pieces_of_either(n):
+    # two sequences over the same pages at the same indices: every 16 bytes are one row's, every other slot is as it was
+    dt, H, d = torch.bfloat16, 3, 64
+    c = Paged(dt, d, H, 16, [n + 5, n + 5], seed=120)
+    c.table[1] = c.table[0]
+    before = c.k.clone(), c.v.clone()
+    k, v = (_rand((2 * n, H, d), dt, 121 + i) for i in range(2))
+    vdx.rope3d_append(None, k, v, vdx.PagedKV(c.k, c.v, c.table), cu_of([n, n]), c.kv_len, (2000, 1, 1), SECTIONS[d])
+    vdx.sync_check()
+    pos = torch.arange(5, 5 + n, device="cuda")
+    slots = c.slots(0, pos)
+    got = c.v[slots].view(n, H, d // 8, 8)
+    a, b = v[:n].view(n, H, d // 8, 8), v[n:].view(n, H, d // 8, 8)
+    assert bool(((got == a).all(-1) | (got == b).all(-1)).all())
+    errs = []
+    for x in (k[:n], k[n:]):
+        ref = rotate(x, pos, (2000, 1, 1), SECTIONS[d], 10000.0)
+        errs.append(((c.k[slots].double() - ref).abs() <= rotate_bound(ref, dt)).view(n, H, d // 8, 8).all(-1))
+    assert bool((errs[0] | errs[1]).all())
+    touched = torch.zeros(c.k.shape[:2], dtype=torch.bool, device="cuda")
+    touched[slots] = True
+    for now, was in zip((c.k, c.v), before):
+        assert torch.equal(now[~touched].view(torch.int16), was[~touched].view(torch.int16))

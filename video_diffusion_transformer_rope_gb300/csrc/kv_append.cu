@@ -124,7 +124,9 @@ struct RowWalk {
       }
       if (tok[e] < 0 || at[t] < 0) continue;
       T* to = dst + (kKind == 0 ? t * dst_row : at[t]) + head[e] * dst_head;
-      *reinterpret_cast<uint4*>(to) = y;      // the next call reads it: no streaming hint
+      // 16 bytes a lane, in no order among rows: two rows for one slot leave pieces of both.  The next call
+      // reads it: no streaming hint.
+      *reinterpret_cast<uint4*>(to) = y;
     }
   }
 };
