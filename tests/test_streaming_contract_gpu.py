@@ -141,3 +141,77 @@ def test_two_rows_for_one_slot_leave_pieces_of_either(n):
     touched[slots] = True
     for now, was in zip((c.k, c.v), before):
         assert torch.equal(now[~touched].view(torch.int16), was[~touched].view(torch.int16))
+
+
+# ------------------------------------------------------------------------- frame-causal masks and dropped pages
+def _offset_limits(n, length, block, off):
+    p = torch.arange(length - n, length, device="cuda")
+    lim = (torch.div(p + off, block, rounding_mode="floor") + 1) * block - off
+    return torch.where(p < 0, torch.zeros_like(p), lim.clamp(0, length))
+
+
+@pytest.mark.parametrize("block", [1, 7, 100, 1560, 2 ** 31 - 1])
+@pytest.mark.parametrize("news,lens,offs", [
+    ([1, 3, 2], [50, 300, 7], [0, 93, 640]),                       # the few-row kernel
+    ([1], [20000], [1111]),                                        # its splits, joined through scratch
+    ([40, 300, 0, 129], [90, 700, 5, 129], [256, 99, 13, 5]),      # tiles
+    ([200, 1], [3000, 2000], [1559, 2 ** 31 - 1]),                 # split tiles; the largest offset
+    ([5, 60], [3, 50], [3, 1600]),                                 # more rows than keys: negative indices see nothing
+])
+def test_blocks_are_counted_from_grid_token_zero(news, lens, offs, block):
+    dt, H, d, page = torch.bfloat16, 2, 64, 32
+    c = Paged(dt, d, H, page, lens, seed=130)
+    q = _rand((sum(news), H, d), dt, 131, 1.5)
+    out, lse = vdx.paged_attn(q, vdx.PagedKV(c.k, c.v, c.table), cu_of(news), c.kv_len, max_q=max(news), max_kv=max(lens),
+                              causal_block=block, pos_offset=torch.tensor(offs, dtype=torch.int32, device="cuda"))
+    vdx.sync_check()
+    at = 0
+    for s, (n, length, off) in enumerate(zip(news, lens, offs)):
+        k, v = c.get(s)
+        check_attention(out[at:at + n], lse[:, at:at + n], attend(q[at:at + n], k, v, _offset_limits(n, length, block, off)), dt,
+                        f"sequence {s}: {n} of {length}, offset {off}")
+        at += n
+
+
+def test_negative_offsets_and_no_mask():
+    # an offset below 0 (tokens that the cache keeps before the grid's first): blocks are counted downwards too
+    dt, H, d = torch.float16, 2, 64
+    c = Paged(dt, d, H, 16, [90, 200], seed=132)
+    q = _rand((42, H, d), dt, 133, 1.5)
+    cache, off = vdx.PagedKV(c.k, c.v, c.table), torch.tensor([-30, -101], dtype=torch.int32, device="cuda")
+    for block in (1, 24):
+        out, lse = vdx.paged_attn(q, cache, cu_of([2, 40]), c.kv_len, max_q=40, max_kv=200, causal_block=block, pos_offset=off)
+        for s, rows, length in ((0, slice(0, 2), 90), (1, slice(2, 42), 200)):
+            k, v = c.get(s)
+            ref = attend(q[rows], k, v, _offset_limits(rows.stop - rows.start, length, block, int(off[s])))
+            check_attention(out[rows], lse[:, rows], ref, dt)
+    a = vdx.paged_attn(q, cache, cu_of([2, 40]), c.kv_len, max_q=40, max_kv=200, pos_offset=off)
+    b = vdx.paged_attn(q, cache, cu_of([2, 40]), c.kv_len, max_q=40, max_kv=200)
+    vdx.sync_check()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_dropping_pages_inside_a_frame_changes_only_what_is_gone():
+    # pages of 16 tokens, frames of 54: the first pages leave the table, the new frame still sees whole frames
+    dt, H, d, page, frame, frames = torch.bfloat16, 2, 128, 16, 54, 4
+    grid = (frames + 1, 6, 9)
+    n, total = frame + 20, frame * frames + 20                    # the chunk: the last frame and part of the next
+    width = -(-total // page)
+    k, v = (torch.full((width, page, H, d), math.nan, dtype=dt, device="cuda") for _ in range(2))
+    x = _rand((total, 3 * H, d), dt, 134)
+    table = torch.arange(width, dtype=torch.int32, device="cuda").view(1, -1)
+    rot = vdx.rope3d_append(x[:, :H], x[:, H:2 * H], x[:, 2 * H:], vdx.PagedKV(k, v, table), cu_of([total]),
+                            torch.tensor([total], dtype=torch.int32, device="cuda"), grid, SECTIONS[d])
+    kk, vv = k.view(-1, H, d)[:total], v.view(-1, H, d)[:total]
+    for gone in (1, 5):
+        drop = gone * page
+        cache = vdx.PagedKV(k, v, table[:, gone:].contiguous())
+        lens, off = (torch.tensor([t], dtype=torch.int32, device="cuda") for t in (total - drop, drop))
+        again = vdx.rope3d_append(x[-n:, :H], x[-n:, H:2 * H], x[-n:, 2 * H:], cache, cu_of([n]), lens, grid, SECTIONS[d],
+                                  pos_offset=off)
+        assert torch.equal(again, rot[-n:])
+        out, lse = vdx.paged_attn(again, cache, cu_of([n]), lens, max_q=n, causal_block=frame, pos_offset=off)
+        vdx.sync_check()
+        p = torch.arange(total - n, total, device="cuda")
+        lim = ((torch.div(p, frame, rounding_mode="floor") + 1) * frame).clamp(max=total) - drop
+        check_attention(out, lse, attend(rot[-n:], kk[drop:], vv[drop:], lim), dt, f"{gone} pages gone")

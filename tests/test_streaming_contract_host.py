@@ -60,3 +60,8 @@ def test_append_takes_caches_side_by_side(L, ckw):
     # refused only for what is checked after the caches: q and k of the call lie in the key cache
     r = L.vdx_rope3d_append(ctypes.byref(_cache(**ckw)), ctypes.byref(_append(k=FAKE + 16)), None)
     assert r == B.VDX_ERR_ARG and "the cache overlaps q, k, v or q_out" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+def test_paged_attention_checks_its_position_offsets(L):
+    r = L.vdx_paged_attn(ctypes.byref(_cache()), ctypes.byref(_paged(pos_offset=FAKE + 9 * G + 2)), None)
+    assert r == B.VDX_ERR_ALIGN and "pos_offset" in L.vdx_last_error().decode(), L.vdx_last_error()

@@ -52,7 +52,7 @@ class PagedAttnArgs(ctypes.Structure):
     """vdx_paged_attn_args (include/vdx.h)."""
     _fields_ = [("q", _p), ("out", _p), ("lse", _p), ("q_row", _ll), ("q_head", _ll), ("rows", _i), ("Hq", _i),
                 ("cu", _p), ("kv_len", _p), ("max_q", _i), ("max_kv", _i), ("causal_block", _i), ("scale", _f),
-                ("workspace", _p), ("workspace_bytes", _z)]
+                ("workspace", _p), ("workspace_bytes", _z), ("pos_offset", _p)]
 
 
 class CrossAttnArgs(ctypes.Structure):

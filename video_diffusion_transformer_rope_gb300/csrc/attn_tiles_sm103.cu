@@ -80,9 +80,8 @@ enum : int {
 
 // One unit of work, as warp 10 hands it to the other roles.
 struct Unit {
-  int end;                 // no unit: none is left
-  int s, hk, unit, z;      // sequence, kv head, index among (sequence, head, block), split
-  int row0, n, keys;       // the sequence's first row, rows and keys (SeqInfo)
+  int s, hk, unit, z;      // sequence, kv head, index among (sequence, head, block), split; s < 0: no unit is left
+  int row0, n, keys, shift;    // the sequence's first row, rows, keys and blocks' shift (SeqInfo)
   int tok0, ntok;          // first token of the block and live tokens in it (<= 0: none)
   int len;                 // keys that its last row sees
   int t0, t1;              // key tiles of this split
@@ -252,7 +251,6 @@ struct TileCursor {
 template <bool kPaged>
 __device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom<kPaged>& g, int it, bool report) {
   Unit u;
-  u.end = 0;
   const int blk = it % p.nblk;
   int r = it / p.nblk;
   u.z = r % p.nsplit;
@@ -264,6 +262,7 @@ __device__ __forceinline__ Unit make_unit(const KvParams& p, const TileGeom<kPag
   u.row0 = sq.row0;
   u.n = sq.n;
   u.keys = sq.len;
+  u.shift = sq.shift;
   const int per = p.block_rows / p.g;
   u.tok0 = blk * per;                                    // nblk * per stays near max_q < 2^31
   u.ntok = min(per, min(sq.n, p.max_q) - u.tok0);
@@ -499,7 +498,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       UnitReader in{sCtl};
       while (ok) {
         if (!(ok = in.wait())) break;
-        if (VDX_UNIT(in, end)) {
+        if (VDX_UNIT(in, s) < 0) {
           in.release();
           break;
         }
@@ -612,7 +611,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       UnitReader in{sCtl};
       while (ok) {
         if (!(ok = in.wait())) break;
-        if (VDX_UNIT(in, end)) {
+        if (VDX_UNIT(in, s) < 0) {
           in.release();
           break;
         }
@@ -698,7 +697,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       UnitReader in{sCtl};
       while (ok) {
         if (!(ok = in.wait())) break;
-        if (VDX_UNIT(in, end)) {
+        if (VDX_UNIT(in, s) < 0) {
           in.release();
           break;
         }
@@ -745,7 +744,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         const int slot = k % kUnitSlots;
         if (k >= kUnitSlots && !(ok = wait(sCtl + kBarUnitEmpty + 8 * slot, k / kUnitSlots - 1, kSiteUnitEmpty))) break;
         Unit u;
-        u.end = 1;
+        u.s = -1;
         u.t0 = u.t1 = u.ntok = 0;
         const bool more = it < units;
         if (more) u = make_unit<kPaged>(p, geom, it, leader && lane == 0);
@@ -811,7 +810,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       UnitReader in{sCtl};
       while (ok) {
         if (!(ok = in.wait())) break;
-        if (VDX_UNIT(in, end)) {
+        if (VDX_UNIT(in, s) < 0) {
           in.release();
           break;
         }
@@ -899,7 +898,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) mbar_arrive(sCtl + kBarUnitEmpty + 8 * slot);
       };
-      if (u.end) {
+      if (u.s < 0) {
         release();
         break;
       }
@@ -911,7 +910,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         continue;
       }
       const bool live = in_tile && tok < u.ntok;
-      const int limit = !live ? 0 : (kPaged ? visible_limit(p, SeqInfo{u.row0, u.n, u.keys}, u.tok0 + tok) : u.len);
+      const int limit = !live ? 0 : (kPaged ? visible_limit(p, SeqInfo{u.row0, u.n, u.keys, u.shift}, u.tok0 + tok) : u.len);
       const bool any_live = __any_sync(0xffffffffu, live);
       // tiles below this one are whole for every live row of the warp
       const int whole_to = !kPaged ? u.len / kBN
@@ -992,7 +991,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const int h = u.hk * p.g + my_head;
       const long long prow = (static_cast<long long>(u.unit) * p.nsplit + u.z) * p.block_rows + tok * p.g + my_head;
       if (live) {
-        const SeqInfo sq{u.row0, u.n, u.keys};
+        const SeqInfo sq{u.row0, u.n, u.keys, u.shift};
         if (kSplit)
           p.part_ml[prow] = make_float2(empty ? -INFINITY : m, l);
         else if (p.lse)

@@ -233,7 +233,7 @@ vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bo
   p.q_b = 0; p.q_t = a->q_row; p.q_h = a->q_head;
   p.k_p = c->k_page; p.k_t = c->k_token; p.k_h = c->k_head;
   p.v_p = c->v_page; p.v_t = c->v_token; p.v_h = c->v_head;
-  p.cu = a->cu; p.kv_len = a->kv_len; p.table = c->page_table;
+  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->causal_block ? a->pos_offset : nullptr; p.table = c->page_table;
   p.table_stride = c->table_stride;
   p.max_pages = c->max_pages; p.num_pages = c->num_pages; p.P = c->page_size;
   p.S = c->seqs; p.N = a->rows; p.Hq = a->Hq; p.Hkv = c->Hkv; p.g = a->Hq / c->Hkv;
@@ -245,6 +245,7 @@ vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bo
   if (!q.empty()) {
     if (vdx_status s = check_i32("cu", a->cu, false)) return s;
     if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
+    if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
   }
   return finish(pb, q, cache_tensor(*c, false), cache_tensor(*c, true),
                 static_cast<long long>(a->rows) * a->Hq * c->d, a->lse ? static_cast<long long>(a->rows) * a->Hq : 0,

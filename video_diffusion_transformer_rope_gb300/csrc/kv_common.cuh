@@ -86,6 +86,7 @@ struct SeqInfo {
   int row0;   // first token in q / out
   int n;      // tokens
   int len;    // keys
+  int shift;  // tokens of its block of causal_block that lie before key 0 (dropped ones)
 };
 __device__ __forceinline__ SeqInfo sequence_info(const KvParams& p, int s, bool report) {
   SeqInfo q;
@@ -109,6 +110,11 @@ __device__ __forceinline__ SeqInfo sequence_info(const KvParams& p, int s, bool 
   } else {
     q.len = p.max_kv;
   }
+  q.shift = 0;
+  if (p.pos_offset) {
+    q.shift = load_i32(p.pos_offset + s) % p.causal_block;
+    if (q.shift < 0) q.shift += p.causal_block;
+  }
   if (bad && report) atomicOr(&g_error_word, kErrLength);
   return q;
 }
@@ -117,8 +123,9 @@ __device__ __forceinline__ int visible_limit(const KvParams& p, const SeqInfo& q
   if (p.causal_block <= 0) return q.len;
   const int pos = q.len - q.n + i;        // q.n may exceed q.len: negative positions see nothing
   if (pos < 0) return 0;
-  const long long lim = (static_cast<long long>(pos / p.causal_block) + 1) * p.causal_block;
-  return lim < q.len ? static_cast<int>(lim) : q.len;
+  // to the end of its block; pos < 2^30, shift and causal_block < 2^31
+  const unsigned in_block = (static_cast<unsigned>(pos) + q.shift) % static_cast<unsigned>(p.causal_block);
+  return static_cast<int>(min(static_cast<unsigned>(pos) + (p.causal_block - in_block), static_cast<unsigned>(q.len)));
 }
 
 // Offset of token `tok` of sequence s in q, and in out (elements, head 0).

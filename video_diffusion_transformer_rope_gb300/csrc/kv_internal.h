@@ -26,7 +26,7 @@ struct AppendParams {
   long long kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;
   const int* cu;
   const int* kv_len;
-  const int* pos_offset;      // nullptr: 0
+  const int* pos_offset;      // of causal_block > 0; nullptr: 0
   const int* table;
   long long table_stride;
   const void* q_norm;         // nullptr: no norm
@@ -54,6 +54,7 @@ struct KvParams {
   long long k_p, k_t, k_h, v_p, v_t, v_h;
   const int* cu;
   const int* kv_len;          // nullptr: P keys
+  const int* pos_offset;      // of causal_block > 0; nullptr: 0
   const int* table;
   long long table_stride;
   int max_pages, num_pages, P;

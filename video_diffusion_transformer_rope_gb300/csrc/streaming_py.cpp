@@ -298,6 +298,7 @@ PyObject* paged(PyObject* const* a) {
   const at::Tensor& q = paged_args(a, &c, &x);
   x.causal_block = integer("causal_block", a[8]);
   x.scale = static_cast<float>(real(a[9]));
+  x.pos_offset = int32s("pos_offset", a[14], q, c.seqs);
   const int64_t lse_shape[2] = {x.Hq, x.rows};
   return attention(x, q, lse_shape, a[10], a[11], a[12], a[13], [&] { return g_paged_size(&c, &x); },
                    [&](void* stream) { return g_paged(&c, &x, stream); });
@@ -381,7 +382,7 @@ PyObject* bind(PyObject*, PyObject* args) {
 PyMethodDef kMethods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
     VDX_ENTRY(append, 16),
-    VDX_ENTRY(paged, 14),
+    VDX_ENTRY(paged, 15),
     VDX_ENTRY(paged_size, 8),
     VDX_ENTRY(cross, 9),
     VDX_ENTRY(cross_size, 4),

@@ -78,10 +78,12 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
 
 
 def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, scale=0.0, out=None, lse=None,
-               return_lse=True, stream=None, workspace=None):
+               return_lse=True, stream=None, workspace=None, pos_offset=None):
     """Attention of new tokens over the cache: q [rows, Hq, d], already rotated, keys already appended
     (rope3d_append); cu and kv_len as there.  causal_block 0: every row sees all kv_len keys of its
-    sequence; 1: the keys up to its own; m: whole blocks of m keys (latent frames) up to its own.
+    sequence; 1: the keys up to its own; m: whole blocks of m grid tokens (latent frames) up to its own.
+    pos_offset: as in rope3d_append, where a sequence's oldest pages were dropped: blocks are counted from
+    grid token 0, so key 0 may stand inside one.
 
     max_q, max_kv: host bounds on the rows and keys of a sequence (default: rows, and what the page
     table can hold); tight ones make small launches.  workspace: an optional CUDA tensor of
@@ -92,10 +94,10 @@ def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, sc
     call = (_native or _load()).paged
     if stream is None:
         return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, causal_block, scale, out, lse, return_lse,
-                    workspace)
+                    workspace, pos_offset)
     with _on(stream, q):
         return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, causal_block, scale, out, lse, return_lse,
-                    workspace)
+                    workspace, pos_offset)
 
 
 def paged_attn_workspace_bytes(q, cache, cu, kv_len, max_q=None, max_kv=None):
