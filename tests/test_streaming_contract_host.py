@@ -65,3 +65,42 @@ def test_append_takes_caches_side_by_side(L, ckw):
 def test_paged_attention_checks_its_position_offsets(L):
     r = L.vdx_paged_attn(ctypes.byref(_cache()), ctypes.byref(_paged(pos_offset=FAKE + 9 * G + 2)), None)
     assert r == B.VDX_ERR_ALIGN and "pos_offset" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+# ------------------------------------------------------------------------------------------ the build
+@pytest.fixture
+def small_build(tmp_path, monkeypatch):
+    # one source, linked elsewhere: what build() does, in seconds
+    monkeypatch.setattr(_build, "SOURCES", ["kv_capi.cu"])
+    monkeypatch.setattr(_build, "OUT_DIR", str(tmp_path / "out"))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(_build, "EXT", str(tmp_path / "ext.so"))
+    monkeypatch.setattr(_build, "EXT_STAMP", str(tmp_path / "ext.torch"))
+    return tmp_path
+
+
+def test_the_library_is_built_without_what_the_python_entry_needs(small_build, monkeypatch):
+    base = small_build / "torch"                                   # a PyTorch without CUDA
+    (base / "lib").mkdir(parents=True)
+    (base / "__init__.py").write_text("")
+    monkeypatch.setattr(_build.importlib.util, "find_spec",
+                        lambda name: type("Spec", (), {"origin": str(base / "__init__.py")}))
+    assert _build.build() == _build.LIB and os.path.exists(_build.LIB) and not os.path.exists(_build.EXT)
+    assert not _build._stale() and "no CUDA part" in _build._ext_lacks(str(base))
+    monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name: None)
+    assert not _build._stale() and "not installed" in _build._ext_lacks(None)
+
+
+def test_a_python_without_headers_builds_the_library(small_build, monkeypatch):
+    paths = dict(_build.sysconfig.get_paths(), include=str(small_build))
+    monkeypatch.setattr(_build.sysconfig, "get_paths", lambda: paths)
+    assert _build.build() == _build.LIB and not os.path.exists(_build.EXT) and not _build._stale()
+
+
+def test_an_entry_that_does_not_compile_leaves_the_library(small_build, monkeypatch):
+    def fails(torch):
+        raise RuntimeError("does not compile")
+    monkeypatch.setattr(_build, "_build_ext", fails)
+    with pytest.raises(RuntimeError, match="does not compile"):
+        _build.build()
+    assert os.path.exists(_build.LIB)

@@ -1,5 +1,6 @@
 """Build libvdx.so in-tree with nvcc for sm_103a (GB300), and with the host compiler the Python entry of
-the streaming calls (_streaming_py.so, where PyTorch is installed).
+the streaming calls (_streaming_py.so, where a PyTorch with CUDA and the interpreter's headers are installed;
+the library itself needs neither).
 
 Each .cu file is compiled to an object in parallel, then linked into one shared library with
 the CUDA runtime linked statically (so the library loads on machines without the NVIDIA driver;
@@ -43,10 +44,27 @@ def _deps():
     return files
 
 
-def _torch():
-    """PyTorch's folder and version, without importing it; None where it is not installed."""
+def _ext_lacks(base):
+    """What the Python entry would need and does not find, PyTorch being installed in `base` (None: not at all)."""
+    if base is None:
+        return "PyTorch is not installed"
+    for name in ("lib/libc10_cuda.so", "include/c10/cuda/CUDAStream.h"):
+        if not os.path.exists(os.path.join(base, name)):
+            return f"this PyTorch has no CUDA part ({name})"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "this Python has no headers (Python.h)"
+    return None
+
+
+def _torch_base():
     spec = importlib.util.find_spec("torch")
-    return (os.path.dirname(spec.origin), importlib.metadata.version("torch")) if spec else None
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _torch():
+    """PyTorch's folder and version, without importing it; None where the Python entry cannot be built with it."""
+    base = _torch_base()
+    return None if _ext_lacks(base) else (base, importlib.metadata.version("torch"))
 
 
 def _ext_stamp(version):
@@ -90,7 +108,9 @@ def _build_ext(torch):
 
 def build(force=False, verbose=False):
     """Compile and link libvdx.so, and the Python entry of the streaming calls, if any source is newer.
-    Returns the library path."""
+    Returns the library path.  Where the Python entry cannot be built (no PyTorch with CUDA, no headers) the
+    library is built alone and the streaming calls say why; where its compilation fails, the library is linked
+    all the same before that is raised."""
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()
@@ -110,14 +130,14 @@ def build(force=False, verbose=False):
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         ext = ex.submit(_build_ext, torch) if torch else None
         objs = list(ex.map(compile_one, SOURCES))
-        if ext:
-            ext.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if ext:
+        ext.result()
     if verbose:
         for src in SOURCES:
             print(open(os.path.join(OUT_DIR, src + ".ptxas.txt")).read())

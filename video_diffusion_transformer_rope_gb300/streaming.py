@@ -24,6 +24,10 @@ def _load():
     try:
         from . import _streaming_py as native
     except ImportError as e:
+        from . import _build
+        why = _build._ext_lacks(_build._torch_base())
+        if why:
+            raise RuntimeError(f"the streaming calls are not available: {why}") from e
         raise RuntimeError("the compiled entry of the streaming calls is missing or does not load: build it with "
                            f"video_diffusion_transformer_rope_gb300._build.build() ({e})") from e
     if native.TORCH_VERSION.split("+")[0] != torch.__version__.split("+")[0]:
