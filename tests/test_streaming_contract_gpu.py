@@ -215,3 +215,36 @@ def test_dropping_pages_inside_a_frame_changes_only_what_is_gone():
         p = torch.arange(total - n, total, device="cuda")
         lim = ((torch.div(p, frame, rounding_mode="floor") + 1) * frame).clamp(max=total) - drop
         check_attention(out, lse, attend(rot[-n:], kk[drop:], vv[drop:], lim), dt, f"{gone} pages gone")
+
+
+# ------------------------------------------------------------------------------------ autograd
+def _small(seed=140):
+    dt = torch.bfloat16
+    c = Paged(dt, 64, 2, 16, [40, 9], seed=seed)
+    x, text = _rand((2, 2, 64), dt, seed + 1), _rand((1, 50, 2, 64), dt, seed + 2)
+    return c, vdx.PagedKV(c.k, c.v, c.table), x, cu_of([1, 1]), text
+
+
+def test_tangents_and_transforms_are_refused():
+    import torch.autograd.forward_ad as fw
+    c, cache, x, cu, text = _small()
+    calls = [lambda t: vdx.rope3d_append(t, x, x, cache, cu, c.kv_len, (50, 1, 1)),
+             lambda t: vdx.rope3d_append(x, t, x, cache, cu, c.kv_len, (50, 1, 1)),
+             lambda t: vdx.rope3d_append(x, x, t, cache, cu, c.kv_len, (50, 1, 1)),
+             lambda t: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1, 1), k_norm=t[0, 0]),
+             lambda t: vdx.paged_attn(t, cache, cu, c.kv_len),
+             lambda t: vdx.cross_attn(t[None], text, text)[0][0],
+             lambda t: vdx.cross_attn(text, t[None], t[None])[0]]
+    for i, f in enumerate(calls):
+        with fw.dual_level():
+            with pytest.raises(vdx.VdxError, match="forward"):
+                f(fw.make_dual(x, torch.ones_like(x)))
+                pytest.fail(f"call {i} took a tangent")
+        with pytest.raises(vdx.VdxError, match="forward"):
+            torch.func.jvp(lambda t: f(t), (x,), (torch.ones_like(x),))
+        with pytest.raises(vdx.VdxError, match="transform"):
+            torch.func.vmap(f)(x[None])
+        f(x)
+    with pytest.raises(vdx.VdxError, match="gradient"):
+        vdx.paged_attn(x, cache, cu, c.kv_len, lse=torch.zeros(2, 2, device="cuda", requires_grad=True))
+    vdx.sync_check()

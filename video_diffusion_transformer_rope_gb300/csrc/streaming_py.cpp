@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -66,6 +67,16 @@ const at::Tensor* cuda_tensor(PyObject* o) {
   return t.is_cuda() && t.layout() == at::kStrided ? &t : nullptr;
 }
 
+// These calls have no derivative: neither a gradient nor a forward-mode tangent may be asked of a tensor.
+void forward_only(const char* name, const at::Tensor& t) {
+  if (!t.has_storage())
+    refuse(VDX_ERR_UNSUPPORTED, "%s is wrapped by a function transform: these calls are forward only and take plain tensors", name);
+  if (c10::GradMode::is_enabled() && t.requires_grad())
+    refuse(VDX_ERR_UNSUPPORTED, "%s requires a gradient: these calls are forward only (use torch.no_grad() or detach())", name);
+  if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+    refuse(VDX_ERR_UNSUPPORTED, "%s carries a forward-mode tangent: these calls are forward only", name);
+}
+
 // A CUDA tensor of `dims` dimensions on like's device with like's type and dense channels (like NULL: a
 // tensor that the others have to be like).
 const at::Tensor& tensor(const char* name, PyObject* o, const at::Tensor* like, int dims) {
@@ -78,8 +89,7 @@ const at::Tensor& tensor(const char* name, PyObject* o, const at::Tensor* like, 
     if (n > INT_MAX) refuse(VDX_ERR_ARG, "%s: %s is too large", name, text(t->sizes()).c_str());
   if (t->stride(dims - 1) != 1 && t->size(dims - 1) > 1)
     refuse(VDX_ERR_ARG, "%s: the channels of a head must be contiguous", name);
-  if (t->requires_grad() && c10::GradMode::is_enabled())
-    refuse(VDX_ERR_UNSUPPORTED, "%s requires a gradient: these calls are forward only (use torch.no_grad() or detach())", name);
+  forward_only(name, *t);
   return *t;
 }
 int dtype_of(const at::Tensor& t) {
@@ -189,6 +199,7 @@ PyObject* attention(Args& a, const at::Tensor& q, at::IntArrayRef lse_shape, PyO
     const at::Tensor* t = cuda_tensor(lse_);
     if (!t || t->scalar_type() != at::kFloat || t->sizes() != lse_shape || !t->is_contiguous() || t->device() != q.device())
       refuse(VDX_ERR_ARG, "lse must be a contiguous float32 tensor of shape %s on %s", text(lse_shape).c_str(), dev(q).c_str());
+    forward_only("lse", *t);
     lse = *t;
   } else {
     const int want = PyObject_IsTrue(return_lse);
