@@ -248,3 +248,37 @@ def test_tangents_and_transforms_are_refused():
     with pytest.raises(vdx.VdxError, match="gradient"):
         vdx.paged_attn(x, cache, cu, c.kv_len, lse=torch.zeros(2, 2, device="cuda", requires_grad=True))
     vdx.sync_check()
+
+
+def test_autograd_sees_what_the_calls_write():
+    # a tensor that autograd saved and a call then overwrote must not be used for a gradient
+    c, cache, x, cu, text = _small(150)
+    w = torch.ones((), device="cuda", requires_grad=True)
+    q_out, out, lse = torch.empty_like(x), torch.empty_like(x), torch.empty(2, 2, device="cuda")
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    text_out = torch.empty_like(text)
+    with torch.no_grad():
+        for t in (q_out, out, lse, text_out):
+            t.zero_()
+    calls = [(lambda: vdx.rope3d_append(x, x, x, cache, cu, c.kv_len, (50, 1, 1), q_out=q_out), [c.k, c.v, q_out], [x, c.table, cu]),
+             (lambda: vdx.rope3d_append(None, x, x, cache, cu, c.kv_len, (50, 1, 1)), [c.k, c.v], [x]),
+             (lambda: vdx.paged_attn(x, cache, cu, c.kv_len, out=out, lse=lse, workspace=ws), [out, lse, ws], [x, c.k, c.v]),
+             (lambda: vdx.cross_attn(text, text, text, out=text_out), [text_out], [text])]
+    for call, writes, reads in calls:
+        saved = [(t, (w * t.detach()).sum()) for t in writes + reads if t.dtype.is_floating_point]   # saves t for w's gradient
+        before = [t._version for t in writes + reads]
+        call()
+        now = [t._version for t in writes + reads]
+        assert all(b > a for a, b in zip(before[:len(writes)], now)) and now[len(writes):] == before[len(writes):]
+        for t, y in saved:
+            if any(t is o for o in writes):
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    y.backward()
+            else:
+                y.backward()
+    with torch.inference_mode():                                   # tensors without a version
+        a, b = torch.zeros_like(c.k), torch.zeros_like(c.v)
+        o = torch.empty_like(x)
+    vdx.rope3d_append(x, x, x, vdx.PagedKV(a, b, c.table), cu, c.kv_len, (50, 1, 1), q_out=o)
+    vdx.sync_check()
+    assert bool((b != 0).any())

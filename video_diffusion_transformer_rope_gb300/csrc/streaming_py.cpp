@@ -139,8 +139,13 @@ double real(PyObject* o) {
   return v;
 }
 const void* address(const at::Tensor& t) { return t.const_data_ptr(); }
+// A tensor of the caller's that the call has written: autograd must be able to tell that one it saved is not
+// what it was.  (Inference tensors have no version.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 
-const at::Tensor& cache_struct(PyObject* k_, PyObject* v_, PyObject* table_, vdx_paged_kv* c) {
+const at::Tensor& cache_struct(PyObject* k_, PyObject* v_, PyObject* table_, vdx_paged_kv* c, bool writes) {
   const at::Tensor& k = tensor("the key cache", k_, nullptr, 4);
   const at::Tensor& v = tensor("the value cache", v_, &k, 4);
   if (k.sizes() != v.sizes())
@@ -149,8 +154,8 @@ const at::Tensor& cache_struct(PyObject* k_, PyObject* v_, PyObject* table_, vdx
   if (!t || t->scalar_type() != at::kInt || t->device() != k.device() || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1) ||
       t->size(0) > INT_MAX - 1 || t->size(1) > INT_MAX)
     refuse(VDX_ERR_ARG, "page_table must be an int32 [seqs, max_pages] tensor on %s with contiguous rows", dev(k).c_str());
-  c->k = const_cast<void*>(address(k));
-  c->v = const_cast<void*>(address(v));
+  c->k = writes ? k.mutable_data_ptr() : const_cast<void*>(address(k));
+  c->v = writes ? v.mutable_data_ptr() : const_cast<void*>(address(v));
   c->k_page = k.stride(0); c->k_token = k.stride(1); c->k_head = k.stride(2);
   c->v_page = v.stride(0); c->v_token = v.stride(1); c->v_head = v.stride(2);
   c->page_table = static_cast<const int32_t*>(address(*t));
@@ -220,6 +225,9 @@ PyObject* attention(Args& a, const at::Tensor& q, at::IntArrayRef lse_shape, PyO
     a.workspace_bytes = static_cast<size_t>(workspace.numel()) * workspace.element_size();
   }
   call(q, run);
+  if (out_ != Py_None) written(out);
+  if (lse_ != Py_None) written(lse);
+  if (workspace_ != Py_None) written(workspace);
   PyObject* o = out_ == Py_None ? THPVariable_Wrap(out) : Py_NewRef(out_);
   PyObject* l = !lse.defined() ? Py_NewRef(Py_None) : (lse_ == Py_None ? THPVariable_Wrap(lse) : Py_NewRef(lse_));
   PyObject* r = o && l ? PyTuple_Pack(2, o, l) : nullptr;
@@ -233,7 +241,7 @@ PyObject* append(PyObject* const* a) {
   PyObject *q_ = a[0], *q_out_ = a[12];
   vdx_paged_kv c{};
   vdx_append_args x{};
-  const at::Tensor& like = cache_struct(a[3], a[4], a[5], &c);
+  const at::Tensor& like = cache_struct(a[3], a[4], a[5], &c, true);
   const at::Tensor& k = tensor("k", a[1], &like, 3);
   const at::Tensor& v = tensor("v", a[2], &like, 3);
   if (k.size(1) != c.Hkv || k.size(2) != c.d || v.sizes() != k.sizes())
@@ -259,9 +267,14 @@ PyObject* append(PyObject* const* a) {
   three("sections", a[14], &x.sec_t, &x.sec_h, &x.sec_w);
   x.theta = real(a[15]);
   x.eps = static_cast<float>(real(a[11]));
+  auto run = [&] {
+    call(like, [&](void* stream) { return g_append(&c, &x, stream); });
+    written(THPVariable_Unpack(a[3]));
+    written(THPVariable_Unpack(a[4]));
+  };
   if (q_ == Py_None) {
     if (q_out_ != Py_None) refuse(VDX_ERR_ARG, "q_out without q");
-    call(like, [&](void* stream) { return g_append(&c, &x, stream); });
+    run();
     Py_RETURN_NONE;
   }
   const at::Tensor& q = tensor("q", q_, &like, 3);
@@ -282,14 +295,15 @@ PyObject* append(PyObject* const* a) {
   if (x.rows > 0) {                                        // empty tensors have no address
     x.q_out = out.mutable_data_ptr();
     x.q_out_row = out.stride(0); x.q_out_head = out.stride(1);
-    call(like, [&](void* stream) { return g_append(&c, &x, stream); });
+    run();
+    if (q_out_ != Py_None) written(out);
   }
   return q_out_ == Py_None ? THPVariable_Wrap(out) : Py_NewRef(q_out_);
 }
 
 // q, the cache's three tensors, cu, kv_len, max_q, max_kv of a paged call
 const at::Tensor& paged_args(PyObject* const* a, vdx_paged_kv* c, vdx_paged_attn_args* x) {
-  const at::Tensor& like = cache_struct(a[1], a[2], a[3], c);
+  const at::Tensor& like = cache_struct(a[1], a[2], a[3], c, false);
   const at::Tensor& q = tensor("q", a[0], &like, 3);
   if (q.size(2) != c->d)
     refuse(VDX_ERR_ARG, "q %s does not match the cache's head dimension %d", text(q.sizes()).c_str(), c->d);
