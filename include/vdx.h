@@ -296,6 +296,7 @@ typedef struct vdx_paged_attn_args {
   const int32_t* pos_offset;   /* [seqs] or NULL; read with causal_block > 0                      */
 } vdx_paged_attn_args;
 vdx_status vdx_paged_attn(const vdx_paged_kv* cache, const vdx_paged_attn_args* args, void* stream);
+/* 0 also where the call would be refused: vdx_last_error() is not empty then. */
 size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* cache, const vdx_paged_attn_args* args);
 
 /* Cross attention: q [B, N, Hq, d] over k, v [B, M, Hkv, d] (an encoder's states; no positions).

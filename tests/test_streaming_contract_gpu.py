@@ -282,3 +282,21 @@ def test_autograd_sees_what_the_calls_write():
     vdx.rope3d_append(x, x, x, vdx.PagedKV(a, b, c.table), cu, c.kv_len, (50, 1, 1), q_out=o)
     vdx.sync_check()
     assert bool((b != 0).any())
+
+
+# ------------------------------------------------------------------------------------ what is refused
+def test_workspace_sizes_of_calls_that_are_refused():
+    dt = torch.bfloat16
+    c, cache, x, cu, text = _small(160)
+    wide = torch.zeros(2, 258, 64, dtype=dt, device="cuda")       # 129 query heads to a head of the cache
+    odd = torch.zeros(2, 3, 64, dtype=dt, device="cuda")
+    for f in (lambda: vdx.paged_attn_workspace_bytes(wide, cache, cu, c.kv_len), lambda: vdx.paged_attn_workspace_bytes(odd, cache, cu, c.kv_len),
+              lambda: vdx.paged_attn_workspace_bytes(x, cache, None, c.kv_len),
+              lambda: vdx.cross_attn_workspace_bytes(text[..., :32], text[..., :32], text[..., :32]),
+              lambda: vdx.cross_attn_workspace_bytes(text, text[:, :, :1].expand(-1, -1, 3, -1), text[:, :, :1].expand(-1, -1, 3, -1))):
+        with pytest.raises(vdx.VdxError):
+            f()
+    assert vdx.paged_attn_workspace_bytes(x, cache, cu, c.kv_len, 1, 40) == 0
+    assert vdx.cross_attn_workspace_bytes(text[:, :0], text, text) == 0
+    long = torch.zeros(1, 30000, 2, 64, dtype=dt, device="cuda")
+    assert vdx.cross_attn_workspace_bytes(text[:, :1], long, long) > 0

@@ -170,6 +170,12 @@ const at::Tensor& cache_struct(PyObject* k_, PyObject* v_, PyObject* table_, vdx
   return k;
 }
 
+// 0 bytes are an answer, or a call that the library cannot take: then it has left a message.
+PyObject* bytes_or_refusal(size_t bytes) {
+  if (bytes == 0 && *g_last_error()) refuse(VDX_ERR_ARG, "%s", g_last_error());
+  return PyLong_FromSize_t(bytes);
+}
+
 // Device of the call made current, its current stream, and the interpreter released for the call itself.
 template <typename F>
 void call(const at::Tensor& like, F&& f) {
@@ -332,7 +338,7 @@ PyObject* paged_size(PyObject* const* a) {
   vdx_paged_kv c{};
   vdx_paged_attn_args x{};
   const c10::cuda::CUDAGuard guard(paged_args(a, &c, &x).device());
-  return PyLong_FromSize_t(g_paged_size(&c, &x));
+  return bytes_or_refusal(g_paged_size(&c, &x));
 }
 
 // q, k, v, kv_len of a cross-attention call
@@ -370,7 +376,7 @@ PyObject* cross(PyObject* const* a) {
 PyObject* cross_size(PyObject* const* a) {
   vdx_cross_attn_args x{};
   const c10::cuda::CUDAGuard guard(cross_args(a, &x).device());
-  return PyLong_FromSize_t(g_cross_size(&x));
+  return bytes_or_refusal(g_cross_size(&x));
 }
 
 template <PyObject* (*kCall)(PyObject* const*), int kArgs>
