@@ -241,7 +241,8 @@ typedef struct vdx_paged_kv {
  * heads) x * rsqrt(mean(x^2) + eps) * weight is applied to each head before the rotation.
  * fp32 arithmetic, angles reduced exactly, one rounding at the end; v is copied bit for bit.
  * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place),
- * also inside a fused projection; otherwise the outputs must not overlap an input, nor each other.  A token outside the grid's T*Hgrid*Wgrid
+ * also inside a fused projection; otherwise the outputs (q_out and the cache) must not overlap an
+ * input (lengths, page table and weights too), nor each other.  A token outside the grid's T*Hgrid*Wgrid
  * positions, or with a cache index below 0 or past its page table, is skipped and reported; so are the
  * tokens of a sequence whose range in cu is no range of the call's rows.
  * Two rows of one call that land in the same cache slot (sequences whose tables share a page that both
@@ -277,7 +278,7 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* cache, const vdx_append_args* a
  *   out: [rows, Hq, d] contiguous;  lse: float32 [Hq, rows] or NULL.
  *   max_q, max_kv: host bounds on n and on kv_len (they size the launch; 0 takes rows and
  *   max_pages * page_size).  Rows and keys past them are not computed, and reported.
- *   scale <= 0 selects 1/sqrt(d).  out must not overlap q, k or v.
+ *   scale <= 0 selects 1/sqrt(d).  out, lse and workspace must not overlap an input, nor each other.
  *   workspace: >= vdx_paged_attn_workspace_bytes() bytes of the device, 16-byte aligned, used by
  *   this call alone until it has run; NULL where that is 0. */
 typedef struct vdx_paged_attn_args {

@@ -104,3 +104,48 @@ def test_an_entry_that_does_not_compile_leaves_the_library(small_build, monkeypa
     with pytest.raises(RuntimeError, match="does not compile"):
         _build.build()
     assert os.path.exists(_build.LIB)
+
+
+# ------------------------------------------------------------------------- outputs over what the calls read beside q, k, v
+@pytest.mark.parametrize("ckw,kw", [
+    (dict(), dict(q_out=FAKE + 7 * G)),                                        # cu
+    (dict(), dict(q_out=FAKE + 8 * G - 7 * 1024 + 16)),                        # kv_len, at q_out's end
+    (dict(), dict(pos_offset=FAKE + 64)),
+    (dict(page_table=FAKE + G + 1024), dict()),
+    (dict(page_table=FAKE - 4 * (2 * 8 + 8) + 4), dict()),                     # the last page of the last sequence
+    (dict(), dict(q_norm=FAKE + 6 * G + 512)),
+    (dict(), dict(k_norm=FAKE - 240)),
+])
+def test_append_refuses_outputs_over_lengths_tables_and_weights(L, ckw, kw):
+    r = L.vdx_rope3d_append(ctypes.byref(_cache(**ckw)), ctypes.byref(_append(**kw)), None)
+    assert r == B.VDX_ERR_ARG and "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+@pytest.mark.parametrize("ckw,kw", [
+    (dict(), dict(out=FAKE + 7 * G)), (dict(), dict(lse=FAKE + 8 * G)), (dict(), dict(pos_offset=FAKE + 4 * G + 4, causal_block=3)),
+    (dict(page_table=FAKE + 5 * G + 7 * 4 * 4 - 4), dict()),
+    (dict(page_table=FAKE + 4 * G - 4 * (2 * 8 + 8) + 4), dict()),
+])
+def test_paged_attention_refuses_outputs_over_lengths_and_tables(L, ckw, kw):
+    r = L.vdx_paged_attn(ctypes.byref(_cache(**ckw)), ctypes.byref(_paged(**kw)), None)
+    assert r == B.VDX_ERR_ARG and "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+def test_attention_refuses_scratch_and_outputs_over_lengths(L):
+    c = _cache(page_size=128, max_pages=512, table_stride=512, num_pages=600, k_page=128 * 512, v_page=128 * 512)
+    need = L.vdx_paged_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(_paged(rows=3, max_q=1)))
+    assert need > 0
+    for at in (FAKE + 7 * G, FAKE + 8 * G - need + 16, FAKE + 2 * G + 16):
+        at -= at % 16
+        a = _paged(rows=3, max_q=1, workspace=at, workspace_bytes=need)
+        assert L.vdx_paged_attn(ctypes.byref(c), ctypes.byref(a), None) == B.VDX_ERR_ARG
+        assert "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
+    for kw in (dict(kv_len=FAKE + 3 * G + 64), dict(kv_len=FAKE + 4 * G)):
+        assert L.vdx_cross_attn(ctypes.byref(_cross(**kw)), None) == B.VDX_ERR_ARG
+        assert "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+def test_a_table_stride_past_its_bound_is_refused(L):
+    c = _cache(table_stride=1 << 61)
+    for r in (L.vdx_rope3d_append(ctypes.byref(c), ctypes.byref(_append()), None), L.vdx_paged_attn(ctypes.byref(c), ctypes.byref(_paged()), None)):
+        assert r == B.VDX_ERR_ARG and "table_stride" in L.vdx_last_error().decode(), L.vdx_last_error()

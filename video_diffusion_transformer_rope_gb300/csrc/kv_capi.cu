@@ -66,6 +66,20 @@ bool overlap(const Tensor& a, const void* p, size_t bytes) {
   return p && bytes && !a.empty() && a.begin() < x + bytes && x < a.end();
 }
 
+// What a call reads beside its tensors: lengths, page tables, weights.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+Span ints(const int* p, long long n) { return {p, n > 0 ? static_cast<size_t>(n) * 4 : 0}; }
+Span table_span(const int* table, int seqs, long long stride, int max_pages) {
+  return ints(table, seqs > 0 ? (seqs - 1) * stride + max_pages : 0);
+}
+
 // Whether no row of `a` shares an element with a row of `b`, also where their spans interleave (slices of one
 // fused projection): true if, with some of the dimensions walked inside a window, the windows of both
 // repeat by steps with a common divisor and lie apart within it.
@@ -161,6 +175,7 @@ vdx_status check_cache(const vdx_paged_kv* c, int Hq) {
                 static_cast<long long>(c->max_pages) * c->page_size);
   if (c->table_stride < c->max_pages && c->seqs > 1)
     return fail(VDX_ERR_ARG, "table_stride %lld is smaller than max_pages %d", c->table_stride, c->max_pages);
+  if (c->table_stride > kMaxStride && c->seqs > 1) return fail(VDX_ERR_ARG, "table_stride %lld is too large", c->table_stride);
   if (c->seqs > 0)
     if (vdx_status s = check_i32("page_table", c->page_table, false)) return s;
   if (vdx_status s = check_tensor("the key cache", cache_tensor(*c, false), false)) return s;
@@ -216,7 +231,12 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + static_cast<size_t>(rows) * pb->d * 4);
   }
-  (void)out_bytes;
+  const Span reads[4] = {ints(p.cu, p.cu ? p.S + 1ll : 0), ints(p.kv_len, p.S), ints(p.pos_offset, p.S),
+                         table_span(p.table, p.S, p.table_stride, p.max_pages)};
+  const Span writes[3] = {{p.out, out_bytes}, {p.lse, lse_bytes}, {pb->workspace ? workspace : nullptr, pb->workspace}};
+  for (const Span& r : reads)
+    for (const Span& w : writes)
+      if (overlap(r, w)) return fail(VDX_ERR_ARG, "out, lse or workspace overlaps cu, kv_len, pos_offset or page_table");
   return VDX_OK;
 }
 
@@ -429,6 +449,13 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
   for (const Tensor* t : {&kc, &vc})
     if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
       return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
+  const Span reads[6] = {ints(a->cu, c->seqs + 1ll), ints(a->kv_len, c->seqs), ints(a->pos_offset, c->seqs),
+                         table_span(c->page_table, c->seqs, c->table_stride, c->max_pages),
+                         {a->q_norm, static_cast<size_t>(d) * 2}, {a->k_norm, static_cast<size_t>(d) * 2}};
+  for (const Span& r : reads)
+    for (const Tensor* t : {&kc, &vc, &qo})
+      if (overlap(*t, r.p, r.bytes))
+        return fail(VDX_ERR_ARG, "the cache or q_out overlaps cu, kv_len, pos_offset, page_table, q_norm or k_norm");
 
   vdx::AppendParams p{};
   p.q = a->q; p.k = a->k; p.v = a->v; p.q_out = a->q_out; p.k_cache = c->k; p.v_cache = c->v;
