@@ -149,3 +149,11 @@ def test_a_table_stride_past_its_bound_is_refused(L):
     c = _cache(table_stride=1 << 61)
     for r in (L.vdx_rope3d_append(ctypes.byref(c), ctypes.byref(_append()), None), L.vdx_paged_attn(ctypes.byref(c), ctypes.byref(_paged()), None)):
         assert r == B.VDX_ERR_ARG and "table_stride" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+def test_parameters_whose_products_are_not_finite_are_refused(L):
+    r = L.vdx_rope3d_append(ctypes.byref(_cache()), ctypes.byref(_append(theta=5e-324)), None)
+    assert r == B.VDX_ERR_ARG and "theta" in L.vdx_last_error().decode(), L.vdx_last_error()
+    for r in (L.vdx_paged_attn(ctypes.byref(_cache()), ctypes.byref(_paged(scale=3e38)), None),
+              L.vdx_cross_attn(ctypes.byref(_cross(scale=3e38)), None)):
+        assert r == B.VDX_ERR_ARG and "scale" in L.vdx_last_error().decode(), L.vdx_last_error()

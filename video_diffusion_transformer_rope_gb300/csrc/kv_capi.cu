@@ -196,6 +196,7 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
   vdx::KvParams& p = pb->p;
   if (!std::isfinite(scale)) return fail(VDX_ERR_ARG, "scale must be finite");
   p.scale_log2 = static_cast<float>((scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(pb->d))) * 1.4426950408889634);
+  if (!std::isfinite(p.scale_log2)) return fail(VDX_ERR_ARG, "scale = %g is too large", static_cast<double>(scale));
   pb->nothing = q.empty();
   if (pb->nothing) return VDX_OK;
   if (static_cast<long long>(p.max_q) * p.g > 0x7ffff000ll)     // row numbers of padded blocks stay in an int
@@ -475,6 +476,7 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
   for (int x = 0; x < 3; ++x)
     for (int j = 0; j < sec[x] / 2; ++j) {
       const double turns = std::pow(a->theta, -2.0 * j / sec[x]) / 6.283185307179586476925286766559;
+      if (!std::isfinite(turns)) return fail(VDX_ERR_ARG, "theta = %g is too small: its powers are not finite", a->theta);
       const double frac = turns - std::floor(turns);
       p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
     }
