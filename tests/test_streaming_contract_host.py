@@ -157,3 +157,9 @@ def test_parameters_whose_products_are_not_finite_are_refused(L):
     for r in (L.vdx_paged_attn(ctypes.byref(_cache()), ctypes.byref(_paged(scale=3e38)), None),
               L.vdx_cross_attn(ctypes.byref(_cross(scale=3e38)), None)):
         assert r == B.VDX_ERR_ARG and "scale" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
+def test_more_sequences_and_heads_than_a_launch_has_blocks_are_refused(L):
+    c = _cache(seqs=1 << 30, max_pages=1, table_stride=1)
+    for r in (L.vdx_paged_attn(ctypes.byref(c), ctypes.byref(_paged()), None), L.vdx_cross_attn(ctypes.byref(_cross(B=1 << 29)), None)):
+        assert r == B.VDX_ERR_ARG and "too many" in L.vdx_last_error().decode(), L.vdx_last_error()

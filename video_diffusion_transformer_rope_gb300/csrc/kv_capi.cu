@@ -201,6 +201,8 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
   if (pb->nothing) return VDX_OK;
   if (static_cast<long long>(p.max_q) * p.g > 0x7ffff000ll)     // row numbers of padded blocks stay in an int
     return fail(VDX_ERR_ARG, "%d rows of %d heads per kv head are too many", p.max_q, p.g);
+  if (static_cast<long long>(p.S) * p.Hkv > 0x3fffffffll)       // a launch has fewer blocks; products below stay in 64 bits
+    return fail(VDX_ERR_ARG, "%d sequences of %d kv heads are too many", p.S, p.Hkv);
   if (vdx_status s = check_tensor("q", q, true)) return s;
   if (vdx_status s = check_tensor("k", k, true)) return s;
   if (vdx_status s = check_tensor("v", v, true)) return s;
