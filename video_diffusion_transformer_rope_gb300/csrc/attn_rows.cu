@@ -93,19 +93,14 @@ attn_rows(const __grid_constant__ KvParams p) {
 
   const int z = blockIdx.x % p.nsplit;
   const int unit = blockIdx.x / p.nsplit;
-  const int blk = unit % p.nblk;
-  const int hk = (unit / p.nblk) % p.Hkv;
-  const int s = unit / p.nblk / p.Hkv;
+  const int hk = unit % p.Hkv, s = unit / p.Hkv;        // all rows of a kv head are one block
   const SeqInfo sq = sequence_info(p, s, threadIdx.x == 0);
-  const long long first_row = static_cast<long long>(blk) * kRows;
-  const long long all_rows = static_cast<long long>(min(sq.n, p.max_q)) * p.g;
-  if (first_row >= all_rows) return;
-  const int live = static_cast<int>(min(static_cast<long long>(kRows), all_rows - first_row));
+  const int live = min(sq.n, p.max_q) * p.g;            // max_q * g <= kRows
+  if (live == 0) return;
 
   // Keys of this split, up to the last row's limit: an equal part for each CTA of a cluster, which
   // wait for one another; fixed ranges otherwise (a CTA past a short sequence's end leaves).
-  const int last_tok = static_cast<int>((first_row + live - 1) / p.g);
-  const int len = visible_limit(p, sq, last_tok);
+  const int len = visible_limit(p, sq, (live - 1) / p.g);
   const long long keys = p.cluster ? (len / (kKeys * kWarps) / p.nsplit + 1) * (kKeys * kWarps) : p.split_keys;
   const long long lo64 = z * keys;
   const int lo = static_cast<int>(min(lo64, static_cast<long long>(len)));
@@ -119,8 +114,7 @@ attn_rows(const __grid_constant__ KvParams p) {
     const int r = nt * 8 + gq;
     const T* src = nullptr;
     if (r < live) {
-      const long long R = first_row + r;
-      const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
+      const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
       src = static_cast<const T*>(p.q) + (p.cu ? 0 : s * p.q_b) + (static_cast<long long>(sq.row0) + tok) * p.q_t + h * p.q_h;
     }
 #pragma unroll
@@ -131,12 +125,12 @@ attn_rows(const __grid_constant__ KvParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = nt * 8 + 2 * c4 + e;
-      limit[nt][e] = rr < live ? min(visible_limit(p, sq, static_cast<int>((first_row + rr) / p.g)), hi) : hi;
+      limit[nt][e] = rr < live ? min(visible_limit(p, sq, rr / p.g), hi) : hi;
     }
   }
   // Below this key every row sees everything.
   const int full_to = p.causal_block > 0
-                          ? min(hi, visible_limit(p, sq, static_cast<int>(first_row / p.g)))
+                          ? min(hi, visible_limit(p, sq, 0))
                           : hi;
 
   float o[kNT][D / 16][4];
@@ -325,8 +319,7 @@ attn_rows(const __grid_constant__ KvParams p) {
   float* cm = sl + kWarps * kRows;                                  // [kRows]: this CTA's maximum and sum
   float* cl = cm + kRows;
   auto store = [&](int r, int dq, float mx, float lt, const float4& acc) {
-    const long long R = first_row + r;
-    const int tok = static_cast<int>(R / p.g), h = hk * p.g + static_cast<int>(R - static_cast<long long>(tok) * p.g);
+    const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
     const bool none = mx == -INFINITY && lt == lt;                  // no key seen; a NaN sum is an answer
     const float inv = none ? 0.f : 1.f / lt;
     uint2 w2;
