@@ -26,6 +26,7 @@ namespace vdx {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kResident = 9;        // blocks that a multiprocessor holds at least (56 registers a thread)
 // Rows that each group has in flight in a block of kTok tokens.  Small blocks and few rows in flight waste
 // little where the heads do not divide by a batch of rows, and leave registers for more blocks: 3 rows of
 // 128 threads and 4 tokens a block take 14.0 us for 3120 tokens of 3 x 12 heads and 215 us for 21600 of
@@ -209,7 +210,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
 }
 
 template <typename T, int D, int kTok>
-__global__ void __launch_bounds__(kThreads, 9)
+__global__ void __launch_bounds__(kThreads, kResident)
 kv_append(const __grid_constant__ AppendParams p) {
   const int row0 = blockIdx.x * kTok;
   wait_for_earlier_work();
@@ -225,19 +226,19 @@ kv_append(const __grid_constant__ AppendParams p) {
 }
 
 template <typename T, int D, int kTok>
-cudaError_t launch_tok(const AppendParams& p, cudaStream_t stream) {
+cudaError_t launch_tok(const AppendParams& p, int sms, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
   const int heads = p.Hq > p.Hkv ? p.Hq : p.Hkv;
   // Few tokens: split the heads over blocks too, until the device is covered (four blocks to a
-  // multiprocessor; with twice that 700 tokens of 12 heads take 10.8 us, not 8.3) or a block's groups have
-  // one row each.
-  const int blocks = (p.rows - 1) / kTok + 1;
+  // multiprocessor) or a block's groups have one row each.  us with 2, 4 and 8 blocks to a multiprocessor: 256
+  // tokens of 12 heads 3.9, 3.6, 3.4; 400 of 12 4.0, 3.9, 4.8; 256 of 40 7.3, 5.3, 5.7; 1100 of 4 4.6, 4.6, 6.7.
+  const int blocks = (p.rows - 1) / kTok + 1, kinds = p.Hq > 0 ? 3 : 2;
   int ny = 1;
   const int most = (kTok * heads + kGroups - 1) / kGroups;
-  while (ny < most && static_cast<long long>(blocks) * ny * 3 < 608) ny *= 2;
+  while (ny < most && static_cast<long long>(blocks) * ny * kinds < 4ll * sms) ny *= 2;
   if (ny > most) ny = most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, ny, p.Hq > 0 ? 3 : 2);
+  cfg.gridDim = dim3(blocks, ny, kinds);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr = launch_early();
@@ -246,17 +247,23 @@ cudaError_t launch_tok(const AppendParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kv_append<T, D, kTok>, p);
 }
 template <typename T, int D>
-cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-  // 4 tokens share a block's look-ups; few tokens are spread wider (12 heads, 2 and 4 to a
-  // block: 128 tokens 4.2 and 5.2 us, 400 5.2 and 6.4, 600 5.7 each, 3120 15.4 and 13.9).
-  return p.rows >= 512 ? launch_tok<T, D, 4>(p, stream) : launch_tok<T, D, 2>(p, stream);
+cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
+  // Blocks of 2 tokens while the device holds all of them at once (912 tokens with q): each has half the work
+  // in turn.  Past that 4 tokens share a block's look-ups.  us, 2 and 4 tokens to a block, d = 128:
+  //   heads   256 tokens   700 tokens   900 tokens   1000 tokens   1560 tokens   3120 tokens
+  //     4     2.8   3.7    3.3   4.7    3.7   4.3    4.7   4.3      5.8   5.2     9.6   8.6
+  //    12     3.6   4.3    4.5   4.9    5.4   5.7    6.5   5.7      8.2   7.1    13.7  12.2
+  //    40     5.3   5.6    8.7   9.3   10.3  11.8   12.7  11.9     19.7  17.1    43.6  36.4
+  // (d = 64 the same up to 900; of 1100 to 2000 tokens, 4 and 40 heads are up to a tenth faster by twos).
+  const long long pairs = ((p.rows - 1) / 2 + 1) * (p.Hq > 0 ? 3ll : 2ll);
+  return pairs <= static_cast<long long>(kResident) * sms ? launch_tok<T, D, 2>(p, sms, stream) : launch_tok<T, D, 4>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, int d, int dtype, cudaStream_t stream) {
-  if (dtype == 0) return d == 128 ? launch<__nv_bfloat16, 128>(p, stream) : launch<__nv_bfloat16, 64>(p, stream);
-  return d == 128 ? launch<__half, 128>(p, stream) : launch<__half, 64>(p, stream);
+cudaError_t launch_append(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream) {
+  if (dtype == 0) return d == 128 ? launch<__nv_bfloat16, 128>(p, sms, stream) : launch<__nv_bfloat16, 64>(p, sms, stream);
+  return d == 128 ? launch<__half, 128>(p, sms, stream) : launch<__half, 64>(p, sms, stream);
 }
 
 cudaError_t read_and_clear_error_word_append(unsigned int* word) { return read_and_clear_word(word); }

@@ -482,7 +482,7 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, vo
       const double frac = turns - std::floor(turns);
       p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
     }
-  const cudaError_t e = vdx::launch_append(p, d, c->dtype, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = vdx::launch_append(p, d, c->dtype, multiprocessors(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));

@@ -39,7 +39,7 @@ struct AppendParams {
   // Turns per position of each channel pair as a 64-bit fixed-point fraction: omega / 2 pi mod 1.
   uint64_t turn[64];
 };
-cudaError_t launch_append(const AppendParams& p, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream);
 
 // Attention over a paged cache (table != nullptr) or over dense keys (one "page" of P = M tokens
 // per batch entry).  Rows: sequence s owns tokens cu[s] .. cu[s+1]-1 of one packed q, or, with
