@@ -300,3 +300,32 @@ def test_workspace_sizes_of_calls_that_are_refused():
     assert vdx.cross_attn_workspace_bytes(text[:, :0], text, text) == 0
     long = torch.zeros(1, 30000, 2, 64, dtype=dt, device="cuda")
     assert vdx.cross_attn_workspace_bytes(text[:, :1], long, long) > 0
+
+
+# ------------------------------------------------------------------------------------ the check of what was reported
+def test_a_check_costs_one_read_until_the_streaming_calls_are_used():
+    # in a process of its own: before any of these calls, vdx_sync_check reads the self-attention's word alone
+    # (one synchronous copy of 4 bytes, as .item() makes one; it takes 1.0 to 1.5 of that, four copies 4)
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, time, torch
+import video_diffusion_transformer_rope_gb300 as vdx
+x = torch.zeros(1, device="cuda")
+def best(f):
+    for _ in range(20):
+        f()
+    t = []
+    for _ in range(9):
+        a = time.perf_counter()
+        for _ in range(50):
+            f()
+        t.append(time.perf_counter() - a)
+    return min(t)
+print(best(vdx.sync_check) / best(lambda: (torch.cuda.current_stream().synchronize(), x.item())))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert float(r.stdout) < 2.5, r.stdout

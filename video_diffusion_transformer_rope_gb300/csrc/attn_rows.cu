@@ -520,6 +520,7 @@ cudaError_t join(const KvParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attn_rows(const KvParams& p, int d, int dtype, cudaStream_t stream) {
+  note_launch();
   if (dtype == 0) return d == 128 ? launch<__nv_bfloat16, 128>(p, stream) : launch<__nv_bfloat16, 64>(p, stream);
   return d == 128 ? launch<__half, 128>(p, stream) : launch<__half, 64>(p, stream);
 }

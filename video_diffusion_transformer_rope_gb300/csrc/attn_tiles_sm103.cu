@@ -1121,6 +1121,7 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
 cudaError_t launch_attn_tiles(const KvParams& p, int d, int dtype, EncodeTiledFn encode, int sms, cudaStream_t stream,
                               const char** what) {
   *what = nullptr;
+  note_launch();
   if (dtype == 0)
     return d == 128 ? launch<__nv_bfloat16, 128>(p, encode, sms, stream, what)
                     : launch<__nv_bfloat16, 64>(p, encode, sms, stream, what);

@@ -262,6 +262,7 @@ cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_append(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream) {
+  note_launch();
   if (dtype == 0) return d == 128 ? launch<__nv_bfloat16, 128>(p, sms, stream) : launch<__nv_bfloat16, 64>(p, sms, stream);
   return d == 128 ? launch<__half, 128>(p, sms, stream) : launch<__half, 64>(p, sms, stream);
 }

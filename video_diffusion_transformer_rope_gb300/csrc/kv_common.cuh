@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -151,8 +152,17 @@ inline cudaLaunchAttribute launch_early() {
   return a;
 }
 
+// Host: whether this translation unit has launched a kernel (or captured one) in this process.  Until then its
+// error word is 0, and reading it would load its kernels and cost every synchronising check a copy.
+static std::atomic<bool> g_launched{false};
+inline void note_launch() {
+  if (!g_launched.load(std::memory_order_relaxed)) g_launched.store(true, std::memory_order_release);
+}
+
 // Host: read and reset this translation unit's error word.
-inline cudaError_t read_and_clear_word(unsigned int* word) {
+static cudaError_t read_and_clear_word(unsigned int* word) {
+  *word = 0;
+  if (!g_launched.load(std::memory_order_acquire)) return cudaSuccess;
   cudaError_t e = cudaMemcpyFromSymbol(word, g_error_word, sizeof(unsigned int));
   if (e != cudaSuccess || *word == 0) return e;
   const unsigned int zero = 0;
