@@ -329,3 +329,23 @@ print(best(vdx.sync_check) / best(lambda: (torch.cuda.current_stream().synchroni
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     assert float(r.stdout) < 2.5, r.stdout
+
+
+@pytest.mark.parametrize("at", [151, 250, 299])
+def test_append_looks_at_the_range_of_every_sequence(at):
+    # 300 sequences of which one has rows; a later range runs backwards, where no row of the call looks
+    S, H, d = 300, 1, 64
+    dt = torch.bfloat16
+    k = torch.zeros(S, 16, H, d, dtype=dt, device="cuda")
+    cache = vdx.PagedKV(k, k.clone(), torch.arange(S, dtype=torch.int32, device="cuda").view(S, 1))
+    x = _rand((4, H, d), dt, 170)
+    cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    cu[150:] = 4
+    kv_len = torch.full((S,), 4, dtype=torch.int32, device="cuda")
+    vdx.rope3d_append(None, x, x, cache, cu, kv_len, (16, 1, 1))
+    vdx.sync_check()
+    assert torch.equal(cache.v[149, :4], x)
+    cu[at + 1:] = 3
+    vdx.rope3d_append(None, x, x, cache, cu, kv_len, (16, 1, 1))
+    with pytest.raises(vdx.VdxError, match="cu or kv_len broke a bound"):
+        vdx.sync_check()

@@ -185,10 +185,11 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
       s_axis[j][2] = col;
     }
   }
-  // One warp of the call looks at every sequence's range (a row's look-up sees only its own).
-  if (kKind == 1 && blockIdx.x == 0 && blockIdx.y == 0 && tid >= kThreads - 32) {
+  // Every sequence's range is looked at (a row's look-up sees only its own), 32 of them by a warp of each block:
+  // many blocks for many sequences.
+  if (kKind == 1 && blockIdx.y == 0 && tid >= kThreads - 32) {
     bool bad = false;
-    for (int s = tid & 31; s < p.S; s += 32) {
+    for (long long s = blockIdx.x * 32ll + (tid & 31); s < p.S; s += gridDim.x * 32ll) {
       const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
       bad = bad || begin < 0 || end < begin || end > p.rows;
     }
