@@ -239,7 +239,9 @@ typedef struct vdx_paged_kv {
  * pos_offset[s] + c (pos_offset NULL: c; larger than 0 when a sequence's oldest pages have been
  * dropped from its table).  With q_norm / k_norm (d values of the call's type, shared by the
  * heads) x * rsqrt(mean(x^2) + eps) * weight is applied to each head before the rotation.
- * fp32 arithmetic, angles reduced exactly, one rounding at the end; v is copied bit for bit.
+ * fp32 arithmetic (angles reduced in 64-bit fixed point, within 2^-25 turns up to position 5e8), one
+ * rounding to the call's type at the end, where vdx_rope3d_attn keeps its rotated q and k in fp16; v is
+ * copied bit for bit.  A norm over all heads of a token is not this one: it goes before the call.
  * q may be NULL (keys and values only).  q_out may equal q with the same strides (in place),
  * also inside a fused projection; otherwise the outputs (q_out and the cache) must not overlap an
  * input (lengths, page table and weights too), nor each other.  A token outside the grid's T*Hgrid*Wgrid
@@ -274,7 +276,8 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* cache, const vdx_append_args* a
  * to its own, also where the oldest pages that were dropped end inside a frame; m = 0: every key).
  * A row that sees no key, or whose p is negative, gets out = 0 and lse = -inf.
  * q, k and v enter the products as they are; scores, softmax statistics and accumulators are
- * fp32; the softmax weights are rounded to the call's type for the product with v.
+ * fp32; the softmax weights are rounded to the call's type for the product with v (fp16: weights below
+ * 2^-14 of a row's largest lose bits).  There is no counterpart of qk_precision.
  *   out: [rows, Hq, d] contiguous;  lse: float32 [Hq, rows] or NULL.
  *   max_q, max_kv: host bounds on n and on kv_len (they size the launch; 0 takes rows and
  *   max_pages * page_size).  Rows and keys past them are not computed, and reported.

@@ -14,6 +14,12 @@
 // launch, no scratch: 15.6 to 9.9 us for 4 sequences of up to 1000 keys); more, for a few heads over a
 // long cache, join through the workspace and the kernel below.
 //
+// Weights are rounded to the call's type for the product with V (an fp32 operand would be two products);
+// scores, sums and accumulators are fp32, and the sum is of the unrounded weights.  What that costs: 0.0023
+// of the result against 64 bits in bf16 where the output's own rounding makes 0.0017, 0.00028 against 0.00021 in
+// fp16 (root mean squares, 48 tokens over 8-33 thousand keys and 9 chunks).  fp16 weights below 2^-14 of the
+// largest lose bits and below 2^-25 vanish.
+//
 // The running maximum moves only when a score exceeds it by more than 8 (log2 units): until then
 // weights stay below 2^8, exact in the fp32 sums, and no lane has to talk to another.
 #include <cstdint>

@@ -34,7 +34,8 @@
 //     S0(j) ; O1 += P1(j-1) V(j-1) ; S1(j) ; O0 += P0(j) V(j)
 // and O1's last product of a unit follows S0 of the next unit's first tile, so the tensor cores do
 // not drain between units.  A block whose rows all fit Q tile 0 leaves tile 1 out.  Exponentials
-// are taken against the running maximum and kept while the row sum shows every p <= 256; the
+// are taken against the running maximum and kept while the row sum shows every p <= 256 (P is rounded to the
+// call's type, as the tensor cores take it; its sum is fp32 and of the unrounded weights); the
 // first tile of a unit, or a row whose scores rose, takes the tile's maximum first.
 //
 // Masks: a row sees keys below its limit; rows of V past the last key any row of the block sees

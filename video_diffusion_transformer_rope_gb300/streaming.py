@@ -70,7 +70,7 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
     cu: int32 [seqs + 1], rows cu[s]:cu[s+1] belong to sequence s; kv_len: int32 [seqs], keys of each
     sequence with the new ones.  grid = (T, Hgrid, Wgrid): the new token with cache index c stands at
     grid token pos_offset[s] + c.  q_norm / k_norm: [d] weights of a per-head RMS norm applied before
-    the rotation.  Slices of a fused projection are taken as they are.  Two rows of a call must not land in
+    the rotation (a norm over all heads of a token goes before the call).  Slices of a fused projection are taken as they are.  Two rows of a call must not land in
     one slot (a page that two sequences share and both write): it would hold pieces of both."""
     call = (_native or _load()).append
     if stream is None:
