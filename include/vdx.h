@@ -270,11 +270,11 @@ vdx_status vdx_rope3d_append(const vdx_paged_kv* cache, const vdx_append_args* a
 /* Attention of the new tokens over the cache (q already rotated, keys already appended):
  *     lse = log sum_c exp(scale * <q, k_c>),   out = sum_c exp(scale * <q, k_c> - lse) v_c
  * over the visible keys c of row i of its sequence, with p = kv_len - n + i and o = pos_offset[s]
- * (that of the append; pos_offset NULL: 0):
+ * (that of the append, given to vdx_paged_attn_offset; otherwise 0):
  *     c < kv_len,  and with causal_block = m > 0 also  c + o < (floor((p + o) / m) + 1) * m
  * (m = 1: each token sees the tokens up to itself; m = tokens of a latent frame: whole frames up
  * to its own, also where the oldest pages that were dropped end inside a frame; m = 0: every key).
- * A row that sees no key, or whose p is negative, gets out = 0 and lse = -inf.
+ * A row that sees no key, or with m > 0 one whose p is negative, gets out = 0 and lse = -inf.
  * q, k and v enter the products as they are; scores, softmax statistics and accumulators are
  * fp32; the softmax weights are rounded to the call's type for the product with v (fp16: weights below
  * 2^-14 of a row's largest lose bits).  There is no counterpart of qk_precision.
@@ -297,9 +297,11 @@ typedef struct vdx_paged_attn_args {
   float scale;
   void* workspace;
   size_t workspace_bytes;
-  const int32_t* pos_offset;   /* [seqs] or NULL; read with causal_block > 0                      */
 } vdx_paged_attn_args;
 vdx_status vdx_paged_attn(const vdx_paged_kv* cache, const vdx_paged_attn_args* args, void* stream);
+/* With pos_offset (device int32 [seqs], or NULL: as vdx_paged_attn), read where causal_block > 0. */
+vdx_status vdx_paged_attn_offset(const vdx_paged_kv* cache, const vdx_paged_attn_args* args,
+                                 const int32_t* pos_offset, void* stream);
 /* 0 also where the call would be refused: vdx_last_error() is not empty then. */
 size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* cache, const vdx_paged_attn_args* args);
 

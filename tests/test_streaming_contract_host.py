@@ -63,7 +63,7 @@ def test_append_takes_caches_side_by_side(L, ckw):
 
 
 def test_paged_attention_checks_its_position_offsets(L):
-    r = L.vdx_paged_attn(ctypes.byref(_cache()), ctypes.byref(_paged(pos_offset=FAKE + 9 * G + 2)), None)
+    r = L.vdx_paged_attn_offset(ctypes.byref(_cache()), ctypes.byref(_paged()), FAKE + 9 * G + 2, None)
     assert r == B.VDX_ERR_ALIGN and "pos_offset" in L.vdx_last_error().decode(), L.vdx_last_error()
 
 
@@ -121,8 +121,14 @@ def test_append_refuses_outputs_over_lengths_tables_and_weights(L, ckw, kw):
     assert r == B.VDX_ERR_ARG and "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
 
 
+def test_paged_attention_refuses_outputs_over_its_position_offsets(L):
+    for out in (FAKE + 4 * G, FAKE + 5 * G):                       # out, lse
+        r = L.vdx_paged_attn_offset(ctypes.byref(_cache()), ctypes.byref(_paged(causal_block=3)), out + 4, None)
+        assert r == B.VDX_ERR_ARG and "overlaps cu, kv_len" in L.vdx_last_error().decode(), L.vdx_last_error()
+
+
 @pytest.mark.parametrize("ckw,kw", [
-    (dict(), dict(out=FAKE + 7 * G)), (dict(), dict(lse=FAKE + 8 * G)), (dict(), dict(pos_offset=FAKE + 4 * G + 4, causal_block=3)),
+    (dict(), dict(out=FAKE + 7 * G)), (dict(), dict(lse=FAKE + 8 * G)),
     (dict(page_table=FAKE + 5 * G + 7 * 4 * 4 - 4), dict()),
     (dict(page_table=FAKE + 4 * G - 4 * (2 * 8 + 8) + 4), dict()),
 ])

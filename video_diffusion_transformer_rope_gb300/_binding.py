@@ -52,7 +52,7 @@ class PagedAttnArgs(ctypes.Structure):
     """vdx_paged_attn_args (include/vdx.h)."""
     _fields_ = [("q", _p), ("out", _p), ("lse", _p), ("q_row", _ll), ("q_head", _ll), ("rows", _i), ("Hq", _i),
                 ("cu", _p), ("kv_len", _p), ("max_q", _i), ("max_kv", _i), ("causal_block", _i), ("scale", _f),
-                ("workspace", _p), ("workspace_bytes", _z), ("pos_offset", _p)]
+                ("workspace", _p), ("workspace_bytes", _z)]
 
 
 class CrossAttnArgs(ctypes.Structure):
@@ -79,6 +79,7 @@ SIGNATURES = {
     "vdx_rope3d_attn_noalloc": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _d, _f, _p]),
     "vdx_rope3d_append": (_i, [_p, _p, _p]),
     "vdx_paged_attn": (_i, [_p, _p, _p]),
+    "vdx_paged_attn_offset": (_i, [_p, _p, _p, _p]),
     "vdx_paged_attn_workspace_bytes": (ctypes.c_size_t, [_p, _p]),
     "vdx_cross_attn": (_i, [_p, _p]),
     "vdx_cross_attn_workspace_bytes": (ctypes.c_size_t, [_p]),

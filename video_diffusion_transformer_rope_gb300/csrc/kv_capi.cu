@@ -243,7 +243,7 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
   return VDX_OK;
 }
 
-vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bool size_only, Problem* pb) {
+vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, const int32_t* pos_offset, bool size_only, Problem* pb) {
   if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
   if (vdx_status s = check_cache(c, a->Hq)) return s;
   if (a->rows < 0 || a->max_q < 0 || a->max_kv < 0 || a->causal_block < 0)
@@ -256,7 +256,7 @@ vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bo
   p.q_b = 0; p.q_t = a->q_row; p.q_h = a->q_head;
   p.k_p = c->k_page; p.k_t = c->k_token; p.k_h = c->k_head;
   p.v_p = c->v_page; p.v_t = c->v_token; p.v_h = c->v_head;
-  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->causal_block ? a->pos_offset : nullptr; p.table = c->page_table;
+  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->causal_block ? pos_offset : nullptr; p.table = c->page_table;
   p.table_stride = c->table_stride;
   p.max_pages = c->max_pages; p.num_pages = c->num_pages; p.P = c->page_size;
   p.S = c->seqs; p.N = a->rows; p.Hq = a->Hq; p.Hkv = c->Hkv; p.g = a->Hq / c->Hkv;
@@ -268,7 +268,7 @@ vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, bo
   if (!q.empty()) {
     if (vdx_status s = check_i32("cu", a->cu, false)) return s;
     if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
-    if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
+    if (vdx_status s = check_i32("pos_offset", pos_offset, true)) return s;
   }
   return finish(pb, q, cache_tensor(*c, false), cache_tensor(*c, true),
                 static_cast<long long>(a->rows) * a->Hq * c->d, a->lse ? static_cast<long long>(a->rows) * a->Hq : 0,
@@ -494,14 +494,22 @@ vdx_status vdx_paged_attn(const vdx_paged_kv* c, const vdx_paged_attn_args* a, v
   NvtxScope nvtx("vdx_paged_attn");
   clear_error();
   Problem pb;
-  if (vdx_status s = paged_problem(c, a, false, &pb)) return s;
+  if (vdx_status s = paged_problem(c, a, nullptr, false, &pb)) return s;
+  return launch(pb, stream);
+}
+
+vdx_status vdx_paged_attn_offset(const vdx_paged_kv* c, const vdx_paged_attn_args* a, const int32_t* pos_offset, void* stream) {
+  NvtxScope nvtx("vdx_paged_attn_offset");
+  clear_error();
+  Problem pb;
+  if (vdx_status s = paged_problem(c, a, pos_offset, false, &pb)) return s;
   return launch(pb, stream);
 }
 
 size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* c, const vdx_paged_attn_args* a) {
   clear_error();
   Problem pb;
-  return paged_problem(c, a, true, &pb) == VDX_OK ? pb.workspace : 0;
+  return paged_problem(c, a, nullptr, true, &pb) == VDX_OK ? pb.workspace : 0;
 }
 
 vdx_status vdx_cross_attn(const vdx_cross_attn_args* a, void* stream) {

@@ -29,7 +29,7 @@ namespace {
 
 PyObject* g_error = nullptr;                       // VdxError, set by bind()
 decltype(&vdx_rope3d_append) g_append = nullptr;
-decltype(&vdx_paged_attn) g_paged = nullptr;
+decltype(&vdx_paged_attn_offset) g_paged = nullptr;
 decltype(&vdx_paged_attn_workspace_bytes) g_paged_size = nullptr;
 decltype(&vdx_cross_attn) g_cross = nullptr;
 decltype(&vdx_cross_attn_workspace_bytes) g_cross_size = nullptr;
@@ -329,10 +329,10 @@ PyObject* paged(PyObject* const* a) {
   const at::Tensor& q = paged_args(a, &c, &x);
   x.causal_block = integer("causal_block", a[8]);
   x.scale = static_cast<float>(real(a[9]));
-  x.pos_offset = int32s("pos_offset", a[14], q, c.seqs);
+  const int32_t* pos_offset = int32s("pos_offset", a[14], q, c.seqs);
   const int64_t lse_shape[2] = {x.Hq, x.rows};
   return attention(x, q, lse_shape, a[10], a[11], a[12], a[13], [&] { return g_paged_size(&c, &x); },
-                   [&](void* stream) { return g_paged(&c, &x, stream); });
+                   [&](void* stream) { return g_paged(&c, &x, pos_offset, stream); });
 }
 PyObject* paged_size(PyObject* const* a) {
   vdx_paged_kv c{};

@@ -34,7 +34,7 @@ def _load():
         raise RuntimeError(f"the streaming calls were built for PyTorch {native.TORCH_VERSION}, this is {torch.__version__}: "
                            "build them again with video_diffusion_transformer_rope_gb300._build.build()")
     native.bind(VdxError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.vdx_rope3d_append, L.vdx_paged_attn, L.vdx_paged_attn_workspace_bytes, L.vdx_cross_attn,
+        L.vdx_rope3d_append, L.vdx_paged_attn_offset, L.vdx_paged_attn_workspace_bytes, L.vdx_cross_attn,
         L.vdx_cross_attn_workspace_bytes, L.vdx_last_error)))
     _native = native
     return native
