@@ -326,6 +326,101 @@ typedef struct vdx_cross_attn_args {
 vdx_status vdx_cross_attn(const vdx_cross_attn_args* args, void* stream);
 size_t vdx_cross_attn_workspace_bytes(const vdx_cross_attn_args* args);
 
+/* ---- The same cache in 8 bits: half the memory, and half the bytes to read.
+ * k and v of a vdx_paged_kv hold e4m3 bytes (strides in elements, that is bytes, multiples of 16), its dtype is that
+ * of the call's other tensors.  A block is VDX_KV8_BLOCK consecutive tokens of a page (the last one of a page
+ * may be short); for each block and head there is a scale 2^e, held as the byte e + 127 (e8m0), and a value is
+ * its code times that scale.  e lies in [VDX_KV8_MIN_EXP, VDX_KV8_MAX_EXP], within which every value is exact in
+ * bf16 and in fp16; bytes outside are read as the nearer end.  With scales that are powers of two a value
+ * keeps its four significant bits whatever the scale, down to 2^-13 of the block's largest (where that is above 2^-7).
+ * What is said above of page sizes, page tables, lengths, heads, streams and reports holds here too. */
+#define VDX_KV8_BLOCK 16
+#define VDX_KV8_MIN_EXP (-15)
+#define VDX_KV8_MAX_EXP 7
+typedef struct vdx_kv8_scales {
+  uint8_t* k;               /* [num_pages, ceil(page_size / VDX_KV8_BLOCK), Hkv], strides in bytes   */
+  uint8_t* v;
+  long long k_page, k_block, k_head, v_page, v_block, v_head;
+} vdx_kv8_scales;
+
+/* vdx_rope3d_append into such a cache.  Keys (normed and rotated) and values go from fp32 to e4m3 with one
+ * rounding, to nearest even, after the block's scale has been found: the least e with |x| <= 448 * 2^e for all new
+ * values x of the block, and for a block whose first token is older than this call, not less than its e so far.
+ * Where e grows the older codes are rounded again (exact, but for those that become e4m3's subnormals).  So a
+ * sequence appended at once and one appended token by token may differ by that.  A block whose first token is new
+ * starts afresh, whatever page and scale held.  Values past 448 * 2^7 are clamped to it and
+ * vdx_sync_check reports VDX_ERR_RANGE; NaN stays NaN.
+ * A block belongs to one sequence: two sequences that share a page (a common prefix) must not append into
+ * a block of it.  q and q_out as in vdx_rope3d_append. */
+vdx_status vdx_rope3d_append8(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_append_args* args, void* stream);
+
+/* vdx_paged_attn_offset over such a cache.  Codes and scales enter the products as the values they stand for; the
+ * softmax weights are rounded to fp16 after a multiplication by 2^7 (weights below 2^-21 of a row's
+ * largest lose bits, below 2^-32 they vanish) where a kv head has at most 32 rows, else to the call's type. */
+vdx_status vdx_paged_attn8(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_paged_attn_args* args,
+                           const int32_t* pos_offset, void* stream);
+/* 0 also where the call would be refused: vdx_last_error() is not empty then. */
+size_t vdx_paged_attn8_workspace_bytes(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_paged_attn_args* args);
+
+/* ---- Which keys are worth their place: the weight that each cached key gathers, and eviction.
+ *
+ * After vdx_paged_attn (or vdx_paged_attn8), with its q, cu, kv_len, causal_block, scale and lse: for every sequence s
+ * that has rows in the call, kv head h and key c < kv_len[s],
+ *     w[s, h, c] = (c < kv_len[s] - n ? decay * w[s, h, c] : 0) + sum over rows i that see c and query heads a of
+ *                  h's group of exp(scale * <q_(i,a), k_c> - lse[a, i])
+ * so that a key starts at 0 with the call that brings it (the buffer needs no clearing), and the entries of a
+ * sequence sum to the rows it has had times Hq / Hkv where decay is 1.  Other entries are left as they were.
+ * fp32 arithmetic; each entry is summed by one thread block in an order that the call's shape fixes, so the same call
+ * gives the same bits.  A row whose lse is -inf (it saw no key) adds nothing, one whose lse is NaN makes its keys'
+ * entries NaN.
+ *   scales: NULL for a 16-bit cache.  The cache's values are not read.
+ *   w: float32 [seqs, Hkv, width], the entries of a head contiguous; kv_len past width or max_kv is clamped and
+ *   reported.  pos_offset as in vdx_paged_attn_offset. */
+typedef struct vdx_paged_weights_args {
+  const void* q;            /* [rows, Hq, d]                                                      */
+  const float* lse;         /* [Hq, rows]                                                         */
+  float* w;
+  long long q_row, q_head, w_seq, w_head;   /* strides                                            */
+  int width;
+  int rows, Hq;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* pos_offset;   /* [seqs] or NULL                                                  */
+  int max_q, max_kv;        /* host bounds, as in vdx_paged_attn                                  */
+  int causal_block;
+  float scale;
+  float decay;              /* finite                                                             */
+} vdx_paged_weights_args;
+vdx_status vdx_paged_attn_weights(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_paged_weights_args* args,
+                                  void* stream);
+
+/* Eviction: of every sequence's L = kv_len[s] keys at most `keep` stay, for each kv head its own.  Where L > keep
+ * these are the last `recent` and, of the others, the keep - recent with the largest w (of equals the one with
+ * the lowest index; NaN counts as the largest); otherwise all.  Keys and values of a head that stay move, in their order,
+ * to cache indices 0, 1, .. of the same sequence of `into`: the same kind of cache by another page table, and
+ * possibly in the same pools, whose pages the call must not read too (the old pages are free afterwards).  In 8 bits the
+ * blocks of `into` get scales by the rule of vdx_rope3d_append8, as if the values were appended at once.
+ * Written beside: kv_len_out[s] = min(L, keep); pos_offset_out[s] = pos_offset[s] + L - kv_len_out[s] (NULL: not
+ * wanted), with which the next token appended stands where it would have stood; index[s, h, j], the old
+ * cache index of the key that is now at j, and w_out[s, h, j], its weight (both for j < keep; -1 and 0 past the new length).
+ *   w_out may be w (same strides); otherwise outputs must not overlap inputs, nor each other.
+ *   max_kv: host bound on L (0: what the page table and width hold); L past it is clamped and reported.
+ *   Slots of `into` that `into`'s table does not reach, or whose page is outside it, are skipped and reported. */
+typedef struct vdx_paged_evict_args {
+  const float* w;           /* [seqs, Hkv, width], the entries of a head contiguous               */
+  float* w_out;             /* [seqs, Hkv, >= keep]                                               */
+  long long w_seq, w_head, w_out_seq, w_out_head;   /* strides                                    */
+  int width;
+  const int32_t* kv_len;
+  const int32_t* pos_offset;   /* [seqs] or NULL: 0                                               */
+  int32_t* kv_len_out;
+  int32_t* pos_offset_out;  /* [seqs] or NULL                                                     */
+  int32_t* index;           /* [seqs, Hkv, keep] contiguous                                       */
+  int keep, recent, max_kv; /* keep >= 1, 0 <= recent <= keep                                     */
+} vdx_paged_evict_args;
+vdx_status vdx_paged_evict(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_paged_kv* into,
+                           const vdx_kv8_scales* into_scales, const vdx_paged_evict_args* args, void* stream);
+
 /* Synchronise `stream`, then read and clear the device error word.  Returns VDX_OK,
  * VDX_ERR_TIMEOUT (a kernel gave up on a pipeline wait; the output of that call is
  * undefined), VDX_ERR_RANGE (a rotated q/k value was clamped to the fp16 range; the output

@@ -63,6 +63,26 @@ class CrossAttnArgs(ctypes.Structure):
                 ("d", _i), ("dtype", _i), ("kv_len", _p), ("scale", _f), ("workspace", _p), ("workspace_bytes", _z)]
 
 
+class Kv8Scales(ctypes.Structure):
+    """vdx_kv8_scales (include/vdx.h)."""
+    _fields_ = [("k", _p), ("v", _p), ("k_page", _ll), ("k_block", _ll), ("k_head", _ll), ("v_page", _ll), ("v_block", _ll),
+                ("v_head", _ll)]
+
+
+class PagedWeightsArgs(ctypes.Structure):
+    """vdx_paged_weights_args (include/vdx.h)."""
+    _fields_ = [("q", _p), ("lse", _p), ("w", _p), ("q_row", _ll), ("q_head", _ll), ("w_seq", _ll), ("w_head", _ll), ("width", _i),
+                ("rows", _i), ("Hq", _i), ("cu", _p), ("kv_len", _p), ("pos_offset", _p), ("max_q", _i), ("max_kv", _i),
+                ("causal_block", _i), ("scale", _f), ("decay", _f)]
+
+
+class PagedEvictArgs(ctypes.Structure):
+    """vdx_paged_evict_args (include/vdx.h)."""
+    _fields_ = [("w", _p), ("w_out", _p), ("w_seq", _ll), ("w_head", _ll), ("w_out_seq", _ll), ("w_out_head", _ll), ("width", _i),
+                ("kv_len", _p), ("pos_offset", _p), ("kv_len_out", _p), ("pos_offset_out", _p), ("index", _p), ("keep", _i),
+                ("recent", _i), ("max_kv", _i)]
+
+
 # name -> (restype, argtypes); mirrors include/vdx.h
 SIGNATURES = {
     "vdx_rope3d_attn": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _d, _f, _p]),
@@ -81,6 +101,11 @@ SIGNATURES = {
     "vdx_paged_attn": (_i, [_p, _p, _p]),
     "vdx_paged_attn_offset": (_i, [_p, _p, _p, _p]),
     "vdx_paged_attn_workspace_bytes": (ctypes.c_size_t, [_p, _p]),
+    "vdx_rope3d_append8": (_i, [_p, _p, _p, _p]),
+    "vdx_paged_attn8": (_i, [_p, _p, _p, _p, _p]),
+    "vdx_paged_attn8_workspace_bytes": (ctypes.c_size_t, [_p, _p, _p]),
+    "vdx_paged_attn_weights": (_i, [_p, _p, _p, _p]),
+    "vdx_paged_evict": (_i, [_p, _p, _p, _p, _p, _p]),
     "vdx_cross_attn": (_i, [_p, _p]),
     "vdx_cross_attn_workspace_bytes": (ctypes.c_size_t, [_p]),
     "vdx_sync_check": (_i, [_p]),

@@ -1,0 +1,63 @@
+// Device helpers of the 8-bit cache: e4m3 codes of 16-token blocks with a power of two as scale.
+//
+// A value is code * 2^e.  With e in [-15, 7] it is exact in bf16 and in fp16: the largest is 448 * 2^7 = 57344, the
+// smallest step 2^-9 * 2^-15 = 2^-24, fp16's own.
+#pragma once
+#include <cuda_fp16.h>
+#include <cstdint>
+
+namespace vdx {
+
+constexpr int kBlock8 = 16;
+constexpr int kMinExp8 = -15, kMaxExp8 = 7;
+
+// The least e in range with amax <= 448 * 2^e = 1.75 * 2^(8 + e); amax >= 0, infinity included.
+__device__ __forceinline__ int block_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kMinExp8), kMaxExp8);
+}
+__device__ __forceinline__ int scale_exponent(uint8_t byte) {
+  return min(max(static_cast<int>(byte) - 127, kMinExp8), kMaxExp8);
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// 2^e as both halves of a pair of fp16; e >= -14 is normal, -15 the subnormal 2^-15.
+__device__ __forceinline__ uint32_t half_two_to(int e) {
+  return e > kMinExp8 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
+}
+
+// Two floats to codes, nearest even, clamped to 448; the first in the low byte.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  return encode2(a, b) | (encode2(c, d) << 16);
+}
+// The two codes of the low (kHigh: high) half of w as a pair of fp16, exactly.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t decode2(uint32_t w) {
+  uint32_t r;
+  if (kHigh)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void decode8(const uint2& x, float (&f)[8]) {
+  const uint32_t h[4] = {decode2<false>(x.x), decode2<true>(x.x), decode2<false>(x.y), decode2<true>(x.y)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+
+}  // namespace vdx

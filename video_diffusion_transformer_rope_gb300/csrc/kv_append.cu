@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "kv8.cuh"
 #include "kv_common.cuh"
 
 namespace vdx {
@@ -39,6 +40,30 @@ constexpr int kResident = 9;        // blocks that a multiprocessor holds at lea
 // 3 x 40; 4 rows of 256 threads and 8 tokens 17.5 and 220 us; 8 rows 24 and 303 us.
 template <int kTok>
 constexpr int kRowsInFlight = kTok > 2 ? 3 : 1;
+
+// 8 channels of a row, d/8 lanes together: the norm, if there is one, and the turn of their pairs by cs[0..3].
+template <int D>
+__device__ __forceinline__ void norm_rotate(float (&f)[8], bool norm, const float (&w)[8], float eps, const float2* cs) {
+  if (norm) {
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    const float inv = rsqrtf(sq * (1.f / D) + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= inv * w[i];
+  }
+  const float4* c4 = reinterpret_cast<const float4*>(cs);
+  const float4 c01 = c4[0], c23 = c4[1];
+  const float cn[4] = {c01.x, c01.z, c23.x, c23.z}, sn[4] = {c01.y, c01.w, c23.y, c23.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float u = f[2 * i], v = f[2 * i + 1];
+    f[2 * i] = fmaf(u, cn[i], -v * sn[i]);
+    f[2 * i + 1] = fmaf(u, sn[i], v * cn[i]);
+  }
+}
 
 // The (token, head) rows of one tensor of a block's tokens, walked by groups of d/8 lanes, kUnroll
 // loads in flight per lane.  One instance per kind (0 q, 1 k, 2 v), so a row carries no choices: with
@@ -55,7 +80,8 @@ struct RowWalk {
   uint4 weights;               // this lane's 8 of the norm's, if there is one
   uint4 x[kUnroll];
   int tok[kUnroll], head[kUnroll];      // tok < 0: past the block's rows
-  __device__ __forceinline__ void init(const AppendParams& p, int row0) {
+  // by, ny: which of how many blocks share the heads of these tokens
+  __device__ __forceinline__ void init(const AppendParams& p, int row0, int by, int ny) {
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes;
     heads = kKind == 0 ? p.Hq : p.Hkv;
@@ -71,9 +97,9 @@ struct RowWalk {
     src += row0 * src_row;
     if (kKind == 0) dst += row0 * dst_row;
     rows = heads > 0 ? min(kTok, p.rows - row0) : 0;
-    step = (kThreads / kLanes) * gridDim.y;
+    step = (kThreads / kLanes) * ny;
     j = 0;
-    h = blockIdx.y * (kThreads / kLanes) + threadIdx.x / kLanes;
+    h = by * (kThreads / kLanes) + threadIdx.x / kLanes;
     wrap();
   }
   __device__ __forceinline__ void wrap() {
@@ -108,25 +134,7 @@ struct RowWalk {
       if (kKind < 2) {
         float f[8];
         unpack8<T>(x[e], f);
-        if (norm) {
-          float sq = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
-#pragma unroll
-          for (int o = D / 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-          const float inv = rsqrtf(sq * (1.f / D) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= inv * w[i];
-        }
-        const float4* c4 = reinterpret_cast<const float4*>(&cs[t][lane * 4]);
-        const float4 c01 = c4[0], c23 = c4[1];
-        const float cn[4] = {c01.x, c01.z, c23.x, c23.z}, sn[4] = {c01.y, c01.w, c23.y, c23.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = f[2 * i], v = f[2 * i + 1];
-          f[2 * i] = fmaf(u, cn[i], -v * sn[i]);
-          f[2 * i + 1] = fmaf(u, sn[i], v * cn[i]);
-        }
+        norm_rotate<D>(f, norm, w, p.eps, &cs[t][lane * 4]);
         y = pack8<T>(f);
       }
       if (tok[e] < 0 || at[t] < 0) continue;
@@ -138,14 +146,33 @@ struct RowWalk {
   }
 };
 
+// Every sequence's range is looked at (a row's look-up sees only its own), 32 of them by a warp of each of n blocks:
+// many blocks for many sequences.
+__device__ __forceinline__ void look_at_ranges(const AppendParams& p, int block, int n) {
+  bool bad = false;
+  for (long long s = block * 32ll + (threadIdx.x & 31); s < p.S; s += n * 32ll) {
+    const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
+    bad = bad || begin < 0 || end < begin || end > p.rows;
+  }
+  if (bad) atomicOr(&g_error_word, kErrLength);
+}
+
+// Cosine and sine of channel pair `pr` at position x of its axis.
+__device__ __forceinline__ float2 cos_sin(const AppendParams& p, int pr, unsigned x) {
+  const int hi = static_cast<int>((static_cast<unsigned long long>(x) * p.turn[pr]) >> 32);        // turns in [-1/2, 1/2) * 2^32
+  float sn, cn;
+  sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);
+  return make_float2(cn, sn);
+}
+
 template <typename T, int D, int kTok, int kKind>
-__device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
+__device__ __forceinline__ void append_rows(const AppendParams& p, int row0, int by, int ny) {
   __shared__ __align__(16) float2 cs[kTok][D / 2];
   __shared__ long long s_at[kTok];    // where each token goes: cache offset, or grid token for q; < 0: nowhere
   __shared__ int s_axis[kTok][3];     // its (t, h, w)
   const int tid = threadIdx.x;
   RowWalk<T, D, kTok, kKind> rows;
-  rows.init(p, row0);
+  rows.init(p, row0, by, ny);
   rows.load();
 
   for (int j = tid >> 5; j < kTok; j += kThreads / 32) {     // one warp per token
@@ -191,25 +218,12 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int row0) {
       s_axis[j][2] = col;
     }
   }
-  // Every sequence's range is looked at (a row's look-up sees only its own), 32 of them by a warp of each block:
-  // many blocks for many sequences.
-  if (kKind == 1 && blockIdx.y == 0 && tid >= kThreads - 32) {
-    bool bad = false;
-    for (long long s = blockIdx.x * 32ll + (tid & 31); s < p.S; s += gridDim.x * 32ll) {
-      const int begin = load_i32(p.cu + s), end = load_i32(p.cu + s + 1);
-      bad = bad || begin < 0 || end < begin || end > p.rows;
-    }
-    if (bad) atomicOr(&g_error_word, kErrLength);
-  }
+  if (kKind == 1 && by == 0 && tid >= kThreads - 32) look_at_ranges(p, blockIdx.x, gridDim.x);
   __syncthreads();
   if (kKind < 2) {
     for (int i = tid; i < kTok * (D / 2); i += kThreads) {
       const int j = i / (D / 2), pr = i % (D / 2);
-      const unsigned long long x = static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]);
-      const int hi = static_cast<int>((x * p.turn[pr]) >> 32);        // turns in [-1/2, 1/2) * 2^32
-      float sn, cn;
-      sincospif(static_cast<float>(hi) * 0x1p-31f, &sn, &cn);
-      cs[j][pr] = make_float2(cn, sn);
+      cs[j][pr] = cos_sin(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
     }
     __syncthreads();
   }
@@ -225,11 +239,198 @@ kv_append(const __grid_constant__ AppendParams p) {
   // wait for memory three times over.  What a row reads depends on its number alone, so the first batch
   // is under way before the block has looked up its tokens' sequences and pages.
   if (blockIdx.z == 0)
-    append_rows<T, D, kTok, 1>(p, row0);
+    append_rows<T, D, kTok, 1>(p, row0, blockIdx.y, gridDim.y);
   else if (blockIdx.z == 1)
-    append_rows<T, D, kTok, 2>(p, row0);
+    append_rows<T, D, kTok, 2>(p, row0, blockIdx.y, gridDim.y);
   else
-    append_rows<T, D, kTok, 0>(p, row0);
+    append_rows<T, D, kTok, 0>(p, row0, blockIdx.y, gridDim.y);
+}
+
+// ------------------------------------------------------------------------------------------ into an 8-bit cache
+// The scale of a block of 16 tokens and a head comes from all of its new values, so a warp takes the whole block of
+// a head: its rows are loaded, normed and turned into registers (d/8 lanes a row), their largest |x| is a shuffle
+// maximum, and the codes leave, 8 bytes a lane.  Where older tokens of the block must be rounded again, the same warp
+// does that too, so nothing is shared between warps.
+//
+// A thread block takes the blocks ("segments") of the cache whose first new token is among its kRows8 rows, for keys or
+// values; a segment may reach up to 15 rows further.  One warp looks up those 31 rows, one to a lane.
+constexpr int kRows8 = 16;
+constexpr int kWindow8 = kRows8 + kBlock8 - 1;
+
+struct Segment8 {
+  int row, count;              // first row in the window, new tokens
+  int older;                   // tokens of the block ahead of them
+  int fits;                    // bit i: the i-th token has a place
+  long long at, scale;         // cache offset of the block's first token, offset of its scales (head 0)
+};
+
+// The last s in [0, S) with cu[s] <= r, by one lane alone (find_sequence has the conditions).
+__device__ __forceinline__ int find_sequence_lane(const int* cu, int S, int r) {
+  int lo = 0, n = S;
+  while (n > 1) {
+    const int half = n / 2;
+    if (load_i32(cu + lo + half) <= r) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
+template <typename T, int D, bool kKeys>
+__device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int nx, int by, int ny) {
+  constexpr int kLanes = D / 8;                  // of a row
+  constexpr int kPer = 32 / kLanes;              // rows of a warp's step
+  constexpr int kSteps = kBlock8 / kPer;
+  __shared__ __align__(16) float2 cs[kKeys ? kWindow8 : 1][D / 2];
+  __shared__ Segment8 segs[kRows8];
+  __shared__ int s_axis[kWindow8][3];
+  __shared__ int s_count;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row0 = bx * kRows8;
+
+  if (warp == 0) {
+    const int r = row0 + lane;
+    int seq = 0, begin = 0, end = 0, slot = 0, page = -1, axis[3] = {0, 0, 0};
+    bool mine = false, fits = false, bad_page = false, bad_position = false;
+    if (lane < kWindow8 && r < p.rows) {
+      seq = find_sequence_lane(p.cu, p.S, r);
+      begin = load_i32(p.cu + seq);
+      end = load_i32(p.cu + seq + 1);
+      mine = begin >= 0 && end >= begin && end <= p.rows && r >= begin && r < end;      // broken ranges: look_at_ranges
+    }
+    if (mine) {
+      const long long c = static_cast<long long>(load_i32(p.kv_len + seq)) - (end - begin) + (r - begin);
+      const long long pos = c + (p.pos_offset ? load_i32(p.pos_offset + seq) : 0);
+      if (c < 0 || c >= static_cast<long long>(p.max_pages) * p.P) {
+        mine = false;
+        bad_position = true;
+      } else {
+        const int pg = static_cast<int>(c / p.P);
+        slot = static_cast<int>(c - static_cast<long long>(pg) * p.P);
+        page = load_i32(p.table + seq * p.table_stride + pg);
+        bad_page = page < 0 || page >= p.num_pages;
+        fits = pos >= 0 && pos < static_cast<long long>(p.T) * p.Hg * p.Wg;
+        bad_position = !fits;
+        if (fits) {
+          const int area = p.Hg * p.Wg;
+          axis[0] = static_cast<int>(pos / area);
+          const int rest = static_cast<int>(pos - static_cast<long long>(axis[0]) * area);
+          axis[1] = rest / p.Wg;
+          axis[2] = rest - axis[1] * p.Wg;
+        }
+      }
+    }
+    if (lane < kRows8 && (bad_page || bad_position)) atomicOr(&g_error_word, (bad_page ? kErrPage : 0u) | (bad_position ? kErrPosition : 0u));
+    if (lane < kWindow8)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s_axis[lane][i] = axis[i];
+    const unsigned placed = __ballot_sync(0xffffffffu, fits);
+    // a segment starts with its sequence's first new row or a block's first token (so does index 0, whatever is before it)
+    const bool leads = mine && lane < kRows8 && !bad_page && (slot % kBlock8 == 0 || r == begin);
+    const unsigned all = __ballot_sync(0xffffffffu, leads);
+    if (leads) {
+      Segment8& g = segs[__popc(all & ((1u << lane) - 1))];
+      g.row = lane;
+      g.older = slot % kBlock8;
+      g.count = min(min(kBlock8 - g.older, p.P - slot), end - r);
+      g.fits = static_cast<int>((placed >> lane) & ((1u << g.count) - 1));
+      const long long tok = slot - g.older;
+      g.at = kKeys ? page * p.kc_page + tok * p.kc_token : page * p.vc_page + tok * p.vc_token;
+      const Scales8& sc = p.scales;
+      g.scale = kKeys ? page * sc.k_page + tok / kBlock8 * sc.k_block : page * sc.v_page + tok / kBlock8 * sc.v_block;
+    }
+    if (lane == 0) s_count = __popc(all);
+  }
+  if (kKeys && by == 0 && warp == 1) look_at_ranges(p, bx, nx);
+  __syncthreads();
+  const int count = s_count;
+  if (count == 0) return;
+  if (kKeys) {
+    const int from = segs[0].row, to = segs[count - 1].row + segs[count - 1].count;
+    for (int i = from * (D / 2) + tid; i < to * (D / 2); i += kThreads) {
+      const int j = i / (D / 2), pr = i % (D / 2);
+      cs[j][pr] = cos_sin(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
+    }
+    __syncthreads();
+  }
+
+  const T* src = static_cast<const T*>(kKeys ? p.k : p.v);
+  const long long src_row = kKeys ? p.k_row : p.v_row, src_head = kKeys ? p.k_head : p.v_head;
+  const long long dst_token = kKeys ? p.kc_token : p.vc_token, dst_head = kKeys ? p.kc_head : p.vc_head;
+  uint8_t* cache = static_cast<uint8_t*>(kKeys ? p.k_cache : p.v_cache);
+  uint8_t* scale = kKeys ? p.scales.k : p.scales.v;
+  const long long scale_head = kKeys ? p.scales.k_head : p.scales.v_head;
+  const int ch = lane % kLanes, sub = lane / kLanes;
+  const bool norm = kKeys && p.k_norm;
+  float w[8];
+  unpack8<T>(norm ? load_b128(static_cast<const T*>(p.k_norm) + ch * 8) : make_uint4(0u, 0u, 0u, 0u), w);
+  bool past = false;
+  for (int t = by * (kThreads / 32) + warp; t < count * p.Hkv; t += ny * (kThreads / 32)) {
+    const int si = t / p.Hkv, h = t - si * p.Hkv;
+    const Segment8 g = segs[si];
+    const T* from = src + static_cast<long long>(row0 + g.row) * src_row + h * src_head + ch * 8;
+    uint8_t* to = cache + g.at + h * dst_head + ch * 8;
+    uint8_t* to_scale = scale + g.scale + h * scale_head;
+    uint4 x[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int j = i * kPer + sub;
+      x[i] = (g.fits >> j & 1) ? load_b128(from + j * src_row) : make_uint4(0u, 0u, 0u, 0u);      // 0 or NaN below: no maximum
+    }
+    const int e_old = g.older ? scale_exponent(*to_scale) : kMinExp8;
+    float f[kSteps][8];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      unpack8<T>(x[i], f[i]);
+      if (kKeys) norm_rotate<D>(f[i], norm, w, p.eps, &cs[min(g.row + i * kPer + sub, kWindow8 - 1)][ch * 4]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(f[i][c]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    past |= top > 448.f * 128.f;
+    const int e = max(e_old, block_exponent(top));
+    const float inv = two_to(-e);
+    if (g.older && e > e_old) {
+      const float down = two_to(e_old - e);
+      for (int j = sub; j < g.older; j += kPer) {
+        uint2* q = reinterpret_cast<uint2*>(to + j * dst_token);
+        float v[8];
+        decode8(*q, v);
+        *q = make_uint2(encode4(v[0] * down, v[1] * down, v[2] * down, v[3] * down),
+                        encode4(v[4] * down, v[5] * down, v[6] * down, v[7] * down));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int j = i * kPer + sub;
+      if (!(g.fits >> j & 1)) continue;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[i][c] *= inv;
+      *reinterpret_cast<uint2*>(to + (g.older + j) * dst_token) =
+          make_uint2(encode4(f[i][0], f[i][1], f[i][2], f[i][3]), encode4(f[i][4], f[i][5], f[i][6], f[i][7]));
+    }
+    if (lane == 0 && g.fits) *to_scale = static_cast<uint8_t>(e + 127);
+  }
+  if (past) atomicOr(&g_error_word, kErrRange8);
+}
+
+template <typename T, int D, int kTok>
+__global__ void __launch_bounds__(kThreads)
+kv_append8(const __grid_constant__ AppendParams p, const int nx, const int ny, const int qx) {
+  wait_for_earlier_work();
+  // keys, values and queries side by side, as in kv_append; the first two by blocks of kRows8 rows
+  const int b = blockIdx.x, each = nx * ny;
+  if (b < each)
+    append_blocks<T, D, true>(p, b % nx, nx, b / nx, ny);
+  else if (b < 2 * each)
+    append_blocks<T, D, false>(p, (b - each) % nx, nx, (b - each) / nx, ny);
+  else
+    append_rows<T, D, kTok, 0>(p, (b - 2 * each) % qx * kTok, (b - 2 * each) / qx, (gridDim.x - 2 * each) / qx);
 }
 
 template <typename T, int D, int kTok>
@@ -266,7 +467,35 @@ cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
   return pairs <= static_cast<long long>(kResident) * sms ? launch_tok<T, D, 2>(p, sms, stream) : launch_tok<T, D, 4>(p, sms, stream);
 }
 
+template <typename T, int D>
+cudaError_t launch8(const AppendParams& p, int sms, cudaStream_t stream) {
+  constexpr int kTok = 2, kGroups = kThreads / (D / 8), kWarps = kThreads / 32;
+  const int nx = (p.rows - 1) / kRows8 + 1, qx = p.Hq > 0 ? (p.rows - 1) / kTok + 1 : 0;
+  int ny = 1, qy = 1;
+  const int most = (p.Hkv * kRows8 + kWarps - 1) / kWarps, q_most = (kTok * p.Hq + kGroups - 1) / kGroups;
+  while (ny < most && 2ll * nx * ny < 2ll * sms) ny *= 2;
+  while (qy < q_most && static_cast<long long>(qx) * qy < 2ll * sms) qy *= 2;
+  ny = ny < most ? ny : most;
+  qy = qy < q_most || qx == 0 ? qy : q_most;
+  const long long blocks = 2ll * nx * ny + static_cast<long long>(qx) * qy;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = launch_early();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_append8<T, D, kTok>, p, nx, ny, qx);
+}
+
 }  // namespace
+
+cudaError_t launch_append8(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream) {
+  note_launch();
+  if (dtype == 0) return d == 128 ? launch8<__nv_bfloat16, 128>(p, sms, stream) : launch8<__nv_bfloat16, 64>(p, sms, stream);
+  return d == 128 ? launch8<__half, 128>(p, sms, stream) : launch8<__half, 64>(p, sms, stream);
+}
 
 cudaError_t launch_append(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream) {
   note_launch();

@@ -2,186 +2,13 @@
 // dispatch.  Nothing here allocates, synchronises or keeps state between calls.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
-#include <numeric>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "kv_internal.h"
-#include "vdx.h"
+#include "kv_checks.h"
 
 namespace {
 
-vdx_status fail(vdx_status s, const char* fmt, ...) noexcept {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  try {
-    vdx::set_last_error(buf);
-  } catch (...) {               // no memory for the message: the status still says what happened
-  }
-  return s;
-}
-void clear_error() noexcept { fail(VDX_OK, "%s", ""); }
-
-struct NvtxScope {
-  explicit NvtxScope(const char* name) { nvtxRangePushA(name); }
-  ~NvtxScope() { nvtxRangePop(); }
-};
-
-int multiprocessors() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
-    cudaGetLastError();
-    return 152;
-  }
-  return sms;
-}
-
-// A strided [n0, n1, n2, d] tensor of 2-byte elements; extents of 0 make it empty.
-struct Tensor {
-  const void* ptr;
-  long long n[3];
-  long long stride[3];
-  int d;
-  bool empty() const { return n[0] == 0 || n[1] == 0 || n[2] == 0; }
-  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(ptr); }
-  uintptr_t end() const {
-    if (empty()) return begin();
-    long long last = d;
-    for (int i = 0; i < 3; ++i) last += (n[i] - 1) * stride[i];
-    return begin() + static_cast<uintptr_t>(last) * 2;
-  }
-};
-bool overlap(const Tensor& a, const Tensor& b) {
-  return !a.empty() && !b.empty() && a.begin() < b.end() && b.begin() < a.end();
-}
-bool overlap(const Tensor& a, const void* p, size_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
-  return p && bytes && !a.empty() && a.begin() < x + bytes && x < a.end();
-}
-
-// What a call reads beside its tensors: lengths, page tables, weights.
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
-Span ints(const int* p, long long n) { return {p, n > 0 ? static_cast<size_t>(n) * 4 : 0}; }
-Span table_span(const int* table, int seqs, long long stride, int max_pages) {
-  return ints(table, seqs > 0 ? (seqs - 1) * stride + max_pages : 0);
-}
-
-// Whether no row of `a` shares an element with a row of `b`, also where their spans interleave (slices of one
-// fused projection): true if, with some of the dimensions walked inside a window, the windows of both
-// repeat by steps with a common divisor and lie apart within it.
-bool rows_apart(const Tensor& a, const Tensor& b) {
-  if (!overlap(a, b)) return true;
-  const long long delta = (static_cast<long long>(b.begin()) - static_cast<long long>(a.begin())) / 2;
-  for (int inside = 0; inside < 7; ++inside) {
-    long long wa = a.d, wb = b.d, step = 0;
-    for (int i = 0; i < 3; ++i)
-      if (inside >> i & 1) {
-        wa += (a.n[i] - 1) * a.stride[i];
-        wb += (b.n[i] - 1) * b.stride[i];
-      } else {
-        if (a.n[i] > 1) step = std::gcd(step, a.stride[i]);
-        if (b.n[i] > 1) step = std::gcd(step, b.stride[i]);
-      }
-    if (step == 0) continue;
-    const long long at = (delta % step + step) % step;
-    if (at >= wa && at + wb <= step) return true;
-  }
-  return false;
-}
-// Whether the rows of a tensor that is written lie apart from one another.
-bool rows_distinct(const Tensor& t) {
-  if (t.empty()) return true;
-  int order[3] = {0, 1, 2};
-  std::sort(order, order + 3, [&](int x, int y) { return t.stride[x] < t.stride[y]; });
-  long long span = t.d;
-  for (int i : order) {
-    if (t.n[i] <= 1) continue;
-    if (t.stride[i] < span) return false;
-    span += (t.n[i] - 1) * t.stride[i];
-  }
-  return true;
-}
-
-constexpr long long kMaxStride = 1ll << 38;   // elements: a tensor map's strides stay below 2^40 bytes
-constexpr long long kMaxSpan = 1ll << 46;     // elements of a whole tensor
-
-// 16-byte alignment, strides in multiples of 8 elements, no zero stride but the batch's.
-vdx_status check_tensor(const char* name, const Tensor& t, bool batch_may_repeat) {
-  if (t.empty()) return VDX_OK;
-  if (!t.ptr) return fail(VDX_ERR_ARG, "%s must be non-NULL", name);
-  if (t.begin() & 15) return fail(VDX_ERR_ALIGN, "%s is not 16-byte aligned", name);
-  long long span = t.d;
-  for (int i = 0; i < 3; ++i) {
-    if (t.n[i] == 1) continue;
-    const long long s = t.stride[i];
-    if (s < 0 || s > kMaxStride || s % 8)
-      return fail(VDX_ERR_ARG, "%s: stride %lld must be a multiple of 8 elements in [0, 2^38]", name, s);
-    if (s < t.d && !(s == 0 && i == 0 && batch_may_repeat))
-      return fail(VDX_ERR_ARG, "%s: stride %lld is smaller than a row of %d channels", name, s, t.d);
-    if (s && t.n[i] - 1 > kMaxSpan / s) return fail(VDX_ERR_ARG, "%s is too large", name);
-    span += (t.n[i] - 1) * s;
-  }
-  if (span > kMaxSpan) return fail(VDX_ERR_ARG, "%s is too large", name);
-  return VDX_OK;
-}
-
-vdx_status check_i32(const char* name, const int32_t* p, bool optional) {
-  if (!p) return optional ? VDX_OK : fail(VDX_ERR_ARG, "%s must be non-NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) & 3) return fail(VDX_ERR_ALIGN, "%s is not 4-byte aligned", name);
-  return VDX_OK;
-}
-
-vdx_status check_heads(int Hq, int Hkv, int d, int dtype) {
-  if (dtype != VDX_DTYPE_BF16 && dtype != VDX_DTYPE_FP16) return fail(VDX_ERR_ARG, "unknown dtype %d", dtype);
-  if (d != 64 && d != 128) return fail(VDX_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
-  if (Hkv < 1 || Hq < 1) return fail(VDX_ERR_ARG, "head counts must be >= 1 (got %d and %d)", Hq, Hkv);
-  if (Hq % Hkv) return fail(VDX_ERR_ARG, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
-  if (Hq / Hkv > 128) return fail(VDX_ERR_UNSUPPORTED, "more than 128 query heads per kv head (%d / %d)", Hq, Hkv);
-  return VDX_OK;
-}
-
-Tensor cache_tensor(const vdx_paged_kv& c, bool v) {
-  Tensor t{v ? c.v : c.k, {c.num_pages, c.page_size, c.Hkv}, {0, 0, 0}, c.d};
-  t.stride[0] = v ? c.v_page : c.k_page;
-  t.stride[1] = v ? c.v_token : c.k_token;
-  t.stride[2] = v ? c.v_head : c.k_head;
-  return t;
-}
-
-vdx_status check_cache(const vdx_paged_kv* c, int Hq) {
-  if (!c) return fail(VDX_ERR_ARG, "the cache must be non-NULL");
-  if (vdx_status s = check_heads(Hq, c->Hkv, c->d, c->dtype)) return s;
-  if (c->seqs < 0 || c->num_pages < 1 || c->max_pages < 1)
-    return fail(VDX_ERR_ARG, "seqs must be >= 0, num_pages and max_pages >= 1 (got %d, %d, %d)", c->seqs, c->num_pages,
-                c->max_pages);
-  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size < 128)
-    return fail(VDX_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or >= 128 (got %d)", c->page_size);
-  if (static_cast<long long>(c->max_pages) * c->page_size > 0x3fffffffll)
-    return fail(VDX_ERR_ARG, "max_pages * page_size = %lld is too large",
-                static_cast<long long>(c->max_pages) * c->page_size);
-  if (c->table_stride < c->max_pages && c->seqs > 1)
-    return fail(VDX_ERR_ARG, "table_stride %lld is smaller than max_pages %d", c->table_stride, c->max_pages);
-  if (c->table_stride > kMaxStride && c->seqs > 1) return fail(VDX_ERR_ARG, "table_stride %lld is too large", c->table_stride);
-  if (c->seqs > 0)
-    if (vdx_status s = check_i32("page_table", c->page_table, false)) return s;
-  if (vdx_status s = check_tensor("the key cache", cache_tensor(*c, false), false)) return s;
-  if (vdx_status s = check_tensor("the value cache", cache_tensor(*c, true), false)) return s;
-  return VDX_OK;
-}
+using namespace vdx::checks;
 
 // ------------------------------------------------------------------------------------- attention
 struct Problem {
@@ -191,8 +18,8 @@ struct Problem {
   size_t workspace = 0;
 };
 
-vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v, long long out_elems,
-                  long long lse_elems, float scale, const void* workspace, size_t workspace_bytes, bool size_only) {
+vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& k_scale, const Tensor& v_scale,
+                  long long out_elems, long long lse_elems, float scale, const void* workspace, size_t workspace_bytes, bool size_only) {
   vdx::KvParams& p = pb->p;
   if (!std::isfinite(scale)) return fail(VDX_ERR_ARG, "scale must be finite");
   p.scale_log2 = static_cast<float>((scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(pb->d))) * 1.4426950408889634);
@@ -237,15 +64,18 @@ vdx_status finish(Problem* pb, const Tensor& q, const Tensor& k, const Tensor& v
   const Span reads[4] = {ints(p.cu, p.cu ? p.S + 1ll : 0), ints(p.kv_len, p.S), ints(p.pos_offset, p.S),
                          table_span(p.table, p.S, p.table_stride, p.max_pages)};
   const Span writes[3] = {{p.out, out_bytes}, {p.lse, lse_bytes}, {pb->workspace ? workspace : nullptr, pb->workspace}};
+  for (const Span& w : writes)
+    if (overlap(k_scale, w.p, w.bytes) || overlap(v_scale, w.p, w.bytes)) return fail(VDX_ERR_ARG, "out, lse or workspace overlaps the scales");
   for (const Span& r : reads)
     for (const Span& w : writes)
       if (overlap(r, w)) return fail(VDX_ERR_ARG, "out, lse or workspace overlaps cu, kv_len, pos_offset or page_table");
   return VDX_OK;
 }
 
-vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, const int32_t* pos_offset, bool size_only, Problem* pb) {
+vdx_status paged_problem(const vdx_paged_kv* c, const vdx_kv8_scales* scales, const vdx_paged_attn_args* a, const int32_t* pos_offset,
+                         bool size_only, Problem* pb) {
   if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
-  if (vdx_status s = check_cache(c, a->Hq)) return s;
+  if (vdx_status s = check_cache(c, a->Hq, scales)) return s;
   if (a->rows < 0 || a->max_q < 0 || a->max_kv < 0 || a->causal_block < 0)
     return fail(VDX_ERR_ARG, "rows, max_q, max_kv and causal_block must be >= 0 (got %d, %d, %d, %d)", a->rows, a->max_q,
                 a->max_kv, a->causal_block);
@@ -270,7 +100,11 @@ vdx_status paged_problem(const vdx_paged_kv* c, const vdx_paged_attn_args* a, co
     if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
     if (vdx_status s = check_i32("pos_offset", pos_offset, true)) return s;
   }
-  return finish(pb, q, cache_tensor(*c, false), cache_tensor(*c, true),
+  p.eight = scales != nullptr;
+  if (scales) p.scales = device_scales(*scales);
+  const Tensor none{};
+  return finish(pb, q, cache_tensor(*c, false, scales), cache_tensor(*c, true, scales),
+                scales ? scale_tensor(*c, *scales, false) : none, scales ? scale_tensor(*c, *scales, true) : none,
                 static_cast<long long>(a->rows) * a->Hq * c->d, a->lse ? static_cast<long long>(a->rows) * a->Hq : 0,
                 a->scale, a->workspace, a->workspace_bytes, size_only);
 }
@@ -297,7 +131,7 @@ vdx_status cross_problem(const vdx_cross_attn_args* a, bool size_only, Problem* 
   const Tensor v{a->v, {a->B, a->M, a->Hkv}, {a->v_batch, a->v_token, a->v_head}, a->d};
   const long long rows = static_cast<long long>(a->B) * a->N * a->Hq;
   if (rows > kMaxSpan / a->d) return fail(VDX_ERR_ARG, "out is too large");
-  return finish(pb, q, k, v, rows * a->d, a->lse ? rows : 0, a->scale, a->workspace, a->workspace_bytes, size_only);
+  return finish(pb, q, k, v, Tensor{}, Tensor{}, rows * a->d, a->lse ? rows : 0, a->scale, a->workspace, a->workspace_bytes, size_only);
 }
 
 vdx_status launch(const Problem& pb, void* stream) {
@@ -326,6 +160,98 @@ vdx_status launch(const Problem& pb, void* stream) {
   return VDX_OK;
 }
 
+// ------------------------------------------------------------------------------------- append
+vdx_status append(const vdx_paged_kv* c, const vdx_kv8_scales* scales, const vdx_append_args* a, void* stream) {
+  if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
+  if (vdx_status s = check_cache(c, a->q ? a->Hq : (c ? c->Hkv : 1), scales)) return s;
+  const int d = c->d;
+  if (a->rows < 0) return fail(VDX_ERR_ARG, "rows must be >= 0 (got %d)", a->rows);
+  if (!a->q != !a->q_out) return fail(VDX_ERR_ARG, "q and q_out go together");
+  if (a->T < 1 || a->Hgrid < 1 || a->Wgrid < 1)
+    return fail(VDX_ERR_ARG, "T, Hgrid and Wgrid must be >= 1 (got %d %d %d)", a->T, a->Hgrid, a->Wgrid);
+  if (static_cast<long long>(a->Hgrid) * a->Wgrid > 0x7fffffffll)
+    return fail(VDX_ERR_ARG, "a frame of %d x %d tokens is too large", a->Hgrid, a->Wgrid);
+  int st = a->sec_t, sh = a->sec_h, sw = a->sec_w;
+  if (st == 0 && sh == 0 && sw == 0) {
+    sh = sw = 2 * (d / 6);
+    st = d - sh - sw;
+  }
+  if (st < 0 || sh < 0 || sw < 0 || ((st | sh | sw) & 1) || static_cast<long long>(st) + sh + sw != d)
+    return fail(VDX_ERR_ARG, "rotary sections %d/%d/%d must be even, non-negative and sum to d=%d", st, sh, sw, d);
+  if (!(a->theta > 0.0) || !std::isfinite(a->theta)) return fail(VDX_ERR_ARG, "theta must be > 0");
+  if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return fail(VDX_ERR_ARG, "eps must be finite and >= 0");
+  if (!a->q && a->q_norm) return fail(VDX_ERR_ARG, "q_norm without q");
+  if (a->rows == 0 || c->seqs == 0) return VDX_OK;
+  const Tensor q{a->q, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_row, a->q_head}, d};
+  const Tensor qo{a->q_out, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_out_row, a->q_out_head}, d};
+  const Tensor k{a->k, {1, a->rows, c->Hkv}, {0, a->k_row, a->k_head}, d};
+  const Tensor v{a->v, {1, a->rows, c->Hkv}, {0, a->v_row, a->v_head}, d};
+  if (vdx_status s = check_tensor("q", q, false)) return s;
+  if (vdx_status s = check_tensor("q_out", qo, false)) return s;
+  if (vdx_status s = check_tensor("k", k, false)) return s;
+  if (vdx_status s = check_tensor("v", v, false)) return s;
+  if (vdx_status s = check_i32("cu", a->cu, false)) return s;
+  if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
+  if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
+  if ((reinterpret_cast<uintptr_t>(a->q_norm) | reinterpret_cast<uintptr_t>(a->k_norm)) & 15)
+    return fail(VDX_ERR_ALIGN, "q_norm or k_norm is not 16-byte aligned");
+  const Tensor kc = cache_tensor(*c, false, scales), vc = cache_tensor(*c, true, scales);
+  const bool in_place = a->q && a->q == a->q_out && a->q_row == a->q_out_row && a->q_head == a->q_out_head;
+  if (a->q && ((!in_place && !rows_apart(qo, q)) || !rows_apart(qo, k) || !rows_apart(qo, v)))
+    return fail(VDX_ERR_ARG, "q_out overlaps q, k or v");
+  if (!rows_distinct(qo)) return fail(VDX_ERR_ARG, "rows of q_out overlap one another");
+  if (vdx_status s = check_written_cache(*c, scales)) return s;
+  for (const Tensor* t : {&kc, &vc})
+    if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
+      return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
+  const Span reads[6] = {ints(a->cu, c->seqs + 1ll), ints(a->kv_len, c->seqs), ints(a->pos_offset, c->seqs),
+                         table_span(c->page_table, c->seqs, c->table_stride, c->max_pages),
+                         {a->q_norm, static_cast<size_t>(d) * 2}, {a->k_norm, static_cast<size_t>(d) * 2}};
+  for (const Span& r : reads)
+    for (const Tensor* t : {&kc, &vc, &qo})
+      if (overlap(*t, r.p, r.bytes))
+        return fail(VDX_ERR_ARG, "the cache or q_out overlaps cu, kv_len, pos_offset, page_table, q_norm or k_norm");
+  if (scales) {
+    for (bool value : {false, true}) {
+      const Tensor t = scale_tensor(*c, *scales, value);
+      if (overlap(t, q) || overlap(t, k) || overlap(t, v) || overlap(t, qo)) return fail(VDX_ERR_ARG, "the scales overlap q, k, v or q_out");
+      for (const Span& r : reads)
+        if (overlap(t, r.p, r.bytes))
+          return fail(VDX_ERR_ARG, "the scales overlap cu, kv_len, pos_offset, page_table, q_norm or k_norm");
+    }
+  }
+
+  vdx::AppendParams p{};
+  p.q = a->q; p.k = a->k; p.v = a->v; p.q_out = a->q_out; p.k_cache = c->k; p.v_cache = c->v;
+  p.q_row = a->q_row; p.q_head = a->q_head; p.k_row = a->k_row; p.k_head = a->k_head;
+  p.v_row = a->v_row; p.v_head = a->v_head; p.q_out_row = a->q_out_row; p.q_out_head = a->q_out_head;
+  p.kc_page = c->k_page; p.kc_token = c->k_token; p.kc_head = c->k_head;
+  p.vc_page = c->v_page; p.vc_token = c->v_token; p.vc_head = c->v_head;
+  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->pos_offset;
+  p.table = c->page_table; p.table_stride = c->table_stride;
+  p.q_norm = a->q_norm; p.k_norm = a->k_norm; p.eps = a->eps;
+  p.rows = a->rows; p.S = c->seqs; p.Hq = a->q ? a->Hq : 0; p.Hkv = c->Hkv;
+  p.P = c->page_size; p.num_pages = c->num_pages; p.max_pages = c->max_pages;
+  p.T = a->T; p.Hg = a->Hgrid; p.Wg = a->Wgrid;
+  p.half_t = st / 2; p.half_h = sh / 2;
+  const int sec[3] = {st, sh, sw};
+  int pair = 0;
+  for (int x = 0; x < 3; ++x)
+    for (int j = 0; j < sec[x] / 2; ++j) {
+      const double turns = std::pow(a->theta, -2.0 * j / sec[x]) / 6.283185307179586476925286766559;
+      if (!std::isfinite(turns)) return fail(VDX_ERR_ARG, "theta = %g is too small: its powers are not finite", a->theta);
+      const double frac = turns - std::floor(turns);
+      p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
+    }
+  if (scales) p.scales = device_scales(*scales);
+  const cudaError_t e = (scales ? vdx::launch_append8 : vdx::launch_append)(p, d, c->dtype, multiprocessors(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
+  }
+  return VDX_OK;
+}
+
 }  // namespace
 
 namespace vdx {
@@ -333,10 +259,11 @@ namespace vdx {
 size_t plan_attention(KvParams* p, int d, int sms) {
   const long long rows = static_cast<long long>(p->max_q) * p->g;
   p->rows_kernel = rows <= 32;
+  if (p->eight) p->rows_kernel = 1;
   if (p->rows_kernel) {
     p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-    p->nblk = 1;
-    const long long units = static_cast<long long>(p->S) * p->Hkv;
+    p->nblk = static_cast<int>((rows - 1) / p->block_rows + 1);
+    const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
     // Two CTAs to a multiprocessor, in one wave where the units leave room for splits: the most
     // splits that fit with a tenth to spare (clusters do not fill every group of processors), of at
     // least 192 keys.  16 x 8 heads over 8192 keys: 2 splits 84.7 us, 1 split 131, 4 (two waves) 93, 8
@@ -407,94 +334,21 @@ extern "C" {
 vdx_status vdx_rope3d_append(const vdx_paged_kv* c, const vdx_append_args* a, void* stream) {
   NvtxScope nvtx("vdx_rope3d_append");
   clear_error();
-  if (!a) return fail(VDX_ERR_ARG, "the arguments must be non-NULL");
-  if (vdx_status s = check_cache(c, a->q ? a->Hq : (c ? c->Hkv : 1))) return s;
-  const int d = c->d;
-  if (a->rows < 0) return fail(VDX_ERR_ARG, "rows must be >= 0 (got %d)", a->rows);
-  if (!a->q != !a->q_out) return fail(VDX_ERR_ARG, "q and q_out go together");
-  if (a->T < 1 || a->Hgrid < 1 || a->Wgrid < 1)
-    return fail(VDX_ERR_ARG, "T, Hgrid and Wgrid must be >= 1 (got %d %d %d)", a->T, a->Hgrid, a->Wgrid);
-  if (static_cast<long long>(a->Hgrid) * a->Wgrid > 0x7fffffffll)
-    return fail(VDX_ERR_ARG, "a frame of %d x %d tokens is too large", a->Hgrid, a->Wgrid);
-  int st = a->sec_t, sh = a->sec_h, sw = a->sec_w;
-  if (st == 0 && sh == 0 && sw == 0) {
-    sh = sw = 2 * (d / 6);
-    st = d - sh - sw;
-  }
-  if (st < 0 || sh < 0 || sw < 0 || ((st | sh | sw) & 1) || static_cast<long long>(st) + sh + sw != d)
-    return fail(VDX_ERR_ARG, "rotary sections %d/%d/%d must be even, non-negative and sum to d=%d", st, sh, sw, d);
-  if (!(a->theta > 0.0) || !std::isfinite(a->theta)) return fail(VDX_ERR_ARG, "theta must be > 0");
-  if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return fail(VDX_ERR_ARG, "eps must be finite and >= 0");
-  if (!a->q && a->q_norm) return fail(VDX_ERR_ARG, "q_norm without q");
-  if (a->rows == 0 || c->seqs == 0) return VDX_OK;
-  const Tensor q{a->q, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_row, a->q_head}, d};
-  const Tensor qo{a->q_out, {1, a->q ? a->rows : 0, a->Hq}, {0, a->q_out_row, a->q_out_head}, d};
-  const Tensor k{a->k, {1, a->rows, c->Hkv}, {0, a->k_row, a->k_head}, d};
-  const Tensor v{a->v, {1, a->rows, c->Hkv}, {0, a->v_row, a->v_head}, d};
-  if (vdx_status s = check_tensor("q", q, false)) return s;
-  if (vdx_status s = check_tensor("q_out", qo, false)) return s;
-  if (vdx_status s = check_tensor("k", k, false)) return s;
-  if (vdx_status s = check_tensor("v", v, false)) return s;
-  if (vdx_status s = check_i32("cu", a->cu, false)) return s;
-  if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
-  if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
-  if ((reinterpret_cast<uintptr_t>(a->q_norm) | reinterpret_cast<uintptr_t>(a->k_norm)) & 15)
-    return fail(VDX_ERR_ALIGN, "q_norm or k_norm is not 16-byte aligned");
-  const Tensor kc = cache_tensor(*c, false), vc = cache_tensor(*c, true);
-  const bool in_place = a->q && a->q == a->q_out && a->q_row == a->q_out_row && a->q_head == a->q_out_head;
-  if (a->q && ((!in_place && !rows_apart(qo, q)) || !rows_apart(qo, k) || !rows_apart(qo, v)))
-    return fail(VDX_ERR_ARG, "q_out overlaps q, k or v");
-  if (!rows_distinct(qo)) return fail(VDX_ERR_ARG, "rows of q_out overlap one another");
-  if (!rows_distinct(kc)) return fail(VDX_ERR_ARG, "tokens of the key cache overlap one another");
-  if (!rows_distinct(vc)) return fail(VDX_ERR_ARG, "tokens of the value cache overlap one another");
-  if (c->k == c->v) return fail(VDX_ERR_ARG, "the key and value caches are the same memory");
-  if (!rows_apart(kc, vc)) return fail(VDX_ERR_ARG, "the key and value caches overlap");
-  for (const Tensor* t : {&kc, &vc})
-    if (overlap(*t, q) || overlap(*t, k) || overlap(*t, v) || overlap(*t, qo))
-      return fail(VDX_ERR_ARG, "the cache overlaps q, k, v or q_out");
-  const Span reads[6] = {ints(a->cu, c->seqs + 1ll), ints(a->kv_len, c->seqs), ints(a->pos_offset, c->seqs),
-                         table_span(c->page_table, c->seqs, c->table_stride, c->max_pages),
-                         {a->q_norm, static_cast<size_t>(d) * 2}, {a->k_norm, static_cast<size_t>(d) * 2}};
-  for (const Span& r : reads)
-    for (const Tensor* t : {&kc, &vc, &qo})
-      if (overlap(*t, r.p, r.bytes))
-        return fail(VDX_ERR_ARG, "the cache or q_out overlaps cu, kv_len, pos_offset, page_table, q_norm or k_norm");
+  return append(c, nullptr, a, stream);
+}
 
-  vdx::AppendParams p{};
-  p.q = a->q; p.k = a->k; p.v = a->v; p.q_out = a->q_out; p.k_cache = c->k; p.v_cache = c->v;
-  p.q_row = a->q_row; p.q_head = a->q_head; p.k_row = a->k_row; p.k_head = a->k_head;
-  p.v_row = a->v_row; p.v_head = a->v_head; p.q_out_row = a->q_out_row; p.q_out_head = a->q_out_head;
-  p.kc_page = c->k_page; p.kc_token = c->k_token; p.kc_head = c->k_head;
-  p.vc_page = c->v_page; p.vc_token = c->v_token; p.vc_head = c->v_head;
-  p.cu = a->cu; p.kv_len = a->kv_len; p.pos_offset = a->pos_offset;
-  p.table = c->page_table; p.table_stride = c->table_stride;
-  p.q_norm = a->q_norm; p.k_norm = a->k_norm; p.eps = a->eps;
-  p.rows = a->rows; p.S = c->seqs; p.Hq = a->q ? a->Hq : 0; p.Hkv = c->Hkv;
-  p.P = c->page_size; p.num_pages = c->num_pages; p.max_pages = c->max_pages;
-  p.T = a->T; p.Hg = a->Hgrid; p.Wg = a->Wgrid;
-  p.half_t = st / 2; p.half_h = sh / 2;
-  const int sec[3] = {st, sh, sw};
-  int pair = 0;
-  for (int x = 0; x < 3; ++x)
-    for (int j = 0; j < sec[x] / 2; ++j) {
-      const double turns = std::pow(a->theta, -2.0 * j / sec[x]) / 6.283185307179586476925286766559;
-      if (!std::isfinite(turns)) return fail(VDX_ERR_ARG, "theta = %g is too small: its powers are not finite", a->theta);
-      const double frac = turns - std::floor(turns);
-      p.turn[pair++] = frac >= 1.0 ? 0ull : static_cast<uint64_t>(std::ldexp(frac, 64));
-    }
-  const cudaError_t e = vdx::launch_append(p, d, c->dtype, multiprocessors(), static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(VDX_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
-  }
-  return VDX_OK;
+vdx_status vdx_rope3d_append8(const vdx_paged_kv* c, const vdx_kv8_scales* scales, const vdx_append_args* a, void* stream) {
+  NvtxScope nvtx("vdx_rope3d_append8");
+  clear_error();
+  if (!scales) return fail(VDX_ERR_ARG, "the scales must be non-NULL");
+  return append(c, scales, a, stream);
 }
 
 vdx_status vdx_paged_attn(const vdx_paged_kv* c, const vdx_paged_attn_args* a, void* stream) {
   NvtxScope nvtx("vdx_paged_attn");
   clear_error();
   Problem pb;
-  if (vdx_status s = paged_problem(c, a, nullptr, false, &pb)) return s;
+  if (vdx_status s = paged_problem(c, nullptr, a, nullptr, false, &pb)) return s;
   return launch(pb, stream);
 }
 
@@ -502,14 +356,34 @@ vdx_status vdx_paged_attn_offset(const vdx_paged_kv* c, const vdx_paged_attn_arg
   NvtxScope nvtx("vdx_paged_attn_offset");
   clear_error();
   Problem pb;
-  if (vdx_status s = paged_problem(c, a, pos_offset, false, &pb)) return s;
+  if (vdx_status s = paged_problem(c, nullptr, a, pos_offset, false, &pb)) return s;
   return launch(pb, stream);
 }
 
 size_t vdx_paged_attn_workspace_bytes(const vdx_paged_kv* c, const vdx_paged_attn_args* a) {
   clear_error();
   Problem pb;
-  return paged_problem(c, a, nullptr, true, &pb) == VDX_OK ? pb.workspace : 0;
+  return paged_problem(c, nullptr, a, nullptr, true, &pb) == VDX_OK ? pb.workspace : 0;
+}
+
+vdx_status vdx_paged_attn8(const vdx_paged_kv* c, const vdx_kv8_scales* scales, const vdx_paged_attn_args* a, const int32_t* pos_offset,
+                           void* stream) {
+  NvtxScope nvtx("vdx_paged_attn8");
+  clear_error();
+  if (!scales) return fail(VDX_ERR_ARG, "the scales must be non-NULL");
+  Problem pb;
+  if (vdx_status s = paged_problem(c, scales, a, pos_offset, false, &pb)) return s;
+  return launch(pb, stream);
+}
+
+size_t vdx_paged_attn8_workspace_bytes(const vdx_paged_kv* c, const vdx_kv8_scales* scales, const vdx_paged_attn_args* a) {
+  clear_error();
+  Problem pb;
+  if (!scales) {
+    fail(VDX_ERR_ARG, "the scales must be non-NULL");
+    return 0;
+  }
+  return paged_problem(c, scales, a, nullptr, true, &pb) == VDX_OK ? pb.workspace : 0;
 }
 
 vdx_status vdx_cross_attn(const vdx_cross_attn_args* a, void* stream) {

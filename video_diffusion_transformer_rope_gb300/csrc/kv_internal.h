@@ -13,6 +13,14 @@ namespace vdx {
 constexpr unsigned kErrPage = 8u;       // a page index outside the cache
 constexpr unsigned kErrLength = 16u;    // a length or row range past its bound
 constexpr unsigned kErrPosition = 32u;  // a token outside the position grid or its page table
+constexpr unsigned kErrRange8 = 64u;    // a value past what an 8-bit cache holds
+
+// Scales of an 8-bit cache (kv8.cuh): a byte per block of 16 tokens and head, strides in bytes.
+struct Scales8 {
+  uint8_t* k;
+  uint8_t* v;
+  long long k_page, k_block, k_head, v_page, v_block, v_head;
+};
 
 // Append: one problem, validated.  Strides in elements.
 struct AppendParams {
@@ -38,8 +46,10 @@ struct AppendParams {
   int half_t, half_h;         // rotary pairs of the t and h axes (the rest turn with w)
   // Turns per position of each channel pair as a 64-bit fixed-point fraction: omega / 2 pi mod 1.
   uint64_t turn[64];
+  Scales8 scales;             // of an 8-bit cache
 };
 cudaError_t launch_append(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_append8(const AppendParams& p, int d, int dtype, int sms, cudaStream_t stream);
 
 // Attention over a paged cache (table != nullptr) or over dense keys (one "page" of P = M tokens
 // per batch entry).  Rows: sequence s owns tokens cu[s] .. cu[s+1]-1 of one packed q, or, with
@@ -73,6 +83,8 @@ struct KvParams {
   int split_keys;             // keys (rows kernel) or key tiles (tile kernel) per split
   float* part_o;              // [unit][split][block_rows][d], unit = (s * Hkv + hk) * nblk + blk
   float2* part_ml;            // [unit][split][block_rows]: running maximum (log2 units) and sum
+  int eight;                  // the cache holds 8-bit codes with these scales
+  Scales8 scales;
 };
 
 // Opt a kernel in to `bytes` of dynamic shared memory, once per device (a process-wide property of the
@@ -97,10 +109,47 @@ cudaError_t launch_attn_tiles(const KvParams& p, int d, int dtype, EncodeTiledFn
                               cudaStream_t stream, const char** what);
 cudaError_t launch_attn_combine(const KvParams& p, int d, int dtype, cudaStream_t stream);
 
+// The weight that each key gathers: the problem's KvParams (out, lse and plan unused) and these.
+struct WeighParams {
+  KvParams kv;
+  const float* lse;           // [Hq][N]
+  float* w;
+  long long w_seq, w_head;
+  float decay;
+  int nsplit, split_keys;     // keys of a block (few-row kernel)
+};
+cudaError_t launch_weigh(WeighParams p, int d, int dtype, int sms, cudaStream_t stream);
+
+// Eviction: one problem, validated.
+struct EvictParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  uint8_t* k_to;
+  uint8_t* v_to;
+  long long k_p, k_t, k_h, v_p, v_t, v_h, kt_p, kt_t, kt_h, vt_p, vt_t, vt_h;      // strides in bytes
+  const int* table;
+  const int* table_to;
+  long long table_stride, table_to_stride;
+  int P, num_pages, P_to, num_pages_to, max_pages_to;
+  int S, Hkv, keep, recent, max_kv;
+  const float* w;
+  float* w_out;
+  long long w_seq, w_head, w_out_seq, w_out_head;
+  const int* kv_len;
+  const int* pos_offset;
+  int* kv_len_out;
+  int* pos_offset_out;
+  int* index;
+  Scales8 scales, scales_to;
+};
+cudaError_t launch_evict(const EvictParams& p, int d, bool eight, int sms, cudaStream_t stream);
+
 // Read and reset the error words of these translation units (synchronous).
 cudaError_t read_and_clear_error_word_append(unsigned int* word);
 cudaError_t read_and_clear_error_word_rows(unsigned int* word);
 cudaError_t read_and_clear_error_word_tiles(unsigned int* word);
+cudaError_t read_and_clear_error_word_weigh(unsigned int* word);
+cudaError_t read_and_clear_error_word_evict(unsigned int* word);
 
 // cuTensorMapEncodeTiled, looked up once (vdx_capi.cu).  Sets vdx_last_error on failure.
 bool encode_tiled_fn(EncodeTiledFn* fn);

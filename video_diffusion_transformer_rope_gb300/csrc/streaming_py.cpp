@@ -33,6 +33,11 @@ decltype(&vdx_paged_attn_offset) g_paged = nullptr;
 decltype(&vdx_paged_attn_workspace_bytes) g_paged_size = nullptr;
 decltype(&vdx_cross_attn) g_cross = nullptr;
 decltype(&vdx_cross_attn_workspace_bytes) g_cross_size = nullptr;
+decltype(&vdx_rope3d_append8) g_append8 = nullptr;
+decltype(&vdx_paged_attn8) g_paged8 = nullptr;
+decltype(&vdx_paged_attn8_workspace_bytes) g_paged8_size = nullptr;
+decltype(&vdx_paged_attn_weights) g_weights = nullptr;
+decltype(&vdx_paged_evict) g_evict = nullptr;
 decltype(&vdx_last_error) g_last_error = nullptr;
 
 struct Raised {};                                  // a Python error is set
@@ -145,30 +150,77 @@ void written(const at::Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-const at::Tensor& cache_struct(PyObject* k_, PyObject* v_, PyObject* table_, vdx_paged_kv* c, bool writes) {
-  const at::Tensor& k = tensor("the key cache", k_, nullptr, 4);
-  const at::Tensor& v = tensor("the value cache", v_, &k, 4);
-  if (k.sizes() != v.sizes())
-    refuse(VDX_ERR_ARG, "the key and value caches differ in shape: %s, %s", text(k.sizes()).c_str(), text(v.sizes()).c_str());
-  const at::Tensor* t = cuda_tensor(table_);
-  if (!t || t->scalar_type() != at::kInt || t->device() != k.device() || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1) ||
-      t->size(0) > INT_MAX - 1 || t->size(1) > INT_MAX)
-    refuse(VDX_ERR_ARG, "page_table must be an int32 [seqs, max_pages] tensor on %s with contiguous rows", dev(k).c_str());
-  c->k = writes ? k.mutable_data_ptr() : const_cast<void*>(address(k));
-  c->v = writes ? v.mutable_data_ptr() : const_cast<void*>(address(v));
-  c->k_page = k.stride(0); c->k_token = k.stride(1); c->k_head = k.stride(2);
-  c->v_page = v.stride(0); c->v_token = v.stride(1); c->v_head = v.stride(2);
-  c->page_table = static_cast<const int32_t*>(address(*t));
-  c->table_stride = t->stride(0);
-  c->num_pages = static_cast<int>(k.size(0));
-  c->page_size = static_cast<int>(k.size(1));
-  c->max_pages = static_cast<int>(t->size(1));
-  c->Hkv = static_cast<int>(k.size(2));
-  c->d = static_cast<int>(k.size(3));
-  c->dtype = dtype_of(k);
-  c->seqs = static_cast<int>(t->size(0));
-  return k;
-}
+// A PagedKV: its structure, and where k and v hold 8-bit codes that of its scales.  The type of such a cache's
+// calls is that of their other tensors (match()).
+struct Cache {
+  vdx_paged_kv c{};
+  vdx_kv8_scales s{};
+  bool eight = false;
+  const at::Tensor* k = nullptr;
+  const at::Tensor* v = nullptr;
+  const at::Tensor* ks = nullptr;
+  const at::Tensor* vs = nullptr;
+
+  // objects: k, v, page_table, k_scale, v_scale
+  Cache(PyObject* k_, PyObject* v_, PyObject* table_, PyObject* ks_, PyObject* vs_, bool writes) {
+    k = &tensor("the key cache", k_, nullptr, 4);
+    v = &tensor("the value cache", v_, k, 4);
+    if (k->sizes() != v->sizes())
+      refuse(VDX_ERR_ARG, "the key and value caches differ in shape: %s, %s", text(k->sizes()).c_str(), text(v->sizes()).c_str());
+    const at::Tensor* t = cuda_tensor(table_);
+    if (!t || t->scalar_type() != at::kInt || t->device() != k->device() || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1) ||
+        t->size(0) > INT_MAX - 1 || t->size(1) > INT_MAX)
+      refuse(VDX_ERR_ARG, "page_table must be an int32 [seqs, max_pages] tensor on %s with contiguous rows", dev(*k).c_str());
+    auto memory = [&](const at::Tensor& x) { return writes ? x.mutable_data_ptr() : const_cast<void*>(address(x)); };
+    c.k = memory(*k);
+    c.v = memory(*v);
+    c.k_page = k->stride(0); c.k_token = k->stride(1); c.k_head = k->stride(2);
+    c.v_page = v->stride(0); c.v_token = v->stride(1); c.v_head = v->stride(2);
+    c.page_table = static_cast<const int32_t*>(address(*t));
+    c.table_stride = t->stride(0);
+    c.num_pages = static_cast<int>(k->size(0));
+    c.page_size = static_cast<int>(k->size(1));
+    c.max_pages = static_cast<int>(t->size(1));
+    c.Hkv = static_cast<int>(k->size(2));
+    c.d = static_cast<int>(k->size(3));
+    c.seqs = static_cast<int>(t->size(0));
+    eight = k->scalar_type() == at::kFloat8_e4m3fn;
+    if (!eight) {
+      if (ks_ != Py_None || vs_ != Py_None) refuse(VDX_ERR_ARG, "k_scale and v_scale belong to caches of float8_e4m3fn");
+      c.dtype = dtype_of(*k);
+      return;
+    }
+    ks = &scale("k_scale", ks_);
+    vs = &scale("v_scale", vs_);
+    s.k = static_cast<uint8_t*>(memory(*ks));
+    s.v = static_cast<uint8_t*>(memory(*vs));
+    s.k_page = ks->stride(0); s.k_block = ks->stride(1); s.k_head = ks->stride(2);
+    s.v_page = vs->stride(0); s.v_block = vs->stride(1); s.v_head = vs->stride(2);
+  }
+  const at::Tensor& scale(const char* name, PyObject* o) const {
+    const at::Tensor* t = cuda_tensor(o);
+    const int64_t blocks = (c.page_size + VDX_KV8_BLOCK - 1) / VDX_KV8_BLOCK;
+    const int64_t shape[3] = {c.num_pages, blocks, c.Hkv};
+    if (!t || t->scalar_type() != at::kFloat8_e8m0fnu || t->device() != k->device() || t->sizes() != at::IntArrayRef(shape))
+      refuse(VDX_ERR_ARG, "%s must be a float8_e8m0fnu tensor of shape %s on %s: a scale for every %d tokens of a page and head", name,
+             text(shape).c_str(), dev(*k).c_str(), VDX_KV8_BLOCK);
+    forward_only(name, *t);
+    return *t;
+  }
+  // A tensor of the call beside the cache, which has the call's type; the first one decides it for an 8-bit cache.
+  const at::Tensor& match(const char* name, PyObject* o, int dims) {
+    if (!eight) return tensor(name, o, k, dims);
+    const at::Tensor& t = tensor(name, o, nullptr, dims);
+    if (t.device() != k->device()) refuse(VDX_ERR_ARG, "%s must be a CUDA tensor on %s", name, dev(*k).c_str());
+    c.dtype = dtype_of(t);
+    return t;
+  }
+  const vdx_kv8_scales* scales() const { return eight ? &s : nullptr; }
+  void mark_written() const {
+    for (const at::Tensor* t : {k, v, ks, vs})
+      if (t) written(*t);
+  }
+};
 
 // 0 bytes are an answer, or a call that the library cannot take: then it has left a message.
 PyObject* bytes_or_refusal(size_t bytes) {
@@ -245,10 +297,11 @@ PyObject* attention(Args& a, const at::Tensor& q, at::IntArrayRef lse_shape, PyO
 // ------------------------------------------------------------------------------------------ the calls
 PyObject* append(PyObject* const* a) {
   PyObject *q_ = a[0], *q_out_ = a[12];
-  vdx_paged_kv c{};
+  Cache cache(a[3], a[4], a[5], a[16], a[17], true);
+  vdx_paged_kv& c = cache.c;
   vdx_append_args x{};
-  const at::Tensor& like = cache_struct(a[3], a[4], a[5], &c, true);
-  const at::Tensor& k = tensor("k", a[1], &like, 3);
+  const at::Tensor& k = cache.match("k", a[1], 3);
+  const at::Tensor& like = k;
   const at::Tensor& v = tensor("v", a[2], &like, 3);
   if (k.size(1) != c.Hkv || k.size(2) != c.d || v.sizes() != k.sizes())
     refuse(VDX_ERR_ARG, "k %s and v %s must be [rows, %d, %d], as the cache's heads", text(k.sizes()).c_str(), text(v.sizes()).c_str(),
@@ -274,9 +327,8 @@ PyObject* append(PyObject* const* a) {
   x.theta = real(a[15]);
   x.eps = static_cast<float>(real(a[11]));
   auto run = [&] {
-    call(like, [&](void* stream) { return g_append(&c, &x, stream); });
-    written(THPVariable_Unpack(a[3]));
-    written(THPVariable_Unpack(a[4]));
+    call(like, [&](void* stream) { return cache.eight ? g_append8(&c, &cache.s, &x, stream) : g_append(&c, &x, stream); });
+    cache.mark_written();
   };
   if (q_ == Py_None) {
     if (q_out_ != Py_None) refuse(VDX_ERR_ARG, "q_out without q");
@@ -307,38 +359,118 @@ PyObject* append(PyObject* const* a) {
   return q_out_ == Py_None ? THPVariable_Wrap(out) : Py_NewRef(q_out_);
 }
 
-// q, the cache's three tensors, cu, kv_len, max_q, max_kv of a paged call
-const at::Tensor& paged_args(PyObject* const* a, vdx_paged_kv* c, vdx_paged_attn_args* x) {
-  const at::Tensor& like = cache_struct(a[1], a[2], a[3], c, false);
-  const at::Tensor& q = tensor("q", a[0], &like, 3);
-  if (q.size(2) != c->d)
-    refuse(VDX_ERR_ARG, "q %s does not match the cache's head dimension %d", text(q.sizes()).c_str(), c->d);
+// q, cu, kv_len, max_q, max_kv of a paged call (a[0], a[4] to a[7])
+const at::Tensor& paged_args(PyObject* const* a, Cache* cache, vdx_paged_attn_args* x) {
+  const vdx_paged_kv& c = cache->c;
+  const at::Tensor& q = cache->match("q", a[0], 3);
+  if (q.size(2) != c.d)
+    refuse(VDX_ERR_ARG, "q %s does not match the cache's head dimension %d", text(q.sizes()).c_str(), c.d);
   x->q = address(q);
   x->q_row = q.stride(0); x->q_head = q.stride(1);
   x->rows = static_cast<int>(q.size(0));
   x->Hq = static_cast<int>(q.size(1));
-  x->cu = int32s("cu", a[4], q, static_cast<int64_t>(c->seqs) + 1);
-  x->kv_len = int32s("kv_len", a[5], q, c->seqs);
+  x->cu = int32s("cu", a[4], q, static_cast<int64_t>(c.seqs) + 1);
+  x->kv_len = int32s("kv_len", a[5], q, c.seqs);
   x->max_q = bound("max_q", a[6]);
   x->max_kv = bound("max_kv", a[7]);
   return q;
 }
+size_t paged_bytes(const Cache& cache, const vdx_paged_attn_args& x) {
+  return cache.eight ? g_paged8_size(&cache.c, &cache.s, &x) : g_paged_size(&cache.c, &x);
+}
 PyObject* paged(PyObject* const* a) {
-  vdx_paged_kv c{};
+  Cache cache(a[1], a[2], a[3], a[15], a[16], false);
   vdx_paged_attn_args x{};
-  const at::Tensor& q = paged_args(a, &c, &x);
+  const at::Tensor& q = paged_args(a, &cache, &x);
   x.causal_block = integer("causal_block", a[8]);
   x.scale = static_cast<float>(real(a[9]));
-  const int32_t* pos_offset = int32s("pos_offset", a[14], q, c.seqs);
+  const int32_t* pos_offset = int32s("pos_offset", a[14], q, cache.c.seqs);
   const int64_t lse_shape[2] = {x.Hq, x.rows};
-  return attention(x, q, lse_shape, a[10], a[11], a[12], a[13], [&] { return g_paged_size(&c, &x); },
-                   [&](void* stream) { return g_paged(&c, &x, pos_offset, stream); });
+  return attention(x, q, lse_shape, a[10], a[11], a[12], a[13], [&] { return paged_bytes(cache, x); }, [&](void* stream) {
+    return cache.eight ? g_paged8(&cache.c, &cache.s, &x, pos_offset, stream) : g_paged(&cache.c, &x, pos_offset, stream);
+  });
 }
 PyObject* paged_size(PyObject* const* a) {
-  vdx_paged_kv c{};
+  Cache cache(a[1], a[2], a[3], a[8], a[9], false);
   vdx_paged_attn_args x{};
-  const c10::cuda::CUDAGuard guard(paged_args(a, &c, &x).device());
-  return bytes_or_refusal(g_paged_size(&c, &x));
+  const c10::cuda::CUDAGuard guard(paged_args(a, &cache, &x).device());
+  return bytes_or_refusal(paged_bytes(cache, x));
+}
+
+// Gathered weights: float32 [seqs, heads, width], the entries of a head contiguous.
+const at::Tensor& gathered(const char* name, PyObject* o, const Cache& cache, int64_t least) {
+  const at::Tensor* t = cuda_tensor(o);
+  if (!t || t->scalar_type() != at::kFloat || t->device() != cache.k->device() || t->dim() != 3 || t->size(0) != cache.c.seqs ||
+      t->size(1) != cache.c.Hkv || t->size(2) < least || t->size(2) > INT_MAX || (t->size(2) > 1 && t->stride(2) != 1))
+    refuse(VDX_ERR_ARG, "%s must be a float32 tensor [%d, %d, >= %lld] on %s, the entries of a head contiguous", name, cache.c.seqs,
+           cache.c.Hkv, static_cast<long long>(least), dev(*cache.k).c_str());
+  forward_only(name, *t);
+  return *t;
+}
+
+PyObject* weights(PyObject* const* a) {
+  Cache cache(a[1], a[2], a[3], a[14], a[15], false);
+  vdx_paged_attn_args y{};
+  const at::Tensor& q = paged_args(a, &cache, &y);
+  vdx_paged_weights_args x{};
+  x.q = y.q; x.q_row = y.q_row; x.q_head = y.q_head; x.rows = y.rows; x.Hq = y.Hq;
+  x.cu = y.cu; x.kv_len = y.kv_len; x.max_q = y.max_q; x.max_kv = y.max_kv;
+  const at::Tensor* lse = cuda_tensor(a[8]);
+  const int64_t lse_shape[2] = {x.Hq, x.rows};
+  if (!lse || lse->scalar_type() != at::kFloat || lse->sizes() != at::IntArrayRef(lse_shape) || !lse->is_contiguous() ||
+      lse->device() != q.device())
+    refuse(VDX_ERR_ARG, "lse must be a contiguous float32 tensor of shape %s on %s", text(lse_shape).c_str(), dev(q).c_str());
+  forward_only("lse", *lse);
+  const at::Tensor& w = gathered("weights", a[9], cache, 0);
+  x.lse = static_cast<const float*>(address(*lse));
+  x.w = static_cast<float*>(w.mutable_data_ptr());
+  x.w_seq = w.stride(0); x.w_head = w.stride(1);
+  x.width = static_cast<int>(w.size(2));
+  x.causal_block = integer("causal_block", a[10]);
+  x.scale = static_cast<float>(real(a[11]));
+  x.decay = static_cast<float>(real(a[12]));
+  x.pos_offset = int32s("pos_offset", a[13], q, cache.c.seqs);
+  call(q, [&](void* stream) { return g_weights(&cache.c, cache.scales(), &x, stream); });
+  written(w);
+  return Py_NewRef(a[9]);
+}
+
+// k, v, table, k_scale, v_scale of a cache; weights, kv_len, keep, recent, max_kv, pos_offset, weights_out; the five of `into`
+PyObject* evict(PyObject* const* a) {
+  Cache cache(a[0], a[1], a[2], a[3], a[4], false);
+  Cache into(a[12], a[13], a[14], a[15], a[16], true);
+  const at::Tensor& like = *cache.k;
+  if (into.eight != cache.eight || into.k->device() != like.device())
+    refuse(VDX_ERR_ARG, "the two caches must be of one type and on one device");
+  vdx_paged_evict_args x{};
+  x.keep = integer("keep", a[7]);
+  x.recent = integer("recent", a[8]);
+  x.max_kv = bound("max_kv", a[9]);
+  if (x.keep < 1) refuse(VDX_ERR_ARG, "keep must be >= 1");
+  const at::Tensor& w = gathered("weights", a[5], cache, 0);
+  x.w = static_cast<const float*>(address(w));
+  x.w_seq = w.stride(0); x.w_head = w.stride(1);
+  x.width = static_cast<int>(w.size(2));
+  x.kv_len = int32s("kv_len", a[6], like, cache.c.seqs);
+  x.pos_offset = int32s("pos_offset", a[10], like, cache.c.seqs);
+  const c10::cuda::CUDAGuard guard(like.device());
+  at::Tensor w_out = a[11] == Py_None ? empty({cache.c.seqs, cache.c.Hkv, x.keep}, like, at::kFloat)
+                                      : gathered("weights_out", a[11], cache, x.keep);
+  x.w_out = static_cast<float*>(w_out.mutable_data_ptr());
+  x.w_out_seq = w_out.stride(0); x.w_out_head = w_out.stride(1);
+  at::Tensor kv_len = empty({cache.c.seqs}, like, at::kInt), offset = empty({cache.c.seqs}, like, at::kInt);
+  at::Tensor index = empty({cache.c.seqs, cache.c.Hkv, x.keep}, like, at::kInt);
+  x.kv_len_out = static_cast<int32_t*>(kv_len.mutable_data_ptr());
+  x.pos_offset_out = static_cast<int32_t*>(offset.mutable_data_ptr());
+  x.index = static_cast<int32_t*>(index.mutable_data_ptr());
+  call(like, [&](void* stream) { return g_evict(&cache.c, cache.scales(), &into.c, into.scales(), &x, stream); });
+  into.mark_written();
+  if (a[11] != Py_None) written(w_out);
+  PyObject* out[4] = {THPVariable_Wrap(kv_len), THPVariable_Wrap(offset), a[11] == Py_None ? THPVariable_Wrap(w_out) : Py_NewRef(a[11]),
+                      THPVariable_Wrap(index)};
+  PyObject* r = out[0] && out[1] && out[2] && out[3] ? PyTuple_Pack(4, out[0], out[1], out[2], out[3]) : nullptr;
+  for (PyObject* o : out) Py_XDECREF(o);
+  return r;
 }
 
 // q, k, v, kv_len of a cross-attention call
@@ -395,14 +527,19 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // bind(VdxError, addresses of the library's functions in the order below)
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* error;
-  unsigned long long f[6];
-  if (!PyArg_ParseTuple(args, "OKKKKKK", &error, f, f + 1, f + 2, f + 3, f + 4, f + 5)) return nullptr;
+  unsigned long long f[11];
+  if (!PyArg_ParseTuple(args, "OKKKKKKKKKKK", &error, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, f + 8, f + 9, f + 10)) return nullptr;
   g_append = reinterpret_cast<decltype(g_append)>(f[0]);
   g_paged = reinterpret_cast<decltype(g_paged)>(f[1]);
   g_paged_size = reinterpret_cast<decltype(g_paged_size)>(f[2]);
   g_cross = reinterpret_cast<decltype(g_cross)>(f[3]);
   g_cross_size = reinterpret_cast<decltype(g_cross_size)>(f[4]);
-  g_last_error = reinterpret_cast<decltype(g_last_error)>(f[5]);
+  g_append8 = reinterpret_cast<decltype(g_append8)>(f[5]);
+  g_paged8 = reinterpret_cast<decltype(g_paged8)>(f[6]);
+  g_paged8_size = reinterpret_cast<decltype(g_paged8_size)>(f[7]);
+  g_weights = reinterpret_cast<decltype(g_weights)>(f[8]);
+  g_evict = reinterpret_cast<decltype(g_evict)>(f[9]);
+  g_last_error = reinterpret_cast<decltype(g_last_error)>(f[10]);
   Py_INCREF(error);
   Py_XSETREF(g_error, error);
   Py_RETURN_NONE;
@@ -412,9 +549,11 @@ PyObject* bind(PyObject*, PyObject* args) {
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name, n>)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
-    VDX_ENTRY(append, 16),
-    VDX_ENTRY(paged, 15),
-    VDX_ENTRY(paged_size, 8),
+    VDX_ENTRY(append, 18),
+    VDX_ENTRY(paged, 17),
+    VDX_ENTRY(paged_size, 10),
+    VDX_ENTRY(weights, 16),
+    VDX_ENTRY(evict, 17),
     VDX_ENTRY(cross, 9),
     VDX_ENTRY(cross_size, 4),
     {nullptr, nullptr, 0, nullptr},

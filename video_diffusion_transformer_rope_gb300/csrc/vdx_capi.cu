@@ -439,7 +439,7 @@ vdx_status vdx_sync_check(void* stream) {
   unsigned int word = 0;
   e = vdx::read_and_clear_error_word_sm103(&word);
   for (auto read : {vdx::read_and_clear_error_word_append, vdx::read_and_clear_error_word_rows,
-                    vdx::read_and_clear_error_word_tiles}) {
+                    vdx::read_and_clear_error_word_tiles, vdx::read_and_clear_error_word_weigh, vdx::read_and_clear_error_word_evict}) {
     unsigned int more = 0;
     if (e == cudaSuccess) e = read(&more);
     word |= more;
@@ -458,6 +458,8 @@ vdx_status vdx_sync_check(void* stream) {
     return fail(VDX_ERR_ARG, "cu or kv_len broke a bound of its call (rows, max_q, max_kv); it was clamped, or its tokens not appended");
   if (word & vdx::kErrPosition)
     return fail(VDX_ERR_ARG, "an appended token was outside the position grid or its page table; it was skipped");
+  if (word & vdx::kErrRange8)
+    return fail(VDX_ERR_RANGE, "a key or value was past 448 * 2^%d, the largest that an 8-bit cache holds, and was clamped to it", VDX_KV8_MAX_EXP);
   return VDX_OK;
 }
 

@@ -1,9 +1,10 @@
-"""Streaming and conditioning calls: appending new tokens to a paged key/value cache, attention of
-those tokens over it, and cross attention to an encoder's states (include/vdx.h describes each
-operation).  The arguments are marshalled by the compiled module _streaming_py (csrc/streaming_py.cpp),
+"""Streaming and conditioning calls: appending new tokens to a paged key/value cache (of 16 or 8 bits), attention of
+those tokens over it, the weight that its keys gather and their eviction, and cross attention to an encoder's
+states (include/vdx.h describes each operation).  The arguments are marshalled by the compiled module _streaming_py (csrc/streaming_py.cpp),
 since these calls are short: no fallback, and every call that the library cannot take raises VdxError
 before anything is launched.
 """
+import collections
 import contextlib
 import ctypes
 from dataclasses import dataclass
@@ -35,7 +36,8 @@ def _load():
                            "build them again with video_diffusion_transformer_rope_gb300._build.build()")
     native.bind(VdxError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.vdx_rope3d_append, L.vdx_paged_attn_offset, L.vdx_paged_attn_workspace_bytes, L.vdx_cross_attn,
-        L.vdx_cross_attn_workspace_bytes, L.vdx_last_error)))
+        L.vdx_cross_attn_workspace_bytes, L.vdx_rope3d_append8, L.vdx_paged_attn8, L.vdx_paged_attn8_workspace_bytes,
+        L.vdx_paged_attn_weights, L.vdx_paged_evict, L.vdx_last_error)))
     _native = native
     return native
 
@@ -55,10 +57,20 @@ class PagedKV:
     """A paged key/value cache: k and v [num_pages, page_size, Hkv, d] (bf16 or fp16 CUDA tensors;
     any token / head order, for example a permuted [num_pages, Hkv, page_size, d]) and page_table
     [seqs, max_pages] int32.  Key c of sequence s is token c % page_size of page
-    page_table[s, c // page_size].  page_size: 16, 32, 64 or any size >= 128."""
+    page_table[s, c // page_size].  page_size: 16, 32, 64 or any size >= 128.
+
+    In 8 bits k and v are float8_e4m3fn, and k_scale, v_scale [num_pages, ceil(page_size / 16), Hkv]
+    float8_e8m0fnu: a power of two for every KV8_BLOCK = 16 tokens of a page and head, which their codes are
+    multiplied by.  The other tensors of a call over such a cache are bf16 or fp16, whichever they are."""
     k: Any
     v: Any
     page_table: Any
+    k_scale: Any = None
+    v_scale: Any = None
+
+
+KV8_BLOCK = 16
+Evicted = collections.namedtuple("Evicted", ["kv_len", "pos_offset", "weights", "index"])
 
 
 def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10000.0, pos_offset=None, q_norm=None,
@@ -71,14 +83,18 @@ def rope3d_append(q, k, v, cache, cu, kv_len, grid, sections=(0, 0, 0), theta=10
     sequence with the new ones.  grid = (T, Hgrid, Wgrid): the new token with cache index c stands at
     grid token pos_offset[s] + c.  q_norm / k_norm: [d] weights of a per-head RMS norm applied before
     the rotation (a norm over all heads of a token goes before the call).  Slices of a fused projection are taken as they are.  Two rows of a call must not land in
-    one slot (a page that two sequences share and both write): it would hold pieces of both."""
+    one slot (a page that two sequences share and both write): it would hold pieces of both.
+
+    An 8-bit cache gets codes of the fp32 keys and values and the scales of the blocks that they land in (a scale grows
+    where new values need it, and the block's older codes are rounded again); sync_check() reports values past
+    448 * 2^7, which are clamped.  Two sequences must not append into one block of such a cache."""
     call = (_native or _load()).append
     if stream is None:
         return call(q, k, v, cache.k, cache.v, cache.page_table, cu, kv_len, pos_offset, q_norm, k_norm, eps, q_out, grid,
-                    sections, theta)
+                    sections, theta, cache.k_scale, cache.v_scale)
     with _on(stream, cache.k):
         return call(q, k, v, cache.k, cache.v, cache.page_table, cu, kv_len, pos_offset, q_norm, k_norm, eps, q_out, grid,
-                    sections, theta)
+                    sections, theta, cache.k_scale, cache.v_scale)
 
 
 def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, scale=0.0, out=None, lse=None,
@@ -98,15 +114,54 @@ def paged_attn(q, cache, cu, kv_len, max_q=None, max_kv=None, causal_block=0, sc
     call = (_native or _load()).paged
     if stream is None:
         return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, causal_block, scale, out, lse, return_lse,
-                    workspace, pos_offset)
+                    workspace, pos_offset, cache.k_scale, cache.v_scale)
     with _on(stream, q):
         return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, causal_block, scale, out, lse, return_lse,
-                    workspace, pos_offset)
+                    workspace, pos_offset, cache.k_scale, cache.v_scale)
 
 
 def paged_attn_workspace_bytes(q, cache, cu, kv_len, max_q=None, max_kv=None):
     """Bytes of scratch that paged_attn needs for these arguments."""
-    return (_native or _load()).paged_size(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv)
+    return (_native or _load()).paged_size(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, cache.k_scale,
+                                               cache.v_scale)
+
+
+def paged_attn_weights(q, cache, cu, kv_len, lse, weights, max_q=None, max_kv=None, causal_block=0, scale=0.0, decay=1.0,
+                       pos_offset=None, stream=None):
+    """Add up, key by key, what the rows of a paged_attn call weighed: weights float32 [seqs, Hkv, width], in place (and
+    returned).  Arguments as in that call, with the lse [Hq, rows] that it returned.  For each sequence with rows,
+
+        weights[s, h, c] = decay * weights[s, h, c] + sum over rows and query heads of group h of exp(score - lse)
+
+    for its keys c, those of the call's own rows starting from 0, so the buffer needs no clearing.  Keys that a row does
+    not see get nothing from it; entries past a sequence's keys, and sequences without rows, stay as they are."""
+    call = (_native or _load()).weights
+    if stream is None:
+        return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, lse, weights, causal_block, scale, decay,
+                    pos_offset, cache.k_scale, cache.v_scale)
+    with _on(stream, q):
+        return call(q, cache.k, cache.v, cache.page_table, cu, kv_len, max_q, max_kv, lse, weights, causal_block, scale, decay,
+                    pos_offset, cache.k_scale, cache.v_scale)
+
+
+def paged_evict(cache, weights, kv_len, keep, into, recent=0, max_kv=None, pos_offset=None, weights_out=None, stream=None):
+    """Evict from `cache` the keys that gathered least, for each sequence and kv head: of more than `keep` keys the last
+    `recent` stay and, of the others, the keep - recent with the largest weights (of equals the first); of fewer, all.
+    What stays moves, in order, to cache indices 0, 1, .. of `into`: a PagedKV of the same kind with another page
+    table, in the same pools or others, whose pages the call must not read too.  Afterwards the old pages are free.
+
+    weights: float32 [seqs, Hkv, width], from paged_attn_weights (float("inf") pins a key, NaN counts as the largest).
+    Returns Evicted(kv_len, pos_offset, weights, index): the new lengths; the position offsets with which the next
+    tokens are appended and attend (pos_offset, or 0, and what each sequence lost); the weights of what stayed and
+    the old cache indices of it, [seqs, Hkv, keep] with 0 and -1 past the new lengths.  weights_out: a buffer for the
+    weights, at least keep wide; it may be `weights` itself."""
+    call = (_native or _load()).evict
+    if stream is None:
+        return Evicted(*call(cache.k, cache.v, cache.page_table, cache.k_scale, cache.v_scale, weights, kv_len, keep, recent, max_kv,
+                             pos_offset, weights_out, into.k, into.v, into.page_table, into.k_scale, into.v_scale))
+    with _on(stream, cache.k):
+        return Evicted(*call(cache.k, cache.v, cache.page_table, cache.k_scale, cache.v_scale, weights, kv_len, keep, recent, max_kv,
+                             pos_offset, weights_out, into.k, into.v, into.page_table, into.k_scale, into.v_scale))
 
 
 def cross_attn(q, k, v, kv_len=None, scale=0.0, out=None, lse=None, return_lse=True, stream=None, workspace=None):
