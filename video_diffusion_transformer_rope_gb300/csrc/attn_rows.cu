@@ -72,16 +72,14 @@ attn_rows(const __grid_constant__ KvParams p) {
 
   const int z = blockIdx.x % p.nsplit;
   const int unit = blockIdx.x / p.nsplit;
-  // all rows of a kv head are one block (max_q * g <= kRows), but for 8-bit caches where they may be many
-  const int sh = k8 ? unit / p.nblk : unit, first = k8 ? (unit - sh * p.nblk) * kRows : 0;
-  const int hk = sh % p.Hkv, s = sh / p.Hkv;
+  const int hk = unit % p.Hkv, s = unit / p.Hkv;        // all rows of a kv head are one block
   const SeqInfo sq = sequence_info(p, s, threadIdx.x == 0);
-  const int live = min(min(sq.n, p.max_q) * p.g - first, kRows);
-  if (live <= 0) return;
+  const int live = min(sq.n, p.max_q) * p.g;            // max_q * g <= kRows
+  if (live == 0) return;
 
   // Keys of this split, up to the last row's limit: an equal part for each CTA of a cluster, which
   // wait for one another; fixed ranges otherwise (a CTA past a short sequence's end leaves).
-  const int len = visible_limit(p, sq, (first + live - 1) / p.g);
+  const int len = visible_limit(p, sq, (live - 1) / p.g);
   const long long keys = p.cluster ? (len / (kKeys * kWarps) / p.nsplit + 1) * (kKeys * kWarps) : p.split_keys;
   const long long lo64 = z * keys;
   const int lo = static_cast<int>(min(lo64, static_cast<long long>(len)));
@@ -96,7 +94,7 @@ attn_rows(const __grid_constant__ KvParams p) {
     const int r = nt * 8 + gq;
     const T* src = nullptr;
     if (r < live) {
-      const int R = first + r, tok = R / p.g, h = hk * p.g + (R - tok * p.g);
+      const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
       src = static_cast<const T*>(p.q) + (p.cu ? 0 : s * p.q_b) + (static_cast<long long>(sq.row0) + tok) * p.q_t + h * p.q_h;
     }
 #pragma unroll
@@ -108,12 +106,12 @@ attn_rows(const __grid_constant__ KvParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = nt * 8 + 2 * c4 + e;
-      limit[nt][e] = rr < live ? min(visible_limit(p, sq, (first + rr) / p.g), hi) : hi;
+      limit[nt][e] = rr < live ? min(visible_limit(p, sq, rr / p.g), hi) : hi;
     }
   }
   // Below this key every row sees everything.
   const int full_to = p.causal_block > 0
-                          ? min(hi, visible_limit(p, sq, first / p.g))
+                          ? min(hi, visible_limit(p, sq, 0))
                           : hi;
 
   float o[kNT][D / 16][4];
@@ -369,7 +367,7 @@ attn_rows(const __grid_constant__ KvParams p) {
   float* cm = sl + kWarps * kRows;                                  // [kRows]: this CTA's maximum and sum
   float* cl = cm + kRows;
   auto store = [&](int r, int dq, float mx, float lt, const float4& acc) {
-    const int R = first + r, tok = R / p.g, h = hk * p.g + (R - tok * p.g);
+    const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
     const bool none = mx == -INFINITY && lt == lt;                  // no key seen; a NaN sum is an answer
     const float inv = none ? 0.f : 1.f / lt;
     uint2 w2;

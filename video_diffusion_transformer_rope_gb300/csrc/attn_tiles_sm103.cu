@@ -28,6 +28,8 @@
 //                    ranges: divisions and dependent loads, ~2000 cycles), and loads their Q tiles
 //   warp 11          stores finished output tiles: one TMA store, or the live rows of a tile that
 //                    ends with its sequence
+//   warps 12-15      8-bit caches only, in warp 8's place: load codes and write them to the K and V rings
+//                    as the values they stand for
 //
 // TMEM (512 columns): S0, S1 at 0 and 128, O0, O1 at 256 and 384; P overwrites the first half of S
 // as packed 16-bit pairs and is the A operand of the second product.  Issue order per key tile j:
@@ -43,6 +45,7 @@
 // anything there), and scores of keys past the limit become -inf, whatever K holds.
 #include <cstdint>
 
+#include "kv8.cuh"
 #include "kv_common.cuh"
 
 namespace vdx {
@@ -51,12 +54,15 @@ namespace {
 constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kThreads = 384;
+constexpr int kThreads8 = 512;     // with the converters of an 8-bit cache
 constexpr int kTmemCols = 512;
 constexpr int kQBufs = 4;          // two Q tiles of two units
 constexpr int kUnitSlots = 4;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kRegsSoftmax = 192, kRegsCtl = 120;     // 2 x 192 + 120 = 3 x 168 at launch
 static_assert(2 * kRegsSoftmax + kRegsCtl <= 3 * 168, "register split over budget");
+constexpr uint32_t kRegsSoftmax8 = 192, kRegsCtl8 = 64, kRegsConvert = 64;
+static_assert(2 * kRegsSoftmax8 + kRegsCtl8 + kRegsConvert <= 4 * 128, "register split over budget");
 
 // Shared memory of one CTA.  Q tiles and K halves are 64-channel parts of 128-byte swizzled rows; a V
 // half is 128 rows of D/2 channels (one part of 128-byte rows, or of 64-byte rows at D = 64).
@@ -301,6 +307,7 @@ struct UnitReader {
 };
 #define VDX_UNIT(reader, field) (reader).get(offsetof(Unit, field))
 constexpr int kUnitReaders = 8 + 3;     // softmax warps, producer, MMA / relay, store
+constexpr int kUnitReaders8 = 8 + 4 + 2;      // converters in the producer's place
 
 // S = Q K^T over the pair (M = 256, N = 128): A = each CTA's Q tile, B = 64 keys from each CTA.
 // The whole MMA warp calls, one elected lane issues.
@@ -420,10 +427,59 @@ __device__ __noinline__ void zero_v_rows(uint32_t v_smem, int from, int lane) {
   __syncwarp();
 }
 
+// Four codes as two pairs of T, times 2^e given by scale_pair<T>(e); exact.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_pair(int e);
+template <>
+__device__ __forceinline__ uint32_t scale_pair<__half>(int e) {
+  return half_two_to(e) * 0x10001u;
+}
+template <>
+__device__ __forceinline__ uint32_t scale_pair<__nv_bfloat16>(int e) {
+  return static_cast<uint32_t>(e + 120 + 127) << 7 | static_cast<uint32_t>(e + 120 + 127) << 23;
+}
+template <typename T>
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi);
+template <>
+__device__ __forceinline__ void expand4<__half>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  lo = half2_mul(decode2<false>(w), scale);
+  hi = half2_mul(decode2<true>(w), scale);
+}
+// A code's exponent and mantissa, moved to where bf16 has its own, are its value times 2^-120 (subnormals too).
+template <>
+__device__ __forceinline__ void expand4<__nv_bfloat16>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  const uint32_t h[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t m = (h[i] & 0x7f007f00u) >> 4;
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&scale));
+    r[i] = *reinterpret_cast<const uint32_t*>(&v) | (h[i] & 0x80008000u);
+  }
+  lo = r[0];
+  hi = r[1];
+}
+// 16 codes of row r, channels 16 c and up of a 64-channel part of 128-byte swizzled rows (64-byte ones: kRow 64).
+template <typename T, int kRow>
+__device__ __forceinline__ void expand_chunk(uint32_t part, int r, int c, const uint4& x, uint32_t scale) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) expand4<T>(w[i], scale, y[2 * i], y[2 * i + 1]);
+  const int turn = kRow == 128 ? r & 7 : (r >> 1) & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st_shared_v4(part + r * kRow + (((2 * c + i) ^ turn) << 4), make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
+}
+
 // One instance per kind of keys and of results, so that none carries the others' code: in this
 // kernel, whose roles' code does not fit the instruction caches, that is time.
-template <typename T, int D, bool kPaged, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+//
+// k8: the cache holds 8-bit codes with scales.  Four more warps load this CTA's halves of a tile's keys and values
+// themselves, 16 bytes a lane, a lane looking up the page and the scales of a key and of a value for the others of its
+// warp, and write them to the rings as T times their scale, which is exact; the rest is as for 16 bits.
+template <typename T, int D, bool kPaged, bool kSplit, bool k8>
+__global__ void __launch_bounds__(k8 ? kThreads8 : kThreads, 1)
 attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kbox,
            const __grid_constant__ CUtensorMap tm_vbox, const __grid_constant__ CUtensorMap tm_out,
@@ -442,6 +498,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // rank 0's full barriers also count one relayed arrival from rank 1, its P-ready and O-empty
     // barriers one arrival from each of rank 1's softmax warps
     const uint32_t full = leader ? 2 : 1, rows = leader ? 128 + 4 : 128;
+    const uint32_t landed = k8 ? full + 3 : full;       // K and V: a converter warp each in place of the one producer
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(smem_addr(&ctl->q_full[i]), full);
       mbar_init(smem_addr(&ctl->q_empty[i]), 1);
@@ -454,14 +511,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       mbar_init(smem_addr(&ctl->staged[i]), 128);
     }
     for (int i = 0; i < kS; ++i) {
-      mbar_init(smem_addr(&ctl->k_full[i]), full);
+      mbar_init(smem_addr(&ctl->k_full[i]), landed);
       mbar_init(smem_addr(&ctl->k_empty[i]), 1);
-      mbar_init(smem_addr(&ctl->v_full[i]), full);
+      mbar_init(smem_addr(&ctl->v_full[i]), landed);
       mbar_init(smem_addr(&ctl->v_empty[i]), 1);
     }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(smem_addr(&ctl->unit_full[i]), 1);
-      mbar_init(smem_addr(&ctl->unit_empty[i]), kUnitReaders);
+      mbar_init(smem_addr(&ctl->unit_empty[i]), k8 ? kUnitReaders8 : kUnitReaders);
     }
     mbar_init(smem_addr(&ctl->claim_full), 1);
     mbar_init(smem_addr(&ctl->claim_ready), 2);          // both CTAs' (used on rank 0)
@@ -486,9 +543,117 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     return warp_wait(bar, parity & 1, sCtl + kOffAbort, site);
   };
 
-  if (warp >= 8) {
-    regs_decrease<kRegsCtl>();
-    if (warp == 8) {
+  // K and V from the other CTA: its copies' bytes, or (k8) what its converters wrote, which the relay announces
+  // with a cluster-scope release
+  auto wait_landed = [&](uint32_t bar, int parity, int site) {
+    return warp_wait<k8>(bar, parity & 1, sCtl + kOffAbort, site);
+  };
+  auto tell_landed = [&](uint32_t bar) {
+    if (k8)
+      mbar_arrive_remote_cluster(mapa_shared(bar, 0));
+    else
+      mbar_arrive_remote(mapa_shared(bar, 0));
+  };
+
+  if (k8 && warp >= 12) {
+    // -------------------------------------------------------------------- converters of 8-bit keys and values
+    regs_decrease<kRegsConvert>();
+    constexpr int kKLanes = D / 16, kKStep = 32 / kKLanes, kKLoads = 16 / kKStep;        // K: 16 keys a warp
+    constexpr int kVLanes = D / 32, kVStep = 32 / kVLanes, kVLoads = 32 / kVStep;        // V: 32 keys, this CTA's channels
+    const int cw = warp - 12;
+    const int kc = lane % kKLanes, kr = lane / kKLanes, vc = lane % kVLanes, vr = lane / kVLanes;
+    int kv = 0;
+    bool ok = true;
+    UnitReader in{sCtl};
+    while (ok) {
+      if (!(ok = in.wait())) break;
+      if (VDX_UNIT(in, s) < 0) {
+        in.release();
+        break;
+      }
+      const int t0 = VDX_UNIT(in, t0), t1 = VDX_UNIT(in, t1), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk), len = VDX_UNIT(in, len);
+      in.release();
+      if (t0 >= t1) continue;
+      const int* table = p.table + static_cast<long long>(s) * p.table_stride;
+      const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + hk * p.k_h + kc * 16;
+      const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + hk * p.v_h + static_cast<int>(rank) * (D / 2) + vc * 16;
+      const uint8_t* kscale = p.scales.k + hk * p.scales.k_head;
+      const uint8_t* vscale = p.scales.v + hk * p.scales.v_head;
+      TileCursor<kPaged> c;
+      c.seek(p, geom, t0);
+      uint4 xk[kKLoads], xv[kVLoads];
+      int ek, ev;                                       // this lane's key's and value's exponents
+      // Row `row` of the tile at c, which this lane looks up: its page (negative: zeros) and slot.
+      auto look_up = [&](int row, int& page, int& slot) {
+        slot = c.off + row;
+        int e = c.page;
+        while (slot >= p.P) {
+          slot -= p.P;
+          ++e;
+        }
+        page = -1;
+        if (c.key0 + row < len) {
+          page = load_i32(table + e);
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+            atomicOr(&g_error_word, kErrPage);
+            page = -1;
+          }
+        }
+      };
+      auto load_keys = [&] {
+        int page, slot;
+        look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), page, slot);
+        ek = page < 0 ? 0 : scale_exponent(kscale[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block]);
+        const long long at = page < 0 ? -1 : page * p.k_p + slot * p.k_t;
+#pragma unroll
+        for (int i = 0; i < kKLoads; ++i) {
+          const long long from = __shfl_sync(0xffffffffu, at, i * kKStep + kr);
+          xk[i] = from < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_b128(kbase + from);
+        }
+      };
+      auto load_values = [&] {
+        int page, slot;
+        look_up(cw * 32 + lane, page, slot);
+        ev = page < 0 ? 0 : scale_exponent(vscale[page * p.scales.v_page + slot / kBlock8 * p.scales.v_block]);
+        const long long at = page < 0 ? -1 : page * p.v_p + slot * p.v_t;
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) {
+          const long long from = __shfl_sync(0xffffffffu, at, i * kVStep + vr);
+          xv[i] = from < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_b128(vbase + from);
+        }
+      };
+      load_keys();
+      load_values();
+      for (int t = t0; t < t1; ++t) {
+        const int st = kv % kS;
+        c.next(p);
+        if (kv >= kS && !(ok = wait(sCtl + kBarKEmpty + 8 * st, kv / kS - 1, kSiteKEmpty))) break;
+        const uint32_t kt = sK + st * Lo::kStageBytes + kc / 4 * Lo::kKPart;
+#pragma unroll
+        for (int i = 0; i < kKLoads; ++i)
+          expand_chunk<T, 128>(kt, cw * 16 + i * kKStep + kr, kc % 4, xk[i], scale_pair<T>(__shfl_sync(0xffffffffu, ek, i * kKStep + kr)));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sCtl + kBarKFull + 8 * st);
+        if (t + 1 < t1) load_keys();                    // the next tile's, while this one's values are written
+        if (kv >= kS && !(ok = wait(sCtl + kBarVEmpty + 8 * st, kv / kS - 1, kSiteVEmpty))) break;
+        const uint32_t vt = sV + st * Lo::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i)
+          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, xv[i], scale_pair<T>(__shfl_sync(0xffffffffu, ev, i * kVStep + vr)));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sCtl + kBarVFull + 8 * st);
+        if (t + 1 < t1) load_values();
+        ++kv;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    regs_decrease<k8 ? kRegsCtl8 : kRegsCtl>();
+    if (k8 && warp == 8) {
+      // the converters do its work
+    } else if (warp == 8) {
       // ------------------------------------------------------------------ TMA producer
       if (lane == 0) {
         tma_prefetch_desc(&tm_k);
@@ -629,7 +794,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
         const uint32_t q_full = sCtl + kBarQFull + 8 * (2 * (n & 1));
-        if (!(ok = wait(q_full, qph, kSiteQFull) && wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
+        if (!(ok = wait(q_full, qph, kSiteQFull) && wait_landed(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
         bool fresh = true;
         while (true) {
           const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
@@ -651,8 +816,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             mma_commit_pair_warp(sCtl + kBarSFull + 8);
             mma_commit_pair_warp(sCtl + kBarKEmpty + 8 * st);
           }
-          ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
-          if (end && tail < kBN) {
+          ok = wait_landed(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
+          if (!k8 && end && tail < kBN) {
             // rank 1 zeroed rows of its half before it arrived: seen at cluster scope (the phase is complete,
             // so this returns at once)
             if (ok) ok = warp_wait<true>(sCtl + kBarVFull + 8 * st, ph, sCtl + kOffAbort, kSiteVFull);
@@ -665,7 +830,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             st = 0;
             ph ^= 1;
           }
-          if (!end && ok) ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
+          if (!end && ok) ok = wait_landed(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
           if (ok) ok = wait(sCtl + kBarPReady, pr0, kSitePReady);
           pr0 ^= 1;
           if (fresh && n > 0 && ok) ok = wait(sCtl + kBarOEmpty, n + 1, kSiteOEmpty);
@@ -713,13 +878,13 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         for (; ok && left > 0; --left) {
           if (!(ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteRelay))) break;
-          if (lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarKFull + 8 * st, 0));
+          if (lane == 0) tell_landed(sCtl + kBarKFull + 8 * st);
           if (!(ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteRelay))) break;
-          if (left == 1 && tail < kBN) {
+          if (!k8 && left == 1 && tail < kBN) {
             zero_v_rows<D>(sV + st * Lo::kStageBytes, tail, lane);
             if (lane == 0) mbar_arrive_remote_cluster(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
           } else if (lane == 0) {
-            mbar_arrive_remote(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
+            tell_landed(sCtl + kBarVFull + 8 * st);
           }
           if (++st == kS) {
             st = 0;
@@ -866,7 +1031,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     __syncwarp();
   } else {
     // -------------------------------------------------------------------- softmax + epilogue
-    regs_increase<kRegsSoftmax>();
+    regs_increase<k8 ? kRegsSoftmax8 : kRegsSoftmax>();
     const int qi = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -1074,7 +1239,7 @@ bool encode_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, int D
 
 template <typename T, int D>
 cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_t stream, const char** what) {
-  CUtensorMap mq, mk, mv, mkb{}, mvb{}, mo;            // no boxes: their maps are never used
+  CUtensorMap mq, mk{}, mv{}, mkb{}, mvb{}, mo;        // no boxes, 8 bits: their maps are never used
   const bool one_q = p.cu != nullptr || p.q_b == 0;
   const bool has_keys = p.P > 0;
   // dimensions: q and out (d, head, token, batch), k and v (d, token, head, page)
@@ -1084,9 +1249,9 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
   const int P = has_keys ? p.P : 1;
   const long long ob = static_cast<long long>(p.N) * p.Hq * D;
   if (!encode_rows<T>(encode, &mq, p.q, D, p.Hq, p.q_h, p.N, p.q_t, one_q ? 1 : p.S, p.q_b, 64, p.g, kBM / p.g) ||
-      !encode_rows<T>(encode, &mk, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, kBN / 2, 1) ||
-      !encode_rows<T>(encode, &mv, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, kBN, 1) ||
-      (p.box_rows && (!encode_rows<T>(encode, &mkb, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, p.box_rows, 1) ||
+      (!p.eight && (!encode_rows<T>(encode, &mk, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, kBN / 2, 1) ||
+                    !encode_rows<T>(encode, &mv, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, kBN, 1))) ||
+      (!p.eight && p.box_rows && (!encode_rows<T>(encode, &mkb, k, D, P, p.k_t, p.Hkv, p.k_h, kpages, p.k_p, 64, p.box_rows, 1) ||
                       !encode_rows<T>(encode, &mvb, v, D, P, p.v_t, p.Hkv, p.v_h, vpages, p.v_p, D / 2, p.box_rows, 1))) ||
       !encode_rows<T>(encode, &mo, p.out, D, p.Hq, D, p.N, static_cast<long long>(p.Hq) * D, p.cu ? 1 : p.S, ob, 64, p.g,
                       kBM / p.g)) {
@@ -1094,16 +1259,17 @@ cudaError_t launch(const KvParams& p, EncodeTiledFn encode, int sms, cudaStream_
     return cudaErrorInvalidValue;
   }
   const int smem = Layout<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
-  static std::atomic<uint64_t> done[4] = {};
-  auto* kernel = p.table ? (p.nsplit > 1 ? attn_tiles<T, D, true, true> : attn_tiles<T, D, true, false>)
-                         : (p.nsplit > 1 ? attn_tiles<T, D, false, true> : attn_tiles<T, D, false, false>);
-  const cudaError_t e = allow_shared(kernel, smem, &done[(p.table ? 2 : 0) + (p.nsplit > 1 ? 1 : 0)]);
+  static std::atomic<uint64_t> done[6] = {};
+  auto* kernel = p.eight   ? (p.nsplit > 1 ? attn_tiles<T, D, true, true, true> : attn_tiles<T, D, true, false, true>)
+                 : p.table ? (p.nsplit > 1 ? attn_tiles<T, D, true, true, false> : attn_tiles<T, D, true, false, false>)
+                           : (p.nsplit > 1 ? attn_tiles<T, D, false, true, false> : attn_tiles<T, D, false, false, false>);
+  const cudaError_t e = allow_shared(kernel, smem, &done[(p.eight ? 4 : p.table ? 2 : 0) + (p.nsplit > 1 ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (units > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * units));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(p.eight ? kThreads8 : kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

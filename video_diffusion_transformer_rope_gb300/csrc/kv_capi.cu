@@ -259,11 +259,10 @@ namespace vdx {
 size_t plan_attention(KvParams* p, int d, int sms) {
   const long long rows = static_cast<long long>(p->max_q) * p->g;
   p->rows_kernel = rows <= 32;
-  if (p->eight) p->rows_kernel = 1;
   if (p->rows_kernel) {
     p->block_rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-    p->nblk = static_cast<int>((rows - 1) / p->block_rows + 1);
-    const long long units = static_cast<long long>(p->S) * p->Hkv * p->nblk;
+    p->nblk = 1;
+    const long long units = static_cast<long long>(p->S) * p->Hkv;
     // Two CTAs to a multiprocessor, in one wave where the units leave room for splits: the most
     // splits that fit with a tenth to spare (clusters do not fill every group of processors), of at
     // least 192 keys.  16 x 8 heads over 8192 keys: 2 splits 84.7 us, 1 split 131, 4 (two waves) 93, 8
@@ -296,6 +295,7 @@ size_t plan_attention(KvParams* p, int d, int sms) {
     // largest power of two up to 64 that divides it is the box.  Dense keys are one page.
     p->box_rows = 0;
     if (p->table && p->P % 8 == 0) p->box_rows = std::min(64, p->P & -p->P);
+    if (p->eight) p->box_rows = 8;                    // no boxes: a lane looks up each key, whatever the page size
     long long tiles = 1;
     if (p->max_kv > 0)
       tiles = p->box_rows ? (p->max_kv + 127) / 128
