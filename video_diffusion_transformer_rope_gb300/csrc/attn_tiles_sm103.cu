@@ -61,7 +61,7 @@ constexpr int kUnitSlots = 4;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kRegsSoftmax = 192, kRegsCtl = 120;     // 2 x 192 + 120 = 3 x 168 at launch
 static_assert(2 * kRegsSoftmax + kRegsCtl <= 3 * 168, "register split over budget");
-constexpr uint32_t kRegsSoftmax8 = 192, kRegsCtl8 = 64, kRegsConvert = 64;
+constexpr uint32_t kRegsSoftmax8 = 144, kRegsCtl8 = 112, kRegsConvert = 112;
 static_assert(2 * kRegsSoftmax8 + kRegsCtl8 + kRegsConvert <= 4 * 128, "register split over budget");
 
 // Shared memory of one CTA.  Q tiles and K halves are 64-channel parts of 128-byte swizzled rows; a V
@@ -368,6 +368,44 @@ __device__ __forceinline__ float exp_row128(const uint32_t (&s)[128], float c, f
   return l0 + l1;
 }
 
+// The same in two halves of 64 columns, straight from tensor memory, for the instances whose converters need the
+// registers: `s` is not held, and the tile's maximum takes a walk of its own.
+__device__ __forceinline__ float row_max_halves(uint32_t s_tmem) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t s[64];
+    tmem_ld64(s_tmem + 64 * h, s);
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = fmax3(m[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + j + 4]));
+  }
+  return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+}
+template <typename T>
+__device__ __forceinline__ float exp_row_halves(uint32_t s_tmem, float c, float base, uint32_t (&pk)[64]) {
+  const uint64_t c2 = f32x2(c, c), nb2 = f32x2(-base, -base);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t s[64];
+    tmem_ld64(s_tmem + 64 * h, s);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const uint64_t a = ffma2(f32x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, nb2);
+      float a0, a1;
+      f32x2_split(a, a0, a1);
+      const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+      acc[e & 3] = fadd2(acc[e & 3], f32x2(p0, p1));
+      pk[32 * h + e] = pack2<T>(p0, p1);
+    }
+  }
+  float l0, l1;
+  f32x2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), l0, l1);
+  return l0 + l1;
+}
+
 // Scores of a row (this thread's TMEM lane) at column `valid` and beyond become -inf, in place: a
 // loop over 32 columns at a time, since ragged tiles are few and unrolled code in the row's path
 // costs the others instruction-cache misses.
@@ -579,11 +617,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + hk * p.v_h + static_cast<int>(rank) * (D / 2) + vc * 16;
       const uint8_t* kscale = p.scales.k + hk * p.scales.k_head;
       const uint8_t* vscale = p.scales.v + hk * p.scales.v_head;
-      TileCursor<kPaged> c;
+      TileCursor<kPaged> c;                             // of the tile whose pages are looked up: two ahead
       c.seek(p, geom, t0);
       uint4 xk[kKLoads], xv[kVLoads];
-      int ek, ev;                                       // this lane's key's and value's exponents
-      // Row `row` of the tile at c, which this lane looks up: its page (negative: zeros) and slot.
+      int ek, ev;                                       // scale bytes of this lane's key and value in xk, xv
+      int k_page, k_slot, v_page, v_slot;               // of the next tile's
+      // The row of the tile at c that this lane looks up: its page and slot (negative: a key that is not there).
       auto look_up = [&](int row, int& page, int& slot) {
         slot = c.off + row;
         int e = c.page;
@@ -591,20 +630,26 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           slot -= p.P;
           ++e;
         }
-        page = -1;
-        if (c.key0 + row < len) {
+        page = 0;
+        if (c.key0 + row < len)
           page = load_i32(table + e);
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-            atomicOr(&g_error_word, kErrPage);
-            page = -1;
-          }
-        }
+        else
+          slot = -1;
+      };
+      auto look_up_tile = [&] {
+        look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), k_page, k_slot);
+        look_up(cw * 32 + lane, v_page, v_slot);
+        c.next(p);
+      };
+      auto place = [&](int page, int slot, long long per_page, long long per_slot) {
+        if (slot < 0) return -1ll;
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page * per_page + slot * per_slot;
+        atomicOr(&g_error_word, kErrPage);
+        return -1ll;
       };
       auto load_keys = [&] {
-        int page, slot;
-        look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), page, slot);
-        ek = page < 0 ? 0 : scale_exponent(kscale[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block]);
-        const long long at = page < 0 ? -1 : page * p.k_p + slot * p.k_t;
+        const long long at = place(k_page, k_slot, p.k_p, p.k_t);
+        ek = at < 0 ? 127 : kscale[k_page * p.scales.k_page + k_slot / kBlock8 * p.scales.k_block];
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kKStep + kr);
@@ -612,39 +657,41 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
       };
       auto load_values = [&] {
-        int page, slot;
-        look_up(cw * 32 + lane, page, slot);
-        ev = page < 0 ? 0 : scale_exponent(vscale[page * p.scales.v_page + slot / kBlock8 * p.scales.v_block]);
-        const long long at = page < 0 ? -1 : page * p.v_p + slot * p.v_t;
+        const long long at = place(v_page, v_slot, p.v_p, p.v_t);
+        ev = at < 0 ? 127 : vscale[v_page * p.scales.v_page + v_slot / kBlock8 * p.scales.v_block];
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kVStep + vr);
           xv[i] = from < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_b128(vbase + from);
         }
       };
+      look_up_tile();
       load_keys();
       load_values();
+      look_up_tile();
       for (int t = t0; t < t1; ++t) {
         const int st = kv % kS;
-        c.next(p);
         if (kv >= kS && !(ok = wait(sCtl + kBarKEmpty + 8 * st, kv / kS - 1, kSiteKEmpty))) break;
         const uint32_t kt = sK + st * Lo::kStageBytes + kc / 4 * Lo::kKPart;
+        const uint32_t sk = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ek)));
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i)
-          expand_chunk<T, 128>(kt, cw * 16 + i * kKStep + kr, kc % 4, xk[i], scale_pair<T>(__shfl_sync(0xffffffffu, ek, i * kKStep + kr)));
+          expand_chunk<T, 128>(kt, cw * 16 + i * kKStep + kr, kc % 4, xk[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(sCtl + kBarKFull + 8 * st);
         if (t + 1 < t1) load_keys();                    // the next tile's, while this one's values are written
         if (kv >= kS && !(ok = wait(sCtl + kBarVEmpty + 8 * st, kv / kS - 1, kSiteVEmpty))) break;
         const uint32_t vt = sV + st * Lo::kStageBytes;
+        const uint32_t sv = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ev)));
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i)
-          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, xv[i], scale_pair<T>(__shfl_sync(0xffffffffu, ev, i * kVStep + vr)));
+          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, xv[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(sCtl + kBarVFull + 8 * st);
         if (t + 1 < t1) load_values();
+        if (t + 2 < t1) look_up_tile();
         ++kv;
       }
     }
@@ -1106,10 +1153,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           // one costs more in instruction-cache misses than the branches do.
           bool look = fresh;
           while (true) {
-            uint32_t s[128];
-            tmem_ld128(tS, s);
+            uint32_t s[k8 ? 1 : 128];
+            if constexpr (!k8) tmem_ld128(tS, s);
             if (look) {
-              const float mt = row_max128(s) * c;
+              float mt;
+              if constexpr (k8)
+                mt = row_max_halves(tS) * c;
+              else
+                mt = row_max128(s) * c;
               if (mt > m) {
                 alpha = ex2_approx(m - mt);
                 l *= alpha;
@@ -1117,7 +1168,11 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
               }
             }
             // a row without keys so far: its scores are -inf and weigh nothing
-            lt = exp_row128<T>(s, c, look && !(m > -INFINITY) ? 0.f : m, pk);
+            const float base = look && !(m > -INFINITY) ? 0.f : m;
+            if constexpr (k8)
+              lt = exp_row_halves<T>(tS, c, base, pk);
+            else
+              lt = exp_row128<T>(s, c, base, pk);
             if (look || !__any_sync(0xffffffffu, live && !(lt <= 256.f))) break;
             look = true;
           }
