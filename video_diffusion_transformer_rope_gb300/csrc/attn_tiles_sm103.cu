@@ -497,6 +497,15 @@ __device__ __forceinline__ void expand4<__nv_bfloat16>(uint32_t w, uint32_t scal
   lo = r[0];
   hi = r[1];
 }
+// 16 bytes to shared memory without waiting for them; zeros unless `live`.
+__device__ __forceinline__ void copy_code16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // 16 codes of row r, channels 16 c and up of a 64-channel part of 128-byte swizzled rows (64-byte ones: kRow 64).
 template <typename T, int kRow>
 __device__ __forceinline__ void expand_chunk(uint32_t part, int r, int c, const uint4& x, uint32_t scale) {
@@ -513,9 +522,10 @@ __device__ __forceinline__ void expand_chunk(uint32_t part, int r, int c, const 
 // One instance per kind of keys and of results, so that none carries the others' code: in this
 // kernel, whose roles' code does not fit the instruction caches, that is time.
 //
-// k8: the cache holds 8-bit codes with scales.  Four more warps load this CTA's halves of a tile's keys and values
-// themselves, 16 bytes a lane, a lane looking up the page and the scales of a key and of a value for the others of its
-// warp, and write them to the rings as T times their scale, which is exact; the rest is as for 16 bits.
+// k8: the cache holds 8-bit codes with scales.  Four more warps copy this CTA's halves of a tile's codes into the stages
+// they belong to, two tiles ahead, 16 bytes a lane (a lane looks up the page and the scales of a key and of a
+// value for the others of its warp); then they spread each row in place to T times its scale, which is exact.  A row's
+// codes and its values are the same lanes', so that a warp needs no other.  The rest is as for 16 bits.
 template <typename T, int D, bool kPaged, bool kSplit, bool k8>
 __global__ void __launch_bounds__(k8 ? kThreads8 : kThreads, 1)
 attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -536,7 +546,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // rank 0's full barriers also count one relayed arrival from rank 1, its P-ready and O-empty
     // barriers one arrival from each of rank 1's softmax warps
     const uint32_t full = leader ? 2 : 1, rows = leader ? 128 + 4 : 128;
-    const uint32_t landed = k8 ? full + 3 : full;       // K and V: a converter warp each in place of the one producer
+    const uint32_t landed = k8 ? 4 * full : full;       // K and V: both CTAs' converter warps instead of producer and relay
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(smem_addr(&ctl->q_full[i]), full);
       mbar_init(smem_addr(&ctl->q_empty[i]), 1);
@@ -581,25 +591,21 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     return warp_wait(bar, parity & 1, sCtl + kOffAbort, site);
   };
 
-  // K and V from the other CTA: its copies' bytes, or (k8) what its converters wrote, which the relay announces
-  // with a cluster-scope release
-  auto wait_landed = [&](uint32_t bar, int parity, int site) {
-    return warp_wait<k8>(bar, parity & 1, sCtl + kOffAbort, site);
-  };
-  auto tell_landed = [&](uint32_t bar) {
-    if (k8)
-      mbar_arrive_remote_cluster(mapa_shared(bar, 0));
-    else
-      mbar_arrive_remote(mapa_shared(bar, 0));
-  };
-
   if (k8 && warp >= 12) {
     // -------------------------------------------------------------------- converters of 8-bit keys and values
     regs_decrease<kRegsConvert>();
     constexpr int kKLanes = D / 16, kKStep = 32 / kKLanes, kKLoads = 16 / kKStep;        // K: 16 keys a warp
     constexpr int kVLanes = D / 32, kVStep = 32 / kVLanes, kVLoads = 32 / kVStep;        // V: 32 keys, this CTA's channels
     const int cw = warp - 12;
+    // Both CTAs' converters arrive at rank 0, whose MMA warp waits for all of them.  What rank 1 wrote lies in its own
+    // shared memory, where the products read it, fenced against the async proxy by each lane: a release of CTA scope
+    // orders it before the arrival (of cluster scope it waits for every load in flight: 7.5 ms, not 4.3, for a 720p frame).
+    const uint32_t leader_ctl = mapa_shared(sCtl, 0);
     const int kc = lane % kKLanes, kr = lane / kKLanes, vc = lane % kVLanes, vr = lane / kVLanes;
+    // Where this lane's codes of row r wait in a stage (in 128-byte rows of 64 channels: the upper part's row, where there
+    // is one, else half of the row): within what the row's own lanes will write.
+    auto raw_k = [&](int r) { return D == 128 ? Lo::kKPart + r * 128 + kc * 16 : r * 128 + (r & 1) * 64 + kc * 16; };
+    auto raw_v = [&](int r) { return r * Lo::kVRow + (r & 1) * (Lo::kVRow / 2) + vc * 16; };
     int kv = 0;
     bool ok = true;
     UnitReader in{sCtl};
@@ -617,11 +623,11 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + hk * p.v_h + static_cast<int>(rank) * (D / 2) + vc * 16;
       const uint8_t* kscale = p.scales.k + hk * p.scales.k_head;
       const uint8_t* vscale = p.scales.v + hk * p.scales.v_head;
-      TileCursor<kPaged> c;                             // of the tile whose pages are looked up: two ahead
+      TileCursor<kPaged> c;                             // of the tile whose pages are looked up next
       c.seek(p, geom, t0);
-      uint4 xk[kKLoads], xv[kVLoads];
-      int ek, ev;                                       // scale bytes of this lane's key and value in xk, xv
-      int k_page, k_slot, v_page, v_slot;               // of the next tile's
+      int ahead = t0;
+      int ek[3], ev[3];                                 // scale bytes of this lane's key and value: this tile's and the next two
+      int k_page, k_slot, v_page, v_slot;               // of the tile to be copied next
       // The row of the tile at c that this lane looks up: its page and slot (negative: a key that is not there).
       auto look_up = [&](int row, int& page, int& slot) {
         slot = c.off + row;
@@ -637,9 +643,11 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           slot = -1;
       };
       auto look_up_tile = [&] {
+        if (ahead >= t1) return;
         look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), k_page, k_slot);
         look_up(cw * 32 + lane, v_page, v_slot);
         c.next(p);
+        ++ahead;
       };
       auto place = [&](int page, int slot, long long per_page, long long per_slot) {
         if (slot < 0) return -1ll;
@@ -647,54 +655,78 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         atomicOr(&g_error_word, kErrPage);
         return -1ll;
       };
-      auto load_keys = [&] {
+      // Codes of tile number n to the rows of its stage that they will fill, once that is free: 16 bytes a lane, which
+      // the same lane reads again.
+      auto copy_keys = [&](int n) {
+        if (n >= kS && !(ok = wait(sCtl + kBarKEmpty + 8 * (n % kS), n / kS - 1, kSiteKEmpty))) return;
         const long long at = place(k_page, k_slot, p.k_p, p.k_t);
-        ek = at < 0 ? 127 : kscale[k_page * p.scales.k_page + k_slot / kBlock8 * p.scales.k_block];
+        ek[2] = at < 0 ? 127 : kscale[k_page * p.scales.k_page + k_slot / kBlock8 * p.scales.k_block];
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kKStep + kr);
-          xk[i] = from < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_b128(kbase + from);
+          copy_code16(sK + n % kS * Lo::kStageBytes + raw_k(cw * 16 + i * kKStep + kr), kbase + max(from, 0ll), from >= 0);
         }
       };
-      auto load_values = [&] {
+      auto copy_values = [&](int n) {
+        if (n >= kS && !(ok = wait(sCtl + kBarVEmpty + 8 * (n % kS), n / kS - 1, kSiteVEmpty))) return;
         const long long at = place(v_page, v_slot, p.v_p, p.v_t);
-        ev = at < 0 ? 127 : vscale[v_page * p.scales.v_page + v_slot / kBlock8 * p.scales.v_block];
+        ev[2] = at < 0 ? 127 : vscale[v_page * p.scales.v_page + v_slot / kBlock8 * p.scales.v_block];
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kVStep + vr);
-          xv[i] = from < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_b128(vbase + from);
+          copy_code16(sV + n % kS * Lo::kStageBytes + raw_v(cw * 32 + i * kVStep + vr), vbase + max(from, 0ll), from >= 0);
         }
       };
       look_up_tile();
-      load_keys();
-      load_values();
-      look_up_tile();
-      for (int t = t0; t < t1; ++t) {
+      for (int i = 0; ok && i < 2; ++i) {               // two tiles ahead of the one that is being written
+        ek[0] = ek[1]; ek[1] = ek[2];
+        ev[0] = ev[1]; ev[1] = ev[2];
+        if (t0 + i < t1) copy_keys(kv + i);
+        copies_commit();
+        if (ok && t0 + i < t1) copy_values(kv + i);
+        copies_commit();
+        look_up_tile();
+      }
+      for (int t = t0; ok && t < t1; ++t) {
         const int st = kv % kS;
-        if (kv >= kS && !(ok = wait(sCtl + kBarKEmpty + 8 * st, kv / kS - 1, kSiteKEmpty))) break;
-        const uint32_t kt = sK + st * Lo::kStageBytes + kc / 4 * Lo::kKPart;
-        const uint32_t sk = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ek)));
+        ek[0] = ek[1]; ek[1] = ek[2];
+        ev[0] = ev[1]; ev[1] = ev[2];
+        if (t + 2 < t1) copy_keys(kv + 2);
+        copies_commit();
+        if (!ok) break;
+        copies_wait<4>();                               // four parts are younger than this tile's keys
+        uint4 x[kKLoads > kVLoads ? kKLoads : kVLoads];
+        const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kKLoads; ++i) x[i] = ld_shared_v4(kt + raw_k(cw * 16 + i * kKStep + kr));
+        __syncwarp();                                   // a row's codes are read before it is written
+        const uint32_t sk = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ek[0])));
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i)
-          expand_chunk<T, 128>(kt, cw * 16 + i * kKStep + kr, kc % 4, xk[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
+          expand_chunk<T, 128>(kt + kc / 4 * Lo::kKPart, cw * 16 + i * kKStep + kr, kc % 4, x[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sCtl + kBarKFull + 8 * st);
-        if (t + 1 < t1) load_keys();                    // the next tile's, while this one's values are written
-        if (kv >= kS && !(ok = wait(sCtl + kBarVEmpty + 8 * st, kv / kS - 1, kSiteVEmpty))) break;
-        const uint32_t vt = sV + st * Lo::kStageBytes;
-        const uint32_t sv = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ev)));
+        if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarKFull + 8 * st);
+        // The values of the tile before leave their stage only after this tile's first scores, so not before the keys above
+        if (t + 2 < t1) copy_values(kv + 2);
+        copies_commit();
+        if (!ok) break;
+        look_up_tile();
+        copies_wait<4>();
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) x[i] = ld_shared_v4(vt + raw_v(cw * 32 + i * kVStep + vr));
+        __syncwarp();
+        const uint32_t sv = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ev[0])));
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i)
-          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, xv[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
+          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, x[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sCtl + kBarVFull + 8 * st);
-        if (t + 1 < t1) load_values();
-        if (t + 2 < t1) look_up_tile();
+        if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarVFull + 8 * st);
         ++kv;
       }
     }
+    copies_wait<0>();
     __syncwarp();
   } else if (warp >= 8) {
     regs_decrease<k8 ? kRegsCtl8 : kRegsCtl>();
@@ -841,7 +873,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
         const uint32_t q_full = sCtl + kBarQFull + 8 * (2 * (n & 1));
-        if (!(ok = wait(q_full, qph, kSiteQFull) && wait_landed(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
+        if (!(ok = wait(q_full, qph, kSiteQFull) && wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
         bool fresh = true;
         while (true) {
           const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
@@ -863,7 +895,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             mma_commit_pair_warp(sCtl + kBarSFull + 8);
             mma_commit_pair_warp(sCtl + kBarKEmpty + 8 * st);
           }
-          ok = wait_landed(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
+          ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
           if (!k8 && end && tail < kBN) {
             // rank 1 zeroed rows of its half before it arrived: seen at cluster scope (the phase is complete,
             // so this returns at once)
@@ -877,7 +909,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             st = 0;
             ph ^= 1;
           }
-          if (!end && ok) ok = wait_landed(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
+          if (!end && ok) ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
           if (ok) ok = wait(sCtl + kBarPReady, pr0, kSitePReady);
           pr0 ^= 1;
           if (fresh && n > 0 && ok) ok = wait(sCtl + kBarOEmpty, n + 1, kSiteOEmpty);
@@ -923,15 +955,15 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           ok = wait(sCtl + kBarQFull + 8 * b, n >> 1, kSiteRelay);
           if (ok && lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarQFull + 8 * b, 0));
         }
-        for (; ok && left > 0; --left) {
+        for (; !k8 && ok && left > 0; --left) {          // 8 bits: the converters tell rank 0 themselves
           if (!(ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteRelay))) break;
-          if (lane == 0) tell_landed(sCtl + kBarKFull + 8 * st);
+          if (lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarKFull + 8 * st, 0));
           if (!(ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteRelay))) break;
-          if (!k8 && left == 1 && tail < kBN) {
+          if (left == 1 && tail < kBN) {
             zero_v_rows<D>(sV + st * Lo::kStageBytes, tail, lane);
             if (lane == 0) mbar_arrive_remote_cluster(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
           } else if (lane == 0) {
-            tell_landed(sCtl + kBarVFull + 8 * st);
+            mbar_arrive_remote(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
           }
           if (++st == kS) {
             st = 0;
