@@ -97,6 +97,7 @@ struct Unit {
 
 struct Ctl {
   uint64_t q_full[kQBufs], q_empty[kQBufs];
+  uint64_t q_ready[kQBufs], q_scaled[kQBufs];      // 8 bits: Q tiles are fp16, in both CTAs (rank 0) and in this one
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t s_full[2], p_ready[2];
@@ -108,7 +109,10 @@ struct Ctl {
   Unit unit[kUnitSlots];
   uint32_t tmem_base;
   int abort_flag;
+  int8_t q_exp[kQBufs][kBM];         // 8 bits: what their rows were multiplied by
 };
+
+static_assert(Layout<128>::kOffCtl + sizeof(Ctl) + 1024 <= 232448, "shared memory of a block");
 
 __device__ __forceinline__ int ld_shared_flag(uint32_t addr) {
   int v;
@@ -177,6 +181,7 @@ __device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, 
 }
 
 // Shared-memory offsets within Ctl: every barrier address is one 32-bit base plus a constant.
+constexpr uint32_t kBarQReady = offsetof(Ctl, q_ready), kBarQScaled = offsetof(Ctl, q_scaled);
 constexpr uint32_t kBarQFull = offsetof(Ctl, q_full), kBarQEmpty = offsetof(Ctl, q_empty), kBarKFull = offsetof(Ctl, k_full),
                    kBarKEmpty = offsetof(Ctl, k_empty), kBarVFull = offsetof(Ctl, v_full), kBarVEmpty = offsetof(Ctl, v_empty),
                    kBarSFull = offsetof(Ctl, s_full), kBarPReady = offsetof(Ctl, p_ready), kBarOFull = offsetof(Ctl, o_full),
@@ -465,38 +470,6 @@ __device__ __noinline__ void zero_v_rows(uint32_t v_smem, int from, int lane) {
   __syncwarp();
 }
 
-// Four codes as two pairs of T, times 2^e given by scale_pair<T>(e); exact.
-template <typename T>
-__device__ __forceinline__ uint32_t scale_pair(int e);
-template <>
-__device__ __forceinline__ uint32_t scale_pair<__half>(int e) {
-  return half_two_to(e) * 0x10001u;
-}
-template <>
-__device__ __forceinline__ uint32_t scale_pair<__nv_bfloat16>(int e) {
-  return static_cast<uint32_t>(e + 120 + 127) << 7 | static_cast<uint32_t>(e + 120 + 127) << 23;
-}
-template <typename T>
-__device__ __forceinline__ void expand4(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi);
-template <>
-__device__ __forceinline__ void expand4<__half>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
-  lo = half2_mul(decode2<false>(w), scale);
-  hi = half2_mul(decode2<true>(w), scale);
-}
-// A code's exponent and mantissa, moved to where bf16 has its own, are its value times 2^-120 (subnormals too).
-template <>
-__device__ __forceinline__ void expand4<__nv_bfloat16>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
-  const uint32_t h[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
-  uint32_t r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t m = (h[i] & 0x7f007f00u) >> 4;
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&scale));
-    r[i] = *reinterpret_cast<const uint32_t*>(&v) | (h[i] & 0x80008000u);
-  }
-  lo = r[0];
-  hi = r[1];
-}
 // 16 bytes to shared memory without waiting for them; zeros unless `live`.
 __device__ __forceinline__ void copy_code16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -506,26 +479,61 @@ template <int kLeft>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
-// 16 codes of row r, channels 16 c and up of a 64-channel part of 128-byte swizzled rows (64-byte ones: kRow 64).
-template <typename T, int kRow>
+// 16 codes of row r, channels 16 c and up of a 64-channel part of 128-byte swizzled rows (64-byte ones: kRow 64), as
+// fp16 times `scale` (a pair of equal powers of two).
+template <int kRow>
 __device__ __forceinline__ void expand_chunk(uint32_t part, int r, int c, const uint4& x, uint32_t scale) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) expand4<T>(w[i], scale, y[2 * i], y[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = half2_mul(decode2<false>(w[i]), scale);
+    y[2 * i + 1] = half2_mul(decode2<true>(w[i]), scale);
+  }
   const int turn = kRow == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     st_shared_v4(part + r * kRow + (((2 * c + i) ^ turn) << 4), make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
+}
+// A row of a Q tile (64-channel parts kPart bytes apart, 128-byte swizzled) from bf16 to fp16, in place, times the power of
+// two that brings its largest channel into [2^14, 2^15); what falls below fp16's steps is less than 2^-39 of
+// that.  Returns the power's exponent.
+template <int D, int kPart>
+__device__ __forceinline__ int query_row_to_half(uint32_t tile, int r) {
+  __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = ld_shared_v4(tile + (c >> 3) * kPart + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));      // NaN: the other
+  }
+  const float m = fmaxf(__low2float(top), __high2float(top));
+  const int e = min(max(14 - (static_cast<int>(__float_as_uint(m) >> 23) - 127), -120), 120);
+  const float up = two_to(e);
+#pragma unroll 2
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t at = tile + (c >> 3) * kPart + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    const uint4 x = ld_shared_v4(at);
+    float f[8];
+    unpack8<__nv_bfloat16>(x, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= up;
+    st_shared_v4(at, pack8<__half>(f));
+  }
+  return e;
 }
 
 // One instance per kind of keys and of results, so that none carries the others' code: in this
 // kernel, whose roles' code does not fit the instruction caches, that is time.
 //
 // k8: the cache holds 8-bit codes with scales.  Four more warps copy this CTA's halves of a tile's codes into the stages
-// they belong to, two tiles ahead, 16 bytes a lane (a lane looks up the page and the scales of a key and of a
-// value for the others of its warp); then they spread each row in place to T times its scale, which is exact.  A row's
-// codes and its values are the same lanes', so that a warp needs no other.  The rest is as for 16 bits.
+// they belong to, a tile ahead, 16 bytes a lane (a lane looks up the page and the scales of a key and of a
+// value for the others of its warp); then they spread each row in place to fp16 times its scale, which is exact.  A row's
+// codes and its values are the same lanes', so that a warp needs no other.  The products are of fp16 whatever
+// T is, since codes become fp16 in one instruction and bf16 in five: queries of bf16 are brought into fp16's
+// range by a power of two for each row, exactly, by the same warps at the start of a unit, and weights are taken
+// times 2^7 (of at most 2^8), so that fp16 keeps those down to 2^-21 of a row's largest.
 template <typename T, int D, bool kPaged, bool kSplit, bool k8>
 __global__ void __launch_bounds__(k8 ? kThreads8 : kThreads, 1)
 attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -546,9 +554,11 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // rank 0's full barriers also count one relayed arrival from rank 1, its P-ready and O-empty
     // barriers one arrival from each of rank 1's softmax warps
     const uint32_t full = leader ? 2 : 1, rows = leader ? 128 + 4 : 128;
-    const uint32_t landed = k8 ? 4 * full : full;       // K and V: both CTAs' converter warps instead of producer and relay
+    const uint32_t landed = k8 ? 8 : full;              // K and V: both CTAs' converter warps instead of producer and relay
     for (int i = 0; i < kQBufs; ++i) {
-      mbar_init(smem_addr(&ctl->q_full[i]), full);
+      mbar_init(smem_addr(&ctl->q_full[i]), k8 ? 1 : full);
+      mbar_init(smem_addr(&ctl->q_ready[i]), 8);
+      mbar_init(smem_addr(&ctl->q_scaled[i]), 4);
       mbar_init(smem_addr(&ctl->q_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -606,7 +616,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // is one, else half of the row): within what the row's own lanes will write.
     auto raw_k = [&](int r) { return D == 128 ? Lo::kKPart + r * 128 + kc * 16 : r * 128 + (r & 1) * 64 + kc * 16; };
     auto raw_v = [&](int r) { return r * Lo::kVRow + (r & 1) * (Lo::kVRow / 2) + vc * 16; };
-    int kv = 0;
+    int kv = 0, n = 0;                                  // tiles, units with tiles
     bool ok = true;
     UnitReader in{sCtl};
     while (ok) {
@@ -616,6 +626,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         break;
       }
       const int t0 = VDX_UNIT(in, t0), t1 = VDX_UNIT(in, t1), s = VDX_UNIT(in, s), hk = VDX_UNIT(in, hk), len = VDX_UNIT(in, len);
+      const bool two = VDX_UNIT(in, ntok) > 2 * per_tile;
       in.release();
       if (t0 >= t1) continue;
       const int* table = p.table + static_cast<long long>(s) * p.table_stride;
@@ -625,8 +636,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const uint8_t* vscale = p.scales.v + hk * p.scales.v_head;
       TileCursor<kPaged> c;                             // of the tile whose pages are looked up next
       c.seek(p, geom, t0);
-      int ahead = t0;
-      int ek[3], ev[3];                                 // scale bytes of this lane's key and value: this tile's and the next two
+      int ek, ev, ek_next = 0, ev_next = 0;             // scale bytes of this lane's key and value
       int k_page, k_slot, v_page, v_slot;               // of the tile to be copied next
       // The row of the tile at c that this lane looks up: its page and slot (negative: a key that is not there).
       auto look_up = [&](int row, int& page, int& slot) {
@@ -642,12 +652,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         else
           slot = -1;
       };
-      auto look_up_tile = [&] {
-        if (ahead >= t1) return;
-        look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), k_page, k_slot);
+      auto look_up_key = [&] { look_up(static_cast<int>(rank) * (kBN / 2) + cw * 16 + (lane & 15), k_page, k_slot); };
+      auto look_up_value = [&] {
         look_up(cw * 32 + lane, v_page, v_slot);
         c.next(p);
-        ++ahead;
       };
       auto place = [&](int page, int slot, long long per_page, long long per_slot) {
         if (slot < 0) return -1ll;
@@ -660,7 +668,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       auto copy_keys = [&](int n) {
         if (n >= kS && !(ok = wait(sCtl + kBarKEmpty + 8 * (n % kS), n / kS - 1, kSiteKEmpty))) return;
         const long long at = place(k_page, k_slot, p.k_p, p.k_t);
-        ek[2] = at < 0 ? 127 : kscale[k_page * p.scales.k_page + k_slot / kBlock8 * p.scales.k_block];
+        ek_next = at < 0 ? 127 : kscale[k_page * p.scales.k_page + k_slot / kBlock8 * p.scales.k_block];
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kKStep + kr);
@@ -670,61 +678,82 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       auto copy_values = [&](int n) {
         if (n >= kS && !(ok = wait(sCtl + kBarVEmpty + 8 * (n % kS), n / kS - 1, kSiteVEmpty))) return;
         const long long at = place(v_page, v_slot, p.v_p, p.v_t);
-        ev[2] = at < 0 ? 127 : vscale[v_page * p.scales.v_page + v_slot / kBlock8 * p.scales.v_block];
+        ev_next = at < 0 ? 127 : vscale[v_page * p.scales.v_page + v_slot / kBlock8 * p.scales.v_block];
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) {
           const long long from = __shfl_sync(0xffffffffu, at, i * kVStep + vr);
           copy_code16(sV + n % kS * Lo::kStageBytes + raw_v(cw * 32 + i * kVStep + vr), vbase + max(from, 0ll), from >= 0);
         }
       };
-      look_up_tile();
-      for (int i = 0; ok && i < 2; ++i) {               // two tiles ahead of the one that is being written
-        ek[0] = ek[1]; ek[1] = ek[2];
-        ev[0] = ev[1]; ev[1] = ev[2];
-        if (t0 + i < t1) copy_keys(kv + i);
-        copies_commit();
-        if (ok && t0 + i < t1) copy_values(kv + i);
-        copies_commit();
-        look_up_tile();
+      look_up_key();
+      look_up_value();
+      copy_keys(kv);
+      copies_commit();
+      if (!ok) break;
+      copy_values(kv);
+      copies_commit();
+      if (!ok) break;
+      if (t0 + 1 < t1) {
+        look_up_key();
+        look_up_value();
       }
-      for (int t = t0; ok && t < t1; ++t) {
+      // This unit's Q tiles to fp16, a row to a lane.  (An unused second one's buffer is already the next but one unit's.)
+      for (int i = 0; ok && i < 2; ++i) {
+        const int b = 2 * (n & 1) + i;
+        if (!(ok = wait(sCtl + kBarQFull + 8 * b, n >> 1, kSiteQFull))) break;
+        if (std::is_same<T, __nv_bfloat16>::value && (i == 0 || two)) {
+          ctl->q_exp[b][cw * 32 + lane] = static_cast<int8_t>(query_row_to_half<D, Lo::kQPart>(sQ + b * Lo::kQBytes, cw * 32 + lane));
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(sCtl + kBarQScaled + 8 * b);
+          mbar_arrive_remote_release(leader_ctl + kBarQReady + 8 * b);
+        }
+      }
+      if (!ok) break;
+      ++n;
+      // Codes are copied a tile ahead: any further, and the stage they need would be that of a tile whose products wait
+      // for what is written here.
+      for (int t = t0; t < t1; ++t) {
         const int st = kv % kS;
-        ek[0] = ek[1]; ek[1] = ek[2];
-        ev[0] = ev[1]; ev[1] = ev[2];
-        if (t + 2 < t1) copy_keys(kv + 2);
+        ek = ek_next;
+        ev = ev_next;
+        if (t + 1 < t1) copy_keys(kv + 1);
         copies_commit();
         if (!ok) break;
-        copies_wait<4>();                               // four parts are younger than this tile's keys
+        if (t + 2 < t1) look_up_key();
+        copies_wait<2>();                               // two parts are younger than this tile's keys
         uint4 x[kKLoads > kVLoads ? kKLoads : kVLoads];
         const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i) x[i] = ld_shared_v4(kt + raw_k(cw * 16 + i * kKStep + kr));
         __syncwarp();                                   // a row's codes are read before it is written
-        const uint32_t sk = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ek[0])));
+        const uint32_t sk = half_two_to(scale_exponent(static_cast<uint8_t>(ek))) * 0x10001u;
 #pragma unroll
         for (int i = 0; i < kKLoads; ++i)
-          expand_chunk<T, 128>(kt + kc / 4 * Lo::kKPart, cw * 16 + i * kKStep + kr, kc % 4, x[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
+          expand_chunk<128>(kt + kc / 4 * Lo::kKPart, cw * 16 + i * kKStep + kr, kc % 4, x[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarKFull + 8 * st);
-        // The values of the tile before leave their stage only after this tile's first scores, so not before the keys above
-        if (t + 2 < t1) copy_values(kv + 2);
+        if (t + 1 < t1) copy_values(kv + 1);
         copies_commit();
         if (!ok) break;
-        look_up_tile();
-        copies_wait<4>();
+        if (t + 2 < t1) look_up_value();
+        copies_wait<2>();
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i) x[i] = ld_shared_v4(vt + raw_v(cw * 32 + i * kVStep + vr));
         __syncwarp();
-        const uint32_t sv = scale_pair<T>(scale_exponent(static_cast<uint8_t>(ev[0])));
+        const uint32_t sv = half_two_to(scale_exponent(static_cast<uint8_t>(ev))) * 0x10001u;
 #pragma unroll
         for (int i = 0; i < kVLoads; ++i)
-          expand_chunk<T, Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, x[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
+          expand_chunk<Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, x[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarVFull + 8 * st);
         ++kv;
       }
+      if (!ok) break;
     }
     copies_wait<0>();
     __syncwarp();
@@ -830,7 +859,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       __syncwarp();
     } else if (warp == 9 && leader) {
       // ------------------------------------------------------------------ MMA issuer
-      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t kType = !k8 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t kIdQK = idesc_f16kind_f32acc(2 * kBM, kBN, kType, 0);
       constexpr uint32_t kIdPV = idesc_f16kind_f32acc(2 * kBM, D, kType, 1);
       // This warp shares its scheduler with two softmax warps, and every instruction between two
@@ -872,7 +901,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           continue;
         }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
-        const uint32_t q_full = sCtl + kBarQFull + 8 * (2 * (n & 1));
+        const uint32_t q_full = sCtl + (k8 ? kBarQReady : kBarQFull) + 8 * (2 * (n & 1));
         if (!(ok = wait(q_full, qph, kSiteQFull) && wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
         bool fresh = true;
         while (true) {
@@ -950,12 +979,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         const int tail = VDX_UNIT(in, tail);
         in.release();
         if (left <= 0) continue;
-        for (int i = 0; ok && i < 2; ++i) {
+        for (int i = 0; !k8 && ok && i < 2; ++i) {          // 8 bits: the converters tell rank 0 themselves
           const int b = 2 * (n & 1) + i;
           ok = wait(sCtl + kBarQFull + 8 * b, n >> 1, kSiteRelay);
           if (ok && lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarQFull + 8 * b, 0));
         }
-        for (; !k8 && ok && left > 0; --left) {          // 8 bits: the converters tell rank 0 themselves
+        for (; !k8 && ok && left > 0; --left) {
           if (!(ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteRelay))) break;
           if (lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarKFull + 8 * st, 0));
           if (!(ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteRelay))) break;
@@ -1120,7 +1149,9 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const bool in_tile = my_tok < per_tile;
     const int tok = (2 * qi + static_cast<int>(rank)) * per_tile + my_tok;   // within a block
     const uint32_t remote = mapa_shared(sCtl, 0);
-    const float c = p.scale_log2;
+    using M = std::conditional_t<k8, __half, T>;     // what the products take
+    constexpr float kLift = k8 ? 7.f : 0.f;          // log2 of what weights are multiplied by
+    float c = p.scale_log2;
     int g = 0, n = 0, nq = 0;                    // this Q tile's key tiles and units; units with key tiles
     bool ok = true;
     // one arrival per thread on rank 0, one per warp from rank 1, whose TMEM accesses are complete
@@ -1160,6 +1191,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // tiles below this one are whole for every live row of the warp
       const int whole_to = !kPaged ? u.len / kBN
                            : !p.box_rows ? 0 : __reduce_min_sync(0xffffffffu, live ? limit : 0x7fffffff) / kBN;
+      if (k8 && std::is_same<T, __nv_bfloat16>::value && t < t1) {
+        // the power of two that this row of Q was multiplied by
+        const int b = 2 * (~nq & 1) + qi;
+        if (!(ok = warp_wait_inline(sCtl + kBarQScaled + 8 * b, ((nq - 1) >> 1) & 1, sCtl + kOffAbort, kSiteQFull))) break;
+        c = p.scale_log2 * two_to(-static_cast<int>(ctl->q_exp[b][row]));
+      }
       float m = -INFINITY, l = 0.f;
       bool fresh = true;                       // no tile of this unit has been weighed yet
       bool scaled = false;                     // O holds earlier tiles' sums (not before the second one)
@@ -1200,12 +1237,12 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
               }
             }
             // a row without keys so far: its scores are -inf and weigh nothing
-            const float base = look && !(m > -INFINITY) ? 0.f : m;
+            const float base = look && !(m > -INFINITY) ? 0.f : m - kLift;
             if constexpr (k8)
-              lt = exp_row_halves<T>(tS, c, base, pk);
+              lt = exp_row_halves<M>(tS, c, base, pk);
             else
-              lt = exp_row128<T>(s, c, base, pk);
-            if (look || !__any_sync(0xffffffffu, live && !(lt <= 256.f))) break;
+              lt = exp_row128<M>(s, c, base, pk);
+            if (look || !__any_sync(0xffffffffu, live && !(lt <= (k8 ? 32768.f : 256.f)))) break;
             look = true;
           }
           fresh = false;
@@ -1246,9 +1283,9 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (live) {
         const SeqInfo sq{u.row0, u.n, u.keys, u.shift};
         if (kSplit)
-          p.part_ml[prow] = make_float2(empty ? -INFINITY : m, l);
+          p.part_ml[prow] = make_float2(empty ? -INFINITY : m - kLift, l);
         else if (p.lse)
-          p.lse[lse_index(p, u.s, sq, h, u.tok0 + tok)] = empty ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+          p.lse[lse_index(p, u.s, sq, h, u.tok0 + tok)] = empty ? -INFINITY : (m - kLift + __log2f(l)) * 0.69314718055994530942f;
         if (!scaled && !kSplit) {
           // the block sees no key at all (a split without keys is not read)
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (out_row(p, u.s, sq, u.tok0 + tok) * p.Hq + h) * D);
