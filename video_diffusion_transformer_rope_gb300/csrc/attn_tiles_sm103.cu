@@ -47,6 +47,8 @@
 
 #include "kv8.cuh"
 #include "kv_common.cuh"
+#include "kv_maps.h"
+#include "sm103_wait.cuh"
 
 namespace vdx {
 namespace {
@@ -82,7 +84,7 @@ struct Layout {
 
 enum : int {
   kSiteQFull = 32, kSiteQEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteSFull, kSitePReady,
-  kSiteOFull, kSiteOEmpty, kSiteDrain, kSiteUnitFull, kSiteUnitEmpty, kSiteStaged, kSiteRelay, kSiteClaim
+  kSiteOFull, kSiteOEmpty, kSiteUnitFull = kSiteDrain + 1, kSiteUnitEmpty, kSiteStaged, kSiteRelay, kSiteClaim
 };
 
 // One unit of work, as warp 10 hands it to the other roles.
@@ -114,72 +116,6 @@ struct Ctl {
 
 static_assert(Layout<128>::kOffCtl + sizeof(Ctl) + 1024 <= 232448, "shared memory of a block");
 
-__device__ __forceinline__ int ld_shared_flag(uint32_t addr) {
-  int v;
-  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_shared_flag(uint32_t addr) {
-  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(1) : "memory");
-}
-
-// Latch a wait that gave up, and the first site that did, beside whatever else has been reported.
-__device__ __forceinline__ void report_timeout(int site) {
-  if ((atomicOr(&g_error_word, 1u) & 1u) == 0) atomicOr(&g_error_word, static_cast<unsigned>(site & 0xff) << 8);
-}
-
-// mbar_try_wait that pairs with another CTA's cluster-scope release: what that CTA wrote by plain stores (or
-// read) before it arrived lies before what follows here.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The rest of a warp's wait for a barrier phase whose first look (mbar_try_wait, which itself blocks for
-// a while) failed.  Kept out of line: a dozen inlined copies would spread the roles' loops over so
-// much code that they miss the instruction caches.  The warp gives up as one, when the CTA's abort
-// flag is raised or after kWaitLimitNs, and then raises the flag and records the site.
-template <bool kCluster>
-__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
-  const unsigned long long t0 = global_timer_ns();
-  while (true) {
-    if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, ld_shared_flag(abort_flag) != 0)) return false;
-    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitLimitNs)) {
-      st_shared_flag(abort_flag);
-      if ((threadIdx.x & 31) == 0) report_timeout(site);
-      return false;
-    }
-  }
-}
-// kCluster: for what the other CTA did by plain accesses.  Waits for copies, products and tensor memory need
-// CTA scope only (the copies' bytes, the commits and the tcgen05 fences order those).
-template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
-  if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
-  return wait_more<kCluster>(bar, parity, abort_flag, site);
-}
-// The softmax warps' form: their registers are past what a function call leaves room for.
-__device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, uint32_t abort_flag, int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const unsigned long long t0 = global_timer_ns();
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    if (__any_sync(0xffffffffu, ld_shared_flag(abort_flag) != 0 || global_timer_ns() - t0 > kWaitLimitNs)) {
-      st_shared_flag(abort_flag);
-      if ((threadIdx.x & 31) == 0) report_timeout(site);
-      return false;
-    }
-  }
-  return true;
-}
-
 // Shared-memory offsets within Ctl: every barrier address is one 32-bit base plus a constant.
 constexpr uint32_t kBarQReady = offsetof(Ctl, q_ready), kBarQScaled = offsetof(Ctl, q_scaled);
 constexpr uint32_t kBarQFull = offsetof(Ctl, q_full), kBarQEmpty = offsetof(Ctl, q_empty), kBarKFull = offsetof(Ctl, k_full),
@@ -189,19 +125,6 @@ constexpr uint32_t kBarQFull = offsetof(Ctl, q_full), kBarQEmpty = offsetof(Ctl,
                    kBarUnitFull = offsetof(Ctl, unit_full), kBarUnitEmpty = offsetof(Ctl, unit_empty),
                    kBarClaimFull = offsetof(Ctl, claim_full), kBarClaimReady = offsetof(Ctl, claim_ready),
                    kOffClaim = offsetof(Ctl, claim), kBarDone = offsetof(Ctl, done), kOffUnit = offsetof(Ctl, unit), kOffAbort = offsetof(Ctl, abort_flag);
-
-// Bounded wait on the way out, whatever the abort flag says: copies and MMAs in flight finish
-// before shared or tensor memory is released.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
-  const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      report_timeout(kSiteDrain);
-      return;
-    }
-  }
-}
 
 // How keys are cut into tiles.  Tiles of 128 consecutive keys whatever the page size, where pages are
 // a multiple of box_rows >= 8 keys (whole swizzle atoms): a tile inside one page is one box of 128
@@ -1342,23 +1265,6 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
-}
-
-// A [n3][n2][n1] grid of rows of D channels (element strides s1, s2, s3) as a map with boxes of
-// b1 x b2 rows of `channels` channels (64: 128-byte swizzle, 32: 64-byte).
-template <typename T>
-bool encode_rows(EncodeTiledFn encode, CUtensorMap* map, const void* base, int D, long long n1, long long s1, long long n2,
-                 long long s2, long long n3, long long s3, int channels, int b1, int b2) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
-                              static_cast<cuuint64_t>(n3)};
-  auto bytes = [&](long long n, long long s) { return static_cast<cuuint64_t>(n > 1 ? s : D) * 2; };   // unused where n = 1
-  const cuuint64_t strides[3] = {bytes(n1, s1), bytes(n2, s2), bytes(n3, s3)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(channels), static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return encode(map, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D>

@@ -3,6 +3,7 @@
 // A value is code * 2^e.  With e in [-15, 7] it is exact in bf16 and in fp16: the largest is 448 * 2^7 = 57344, the
 // smallest step 2^-9 * 2^-15 = 2^-24, fp16's own.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
 
@@ -49,6 +50,38 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// Four codes as two pairs of T times a power of two, exactly: `scale` is pair_two_to<T>(e).
+template <typename T>
+__device__ __forceinline__ uint32_t pair_two_to(int e);
+template <>
+__device__ __forceinline__ uint32_t pair_two_to<__half>(int e) {
+  return half_two_to(e) * 0x10001u;
+}
+template <>
+__device__ __forceinline__ uint32_t pair_two_to<__nv_bfloat16>(int e) {
+  return static_cast<uint32_t>(e + 120 + 127) * 0x800080u;       // times the 2^120 that decode4 leaves out
+}
+template <typename T>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi);
+template <>
+__device__ __forceinline__ void decode4<__half>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  lo = half2_mul(decode2<false>(w), scale);
+  hi = half2_mul(decode2<true>(w), scale);
+}
+// A code's exponent and mantissa, moved to where bf16 has its own, are its value times 2^-120 (subnormals too).
+template <>
+__device__ __forceinline__ void decode4<__nv_bfloat16>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  const uint32_t h[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t m = (h[i] & 0x7f007f00u) >> 4;
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&scale));
+    r[i] = *reinterpret_cast<const uint32_t*>(&v) | (h[i] & 0x80008000u);
+  }
+  lo = r[0];
+  hi = r[1];
 }
 __device__ __forceinline__ void decode8(const uint2& x, float (&f)[8]) {
   const uint32_t h[4] = {decode2<false>(x.x), decode2<true>(x.x), decode2<false>(x.y), decode2<true>(x.y)};

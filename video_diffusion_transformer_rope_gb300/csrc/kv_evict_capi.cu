@@ -82,10 +82,19 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* c, const vdx_kv8_scales* s
   if (a->width > 0)
     for (const Span& r : reads)
       if (overlap(wt, r.p, r.bytes)) return fail(VDX_ERR_ARG, "the weights overlap cu, kv_len, pos_offset, page_table or lse");
-  const cudaError_t e = vdx::launch_weigh(wp, c->d, c->dtype, multiprocessors(), static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  const char* what = nullptr;
+  if (static_cast<long long>(p.max_q) * p.g <= 32) {
+    e = vdx::launch_weigh_rows(wp, c->d, c->dtype, multiprocessors(), st);
+  } else {
+    vdx::EncodeTiledFn encode = nullptr;
+    if (!vdx::encode_tiled_fn(&encode)) return VDX_ERR_CUDA;
+    e = vdx::launch_weigh_tiles(wp, c->d, c->dtype, encode, multiprocessors(), st, &what);
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
-    return fail(VDX_ERR_CUDA, "weights kernel launch: %s", cudaGetErrorString(e));
+    return fail(VDX_ERR_CUDA, "weights kernel launch: %s%s%s", what ? what : "", what ? ": " : "", cudaGetErrorString(e));
   }
   return VDX_OK;
 }

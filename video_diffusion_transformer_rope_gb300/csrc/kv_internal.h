@@ -118,7 +118,9 @@ struct WeighParams {
   float decay;
   int nsplit, split_keys;     // keys of a block (few-row kernel)
 };
-cudaError_t launch_weigh(WeighParams p, int d, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_weigh_rows(WeighParams p, int d, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_weigh_tiles(const WeighParams& p, int d, int dtype, EncodeTiledFn encode, int sms, cudaStream_t stream,
+                               const char** what);
 
 // Eviction: one problem, validated.
 struct EvictParams {
@@ -148,7 +150,8 @@ cudaError_t launch_evict(const EvictParams& p, int d, bool eight, int sms, cudaS
 cudaError_t read_and_clear_error_word_append(unsigned int* word);
 cudaError_t read_and_clear_error_word_rows(unsigned int* word);
 cudaError_t read_and_clear_error_word_tiles(unsigned int* word);
-cudaError_t read_and_clear_error_word_weigh(unsigned int* word);
+cudaError_t read_and_clear_error_word_weigh_rows(unsigned int* word);
+cudaError_t read_and_clear_error_word_weigh_tiles(unsigned int* word);
 cudaError_t read_and_clear_error_word_evict(unsigned int* word);
 
 // cuTensorMapEncodeTiled, looked up once (vdx_capi.cu).  Sets vdx_last_error on failure.

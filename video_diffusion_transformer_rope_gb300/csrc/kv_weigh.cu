@@ -4,11 +4,10 @@
 //
 // for a kv head's rows r, the (token, query head of its group) pairs; lse comes from the attention call.
 //
-// Few rows: bound by DRAM, which each key crosses once (its value is not needed), so K streams as in attn_rows.cu:
+// This file, few rows: bound by DRAM, which each key crosses once (its value is not needed), so K streams as in attn_rows.cu:
 // a warp takes 16 keys at a time through a ring of its own, S^T = K Q^T by m16n8k16 products with the keys on the
 // 16-wide side, and a key's sum over its rows ends as a shuffle over four lanes.  Nothing is shared between warps and
-// each w is written by one lane: the same call gives the same bits.  More rows than fit the fragments are
-// taken 32 at a time.
+// each w is written by one lane: the same call gives the same bits.  More than 32 rows: weigh_tiles_sm103.cu.
 #include <cstdint>
 
 #include "kv_mma.cuh"
@@ -24,7 +23,6 @@ template <typename T, int D, int kNT, bool k8>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 weigh_rows(const __grid_constant__ WeighParams wp) {
   using M = std::conditional_t<k8, __half, T>;
-  constexpr int kRows = 8 * kNT;
   constexpr int kElem = k8 ? 1 : 2;
   constexpr int kChunks = D * kElem / 16;
   constexpr int kRowBytes = D * kElem;
@@ -40,7 +38,7 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
   const int unit = blockIdx.x / wp.nsplit;
   const int hk = unit % p.Hkv, s = unit / p.Hkv;
   const SeqInfo sq = sequence_info(p, s, threadIdx.x == 0 && z == 0);
-  const int rows = min(sq.n, p.max_q) * p.g;
+  const int rows = min(sq.n, p.max_q) * p.g;            // at most 8 * kNT
   if (rows == 0) return;                                // its entries stay as they are
   const long long lo64 = static_cast<long long>(z) * wp.split_keys;
   const int lo = static_cast<int>(min(lo64, static_cast<long long>(sq.len)));
@@ -60,39 +58,36 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
 
   uint32_t qf[kNT][D / 16][2];
   float row_scale[kNT][2], lse2[kNT][2];
-  int limit[kNT][2], full_to = 0;        // below full_to every row sees everything
-  auto load_rows = [&](int first) {
-    const int live = min(rows - first, kRows);
+  int limit[kNT][2];
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const int r = nt * 8 + gq;
-      const T* src = nullptr;
-      if (r < live) {
-        const int R = first + r, tok = R / p.g, h = hk * p.g + (R - tok * p.g);
-        src = static_cast<const T*>(p.q) + (static_cast<long long>(sq.row0) + tok) * p.q_t + h * p.q_h;
-      }
+  for (int nt = 0; nt < kNT; ++nt) {
+    const int r = nt * 8 + gq;
+    const T* src = nullptr;
+    if (r < rows) {
+      const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
+      src = static_cast<const T*>(p.q) + (static_cast<long long>(sq.row0) + tok) * p.q_t + h * p.q_h;
+    }
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[nt][ks][0] = src ? load_b32(src + ks * 16 + (k8 ? 4 : 2) * c4) : 0u;
-        qf[nt][ks][1] = src ? load_b32(src + ks * 16 + (k8 ? 4 * c4 + 2 : 8 + 2 * c4)) : 0u;
-      }
-      row_scale[nt][0] = row_scale[nt][1] = p.scale_log2;
-      if constexpr (k8) query_to_half<T, D>(qf[nt], nt, c4, row_scale, p.scale_log2);
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qf[nt][ks][0] = src ? load_b32(src + ks * 16 + (k8 ? 4 : 2) * c4) : 0u;
+      qf[nt][ks][1] = src ? load_b32(src + ks * 16 + (k8 ? 4 * c4 + 2 : 8 + 2 * c4)) : 0u;
+    }
+    row_scale[nt][0] = row_scale[nt][1] = p.scale_log2;
+    if constexpr (k8) query_to_half<T, D>(qf[nt], nt, c4, row_scale, p.scale_log2);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = nt * 8 + 2 * c4 + e;
-        limit[nt][e] = hi;
-        lse2[nt][e] = INFINITY;                         // 2^(s - inf) = 0: a row that is none, or saw no key
-        if (rr < live) {
-          const int R = first + rr, tok = R / p.g, h = hk * p.g + (R - tok * p.g);
-          limit[nt][e] = min(visible_limit(p, sq, tok), hi);
-          const float l = wp.lse[lse_index(p, s, sq, h, tok)];
-          if (l != -INFINITY) lse2[nt][e] = l * 1.4426950408889634f;
-        }
+    for (int e = 0; e < 2; ++e) {
+      const int rr = nt * 8 + 2 * c4 + e;
+      limit[nt][e] = hi;
+      lse2[nt][e] = INFINITY;                         // 2^(s - inf) = 0: a row that is none, or saw no key
+      if (rr < rows) {
+        const int tok = rr / p.g, h = hk * p.g + (rr - tok * p.g);
+        limit[nt][e] = min(visible_limit(p, sq, tok), hi);
+        const float l = wp.lse[lse_index(p, s, sq, h, tok)];
+        if (l != -INFINITY) lse2[nt][e] = l * 1.4426950408889634f;
       }
     }
-    full_to = min(hi, visible_limit(p, sq, first / p.g));
-  };
+  }
+  const int full_to = min(hi, visible_limit(p, sq, 0));     // below it every row sees everything
 
   int pg = nblocks > 0 ? k_first / p.P : 0;
   int off = nblocks > 0 ? k_first - pg * p.P : 0;
@@ -106,7 +101,6 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
     }
   };
   fetch_pages(k_first);
-  if (rows <= kRows) load_rows(0);
   // scales and weights so far of the blocks being copied, oldest first: lane l has those of key l
   int exps[kStages - 1];
   float old[kStages - 1];
@@ -172,43 +166,40 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
     const uint32_t kt = ring + (i % kStages) * kTileBytes;
     const int key0 = k_first + i * step;
     float sum[2] = {0.f, 0.f};
-    for (int first = 0; first < rows; first += kRows) {
-      if (rows > kRows) load_rows(first);
-      float st[kNT][4];
+    float st[kNT][4];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st[nt][e] = 0.f;
-      if constexpr (k8) {
+      for (int e = 0; e < 4; ++e) st[nt][e] = 0.f;
+    if constexpr (k8) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          uint32_t c[4];
-          ldsm4(c, kt + lrow * kRowBytes + (swizzle(ks + lch, lrow) << 4));
+      for (int ks = 0; ks < D / 16; ks += 2) {
+        uint32_t c[4];
+        ldsm4(c, kt + lrow * kRowBytes + (swizzle(ks + lch, lrow) << 4));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t a[4] = {decode2<false>(c[2 * x]), decode2<false>(c[2 * x + 1]), decode2<true>(c[2 * x]), decode2<true>(c[2 * x + 1])};
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t a[4] = {decode2<false>(c[2 * x]), decode2<false>(c[2 * x + 1]), decode2<true>(c[2 * x]), decode2<true>(c[2 * x + 1])};
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks + x][0], qf[nt][ks + x][1]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t a[4];
-          ldsm4(a, kt + lrow * kRowBytes + (swizzle(2 * ks + lch, lrow) << 4));
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks + x][0], qf[nt][ks + x][1]);
         }
       }
+    } else {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t a[4];
+        ldsm4(a, kt + lrow * kRowBytes + (swizzle(2 * ks + lch, lrow) << 4));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = fmaf(st[nt][e] * (k8 ? key_scale[e >> 1] : 1.f), row_scale[nt][e & 1], -lse2[nt][e & 1]);
-          if (key0 + kKeys > full_to && key0 + gq + (e >> 1) * 8 >= limit[nt][e & 1]) x = -INFINITY;
-          sum[e >> 1] += ex2_approx(x);
-        }
+        for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+      }
     }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = fmaf(st[nt][e] * (k8 ? key_scale[e >> 1] : 1.f), row_scale[nt][e & 1], -lse2[nt][e & 1]);
+        if (key0 + kKeys > full_to && key0 + gq + (e >> 1) * 8 >= limit[nt][e & 1]) x = -INFINITY;
+        sum[e >> 1] += ex2_approx(x);
+      }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
@@ -252,7 +243,7 @@ cudaError_t launch(const WeighParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_weigh(WeighParams p, int d, int dtype, int sms, cudaStream_t stream) {
+cudaError_t launch_weigh_rows(WeighParams p, int d, int dtype, int sms, cudaStream_t stream) {
   note_launch();
   // blocks of 64 to 1024 keys, several to a multiprocessor where there are enough
   const long long units = static_cast<long long>(p.kv.S) * p.kv.Hkv;
@@ -267,6 +258,6 @@ cudaError_t launch_weigh(WeighParams p, int d, int dtype, int sms, cudaStream_t 
   return d == 128 ? launch<__half, 128>(p, stream) : launch<__half, 64>(p, stream);
 }
 
-cudaError_t read_and_clear_error_word_weigh(unsigned int* word) { return read_and_clear_word(word); }
+cudaError_t read_and_clear_error_word_weigh_rows(unsigned int* word) { return read_and_clear_word(word); }
 
 }  // namespace vdx

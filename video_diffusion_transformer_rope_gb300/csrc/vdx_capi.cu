@@ -439,7 +439,8 @@ vdx_status vdx_sync_check(void* stream) {
   unsigned int word = 0;
   e = vdx::read_and_clear_error_word_sm103(&word);
   for (auto read : {vdx::read_and_clear_error_word_append, vdx::read_and_clear_error_word_rows,
-                    vdx::read_and_clear_error_word_tiles, vdx::read_and_clear_error_word_weigh, vdx::read_and_clear_error_word_evict}) {
+                    vdx::read_and_clear_error_word_tiles, vdx::read_and_clear_error_word_weigh_rows,
+                    vdx::read_and_clear_error_word_weigh_tiles, vdx::read_and_clear_error_word_evict}) {
     unsigned int more = 0;
     if (e == cudaSuccess) e = read(&more);
     word |= more;

@@ -1,0 +1,412 @@
+// The weight that each cached key gathers (kv_weigh.cu has the formula) where a kv head has many rows, on the
+// 5th-generation tensor cores.
+//
+//     S^T = K Q^T  (128 keys x 128 rows),   w[key] += sum over the tile's rows of 2^(S^T * scale*log2(e) - lse*log2(e))
+//
+// With the keys as the M side a key is a thread's TMEM lane and its sum stays in that thread's registers: no sum
+// crosses threads, none goes through memory, and the same call gives the same bits.  The keys are the A operand in
+// tensor memory (64 columns for 128 channels), which the threads that own them write there straight from the cache
+// (a thread a key: any page size, and 8-bit codes become T on the way, exactly); only Q streams through shared
+// memory, by TMA, used for two key tiles.  Read as an operand of both and written once that is three quarters of shared
+// memory's rate; with the keys there too it would be past it.
+//
+// Bound: the tensor cores and the exponentials together (a 128 x 128 tile at d = 128 is 512 cycles of products).
+//
+// A unit is (sequence, kv head, 256 keys); a block per multiprocessor takes every gridDim-th of them, and the next
+// unit's keys are under way while the current one's rows are weighed.
+//   warps 0-3, 4-7   key tile 0 / 1: keys to tensor memory, exponentials and sums (thread = key = TMEM lane)
+//   warp 8           TMA producer of the Q ring          warp 9   issues the products
+//   warp 10          -lse*log2(e) of a Q tile's rows, to shared memory
+// TMEM (512 columns): the keys of both tiles at 0 and 64, three S tiles at 128, 256 and 384, used in turn.
+#include <cstdint>
+
+#include "kv8.cuh"
+#include "kv_common.cuh"
+#include "kv_maps.h"
+#include "sm103_wait.cuh"
+
+namespace vdx {
+namespace {
+
+constexpr int kKeys = 128;             // of a tile; a unit has two
+constexpr int kRowTile = 128;
+constexpr int kThreads = 384;
+constexpr int kSBufs = 3;
+constexpr int kLseSlots = 4;
+constexpr int kMaxStages = 12;
+
+template <int D>
+struct Layout {
+  static constexpr int kStageBytes = kRowTile * D * 2;      // 64-channel parts of 128-byte swizzled rows
+  static constexpr int kPart = kRowTile * 128;
+  static constexpr int kParts = D / 64;
+  static constexpr int kStages = D == 128 ? 6 : 12;
+  static constexpr int kOffCtl = kStages * kStageBytes;
+};
+
+enum : int { kSiteQFull = 64, kSiteQEmpty, kSiteKeys, kSiteSFull, kSiteSEmpty, kSiteLseFull, kSiteLseEmpty };
+
+struct Ctl {
+  uint64_t q_full[kMaxStages], q_empty[kMaxStages];
+  uint64_t keys[2];
+  uint64_t s_full[kSBufs], s_empty[kSBufs];
+  uint64_t l_full[kLseSlots], l_empty[kLseSlots];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+  alignas(16) float nl[kLseSlots][kRowTile];
+};
+
+struct Unit {
+  int it;                  // its number; `units`: none is left
+  int s, hk, key0, keys;   // keys of its two tiles
+  SeqInfo sq;
+  int rows, t0, t1;        // rows of the kv head; Q tiles that some key of the unit is seen by
+  __device__ __forceinline__ bool has(int tile) const { return keys > tile * kKeys; }
+};
+
+// The first row token of the sequence that sees key c (visible_limit the other way round).
+__device__ __forceinline__ int first_token(const KvParams& p, const SeqInfo& q, int c) {
+  if (p.causal_block <= 0) return 0;
+  const int pos = static_cast<int>(c - (static_cast<unsigned>(c) + q.shift) % static_cast<unsigned>(p.causal_block));
+  return max(max(pos, 0) - (q.len - q.n), 0);
+}
+
+// The next unit from number `it` on that has work.
+__device__ __forceinline__ Unit next_unit(const KvParams& p, int it, int units, int blocks, int row_tile, bool report) {
+  Unit u;
+  for (; it < units; it += gridDim.x) {
+    const int kb = it % blocks, r = it / blocks;
+    u.hk = r % p.Hkv;
+    u.s = r / p.Hkv;
+    u.sq = sequence_info(p, u.s, report && kb == 0 && u.hk == 0);
+    u.rows = min(u.sq.n, p.max_q) * p.g;
+    u.key0 = kb * 2 * kKeys;
+    u.keys = min(2 * kKeys, u.sq.len - u.key0);
+    if (u.rows > 0 && u.keys > 0) {
+      u.t1 = (u.rows + row_tile - 1) / row_tile;
+      u.t0 = static_cast<int>(min(static_cast<long long>(first_token(p, u.sq, u.key0)) * p.g / row_tile, static_cast<long long>(u.t1)));
+      break;
+    }
+  }
+  u.it = min(it, units);
+  return u;
+}
+
+// sum over 64 columns of 2^(s * c + nl), those below lo or from hi on left out where kMask.
+template <bool kMask>
+__device__ __forceinline__ void weigh64(uint32_t s_tmem, uint32_t nl, float c, int lo, int hi, uint64_t (&acc)[4]) {
+  uint32_t s[64];
+  tmem_ld64(s_tmem, s);
+  const uint64_t c2 = f32x2(c, c);
+#pragma unroll
+  for (int e = 0; e < 64; e += 4) {
+    const uint4 l = ld_shared_v4(nl + e * 4);
+    const uint64_t a = ffma2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f32x2(__uint_as_float(l.x), __uint_as_float(l.y)));
+    const uint64_t b = ffma2(f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, f32x2(__uint_as_float(l.z), __uint_as_float(l.w)));
+    float x[4];
+    f32x2_split(a, x[0], x[1]);
+    f32x2_split(b, x[2], x[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kMask && (e + i < lo || e + i >= hi)) x[i] = -INFINITY;
+      x[i] = ex2_approx(x[i]);
+    }
+    acc[(e >> 1) & 3] = fadd2(acc[(e >> 1) & 3], f32x2(x[0], x[1]));
+    acc[((e >> 1) + 1) & 3] = fadd2(acc[((e >> 1) + 1) & 3], f32x2(x[2], x[3]));
+  }
+}
+
+template <typename T, int D, bool k8>
+__global__ void __launch_bounds__(kThreads, 1)
+weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ WeighParams wp, const int units, const int blocks) {
+  using Lo = Layout<D>;
+  constexpr int kS = Lo::kStages;
+  const KvParams& p = wp.kv;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + Lo::kOffCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sQ = smem_addr(smem);
+  const int row_tile = kRowTile / p.g * p.g;           // whole tokens
+
+  if (tid == 0) {
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(smem_addr(&ctl->q_full[i]), 1);
+      mbar_init(smem_addr(&ctl->q_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->keys[i]), kKeys);
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(smem_addr(&ctl->s_full[i]), 1);
+      mbar_init(smem_addr(&ctl->s_empty[i]), 4);
+    }
+    for (int i = 0; i < kLseSlots; ++i) {
+      mbar_init(smem_addr(&ctl->l_full[i]), 1);
+      mbar_init(smem_addr(&ctl->l_empty[i]), 8);
+    }
+    mbar_init(smem_addr(&ctl->done), 1);
+    ctl->abort_flag = 0;
+    fence_barrier_init();
+  }
+  // rows of a stage behind the last whole token are never copied: they weigh nothing, so they must not be NaN
+  for (int i = tid; i < kS * Lo::kParts * (kRowTile - row_tile) * 8; i += kThreads) {
+    const int ch = i & 7, r = i >> 3, part = r / (kRowTile - row_tile);
+    st_shared_v4(sQ + part * Lo::kPart + (row_tile + r - part * (kRowTile - row_tile)) * 128 + ch * 16, make_uint4(0u, 0u, 0u, 0u));
+  }
+  fence_proxy_async_smem();
+  if (warp == 9) {
+    tmem_alloc(smem_addr(&ctl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  wait_for_earlier_work();
+  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t flag = smem_addr(&ctl->abort_flag);
+  auto wait = [&](const uint64_t* bar, int phase, int site) { return warp_wait(smem_addr(bar), phase & 1, flag, site); };
+  auto first = [&](int it, bool report = false) { return next_unit(p, it, units, blocks, row_tile, report); };
+  const int stride = gridDim.x;
+
+  if (warp == 8) {
+    // -------------------------------------------------------------------- Q tiles
+    if (lane == 0) tma_prefetch_desc(&tm_q);
+    int n = 0;
+    bool ok = true;
+    for (Unit u = first(blockIdx.x, lane == 0); ok && u.it < units; u = first(u.it + stride, lane == 0)) {
+      for (int t = u.t0; t < u.t1; ++t, ++n) {
+        const int st = n % kS;
+        if (n >= kS && !(ok = wait(&ctl->q_empty[st], n / kS - 1, kSiteQEmpty))) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&ctl->q_full[st]);
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(row_tile) * D * 2);
+#pragma unroll
+          for (int h = 0; h < Lo::kParts; ++h)
+            tma_load_4d(sQ + st * Lo::kStageBytes + h * Lo::kPart, &tm_q, bar, h * 64, u.hk * p.g, u.sq.row0 + t * (row_tile / p.g), 0);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0)
+      for (int st = 0; st < kS; ++st)
+        if (n > st) drain_wait(smem_addr(&ctl->q_full[st]), ((n - 1 - st) / kS) & 1);
+    __syncwarp();
+  } else if (warp == 9) {
+    // -------------------------------------------------------------------- products
+    constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    int n = 0, seq = 0, filled[2] = {0, 0};
+    bool ok = true;
+    for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
+      if (u.t0 == u.t1) continue;
+      const int tiles = u.has(1) ? 2 : 1;
+      for (int x = 0; ok && x < tiles; ++x) ok = wait(&ctl->keys[x], filled[x]++, kSiteKeys);
+      for (int t = u.t0; ok && t < u.t1; ++t, ++n) {
+        const int st = n % kS;
+        if (!(ok = wait(&ctl->q_full[st], n / kS, kSiteQFull))) break;
+        const int cols = min(row_tile, u.rows - t * row_tile);
+        // whole tiles take the zero rows too; the last tile only what it has, in sixteens
+        const uint32_t id = idesc_f16kind_f32acc(kKeys, cols == row_tile ? kRowTile : (cols + 15) & ~15, kType, 0);
+        const uint64_t b = smem_desc_sw128(sQ + st * Lo::kStageBytes, 16, 1024);
+        for (int x = 0; x < tiles; ++x, ++seq) {
+          const int buf = seq % kSBufs;
+          if (seq >= kSBufs && !(ok = wait(&ctl->s_empty[buf], seq / kSBufs - 1, kSiteSEmpty))) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ts_warp(tmem + 128 + buf * 128, tmem + x * 64 + kk * 8, b + (kk >> 2) * (Lo::kPart >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
+          mma_commit_warp(smem_addr(&ctl->s_full[buf]));
+        }
+        if (!ok) break;
+        mma_commit_warp(smem_addr(&ctl->q_empty[st]));
+      }
+    }
+    mma_commit_warp(smem_addr(&ctl->done));
+    drain_wait(smem_addr(&ctl->done), 0);
+  } else if (warp == 10) {
+    // -------------------------------------------------------------------- lse of the rows
+    int n = 0;
+    bool ok = true;
+    for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
+      for (int t = u.t0; t < u.t1; ++t, ++n) {
+        const int slot = n % kLseSlots;
+        float v[kRowTile / 32];
+#pragma unroll
+        for (int i = 0; i < kRowTile / 32; ++i) {
+          const int x = i * 32 + lane, R = t * row_tile + x;
+          v[i] = -INFINITY;                              // no row, or one that saw no key: 2^-inf = 0
+          if (x < row_tile && R < u.rows) {
+            const int tok = R / p.g, h = u.hk * p.g + (R - tok * p.g);
+            const float l = wp.lse[lse_index(p, u.s, u.sq, h, tok)];
+            if (l != -INFINITY) v[i] = l * -1.4426950408889634f;
+          }
+        }
+        if (n >= kLseSlots && !(ok = wait(&ctl->l_empty[slot], n / kLseSlots - 1, kSiteLseEmpty))) break;
+#pragma unroll
+        for (int i = 0; i < kRowTile / 32; ++i) ctl->nl[slot][i * 32 + lane] = v[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_full[slot]));
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // -------------------------------------------------------------------- keys, exponentials, sums
+    constexpr int kLoads = D * (k8 ? 1 : 2) / 16;
+    const int x = warp >> 2;                             // key tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint4 raw[kLoads];
+    int exponent = 0;
+    auto load_key = [&](const Unit& u) {
+      const int c = u.key0 + x * kKeys + row;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c >= u.sq.len) return;
+      const int pg = c / p.P, slot = c - pg * p.P;
+      const int page = load_i32(p.table + u.s * p.table_stride + pg);
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+        atomicOr(&g_error_word, kErrPage);               // its key reads as zeros
+        return;
+      }
+      const uint8_t* at = static_cast<const uint8_t*>(p.k) + (page * p.k_p + slot * p.k_t + u.hk * p.k_h) * (k8 ? 1 : 2);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = load_b128(at + i * 16);
+      if (k8) exponent = scale_exponent(p.scales.k[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block + u.hk * p.scales.k_head]);
+    };
+    // 32 columns are 64 channels
+    auto write_key = [&] {
+      const uint32_t scale = k8 ? pair_two_to<T>(exponent) : 0u;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t y[32];
+#pragma unroll
+        for (int i = 0; i < kLoads / (D / 64); ++i) {
+          const uint4 r = raw[h * (kLoads / (D / 64)) + i];
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (k8)
+              decode4<T>(w[e], scale, y[i * 8 + 2 * e], y[i * 8 + 2 * e + 1]);
+            else
+              y[i * 4 + e] = w[e];
+          }
+        }
+        tmem_st32(tmem + lanes + x * 64 + h * 32, y);
+      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(smem_addr(&ctl->keys[x]));
+    };
+    int n = 0, seq = 0;
+    bool ok = true;
+    Unit u = first(blockIdx.x);
+    bool ahead = u.it < units && u.has(x) && u.t0 < u.t1;        // raw holds the next key to be written
+    if (ahead) {
+      load_key(u);
+      write_key();
+    }
+    while (ok && u.it < units) {
+      const Unit next = first(u.it + stride);
+      ahead = next.it < units && next.has(x) && next.t0 < next.t1;
+      if (ahead) load_key(next);
+      const int c = u.key0 + x * kKeys + row;
+      const bool live = c < u.sq.len;
+      float* w = wp.w + u.s * wp.w_seq + u.hk * wp.w_head + c;
+      const float old = live && c < u.sq.len - u.sq.n ? *w * wp.decay : 0.f;
+      // rows below this one do not see the key; the whole warp's keys are seen from `clear` on
+      const long long r0 = live ? static_cast<long long>(first_token(p, u.sq, c)) * p.g : 0;
+      const int from = static_cast<int>(min(r0, static_cast<long long>(u.rows)));
+      const int clear = __reduce_max_sync(0xffffffffu, from);
+      const int tiles = u.has(1) ? 2 : 1;
+      float total = 0.f;
+      for (int t = u.t0; t < u.t1; ++t, ++n, seq += tiles) {
+        const int slot = n % kLseSlots;
+        if (u.has(x)) {
+          const int buf = (seq + x) % kSBufs;
+          if (!(ok = warp_wait_inline(smem_addr(&ctl->s_full[buf]), ((seq + x) / kSBufs) & 1, flag, kSiteSFull))) break;
+          tc_fence_after_sync();
+          // the last product of this unit with this tile's keys is done: the next unit's take their place
+          if (t + 1 == u.t1 && ahead) write_key();
+          if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
+          const int cols = min(row_tile, u.rows - t * row_tile), lo = from - t * row_tile;
+          const uint32_t ts = tmem + lanes + 128 + buf * 128, nl = smem_addr(&ctl->nl[slot][0]);
+          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          if (cols == row_tile && clear <= t * row_tile) {
+            weigh64<false>(ts, nl, p.scale_log2, 0, 64, acc);
+            weigh64<false>(ts + 64, nl + 256, p.scale_log2, 0, 64, acc);
+          } else {
+#pragma unroll 1
+            for (int ch = 0; ch < cols; ch += 64) weigh64<true>(ts + ch, nl + ch * 4, p.scale_log2, lo - ch, cols - ch, acc);
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&ctl->s_empty[buf]));
+            mbar_arrive(smem_addr(&ctl->l_empty[slot]));
+          }
+          float a, b;
+          f32x2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
+          total += a + b;
+        } else {
+          if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
+          if (lane == 0) mbar_arrive(smem_addr(&ctl->l_empty[slot]));
+        }
+      }
+      if (!ok) break;
+      if (live) *w = old + total;
+      if (ahead && !(u.has(x) && u.t0 < u.t1)) write_key();
+      u = next;
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D, bool k8>
+cudaError_t launch_kind(const WeighParams& p, EncodeTiledFn encode, int sms, cudaStream_t stream, const char** what) {
+  CUtensorMap mq;
+  if (!encode_rows<T>(encode, &mq, p.kv.q, D, p.kv.Hq, p.kv.q_h, p.kv.N, p.kv.q_t, 1, 0, 64, p.kv.g, kRowTile / p.kv.g)) {
+    *what = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  constexpr int kSmem = Layout<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
+  static_assert(kSmem <= 232448, "shared memory of a block");
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared(weigh_tiles<T, D, k8>, kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const int blocks = (p.kv.max_kv + 2 * kKeys - 1) / (2 * kKeys);
+  const long long units = static_cast<long long>(p.kv.S) * p.kv.Hkv * blocks;
+  if (units > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+  if (units == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units < sms ? units : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSmem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = launch_early();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weigh_tiles<T, D, k8>, mq, p, static_cast<int>(units), blocks);
+}
+template <typename T, int D>
+cudaError_t launch(const WeighParams& p, EncodeTiledFn encode, int sms, cudaStream_t stream, const char** what) {
+  return p.kv.eight ? launch_kind<T, D, true>(p, encode, sms, stream, what) : launch_kind<T, D, false>(p, encode, sms, stream, what);
+}
+
+}  // namespace
+
+cudaError_t launch_weigh_tiles(const WeighParams& p, int d, int dtype, EncodeTiledFn encode, int sms, cudaStream_t stream, const char** what) {
+  *what = nullptr;
+  note_launch();
+  if (dtype == 0)
+    return d == 128 ? launch<__nv_bfloat16, 128>(p, encode, sms, stream, what) : launch<__nv_bfloat16, 64>(p, encode, sms, stream, what);
+  return d == 128 ? launch<__half, 128>(p, encode, sms, stream, what) : launch<__half, 64>(p, encode, sms, stream, what);
+}
+
+cudaError_t read_and_clear_error_word_weigh_tiles(unsigned int* word) { return read_and_clear_word(word); }
+
+}  // namespace vdx
