@@ -4,20 +4,21 @@
 //     S^T = K Q^T  (128 keys x 128 rows),   w[key] += sum over the tile's rows of 2^(S^T * scale*log2(e) - lse*log2(e))
 //
 // With the keys as the M side a key is a thread's TMEM lane and its sum stays in that thread's registers: no sum
-// crosses threads, none goes through memory, and the same call gives the same bits.  The keys are the A operand in
-// tensor memory (64 columns for 128 channels), which the threads that own them write there straight from the cache
-// (a thread a key: any page size, and 8-bit codes become T on the way, exactly); only Q streams through shared
-// memory, by TMA, used for two key tiles.  Read as an operand of both and written once that is three quarters of shared
-// memory's rate; with the keys there too it would be past it.
+// goes through memory, and the same call gives the same bits.  The keys are the A operand in tensor memory (64
+// columns for 128 channels): only Q streams through shared memory, by TMA, each tile used for two key tiles.  Read as
+// an operand of both and written once that is three quarters of shared memory's rate; with the keys there too it
+// would be past it.  A warp copies the next unit's keys to shared memory meanwhile (any page size), from where the
+// threads that own them put them into tensor memory, 8-bit codes as T, exactly.
 //
-// Bound: the tensor cores and the exponentials together (a 128 x 128 tile at d = 128 is 512 cycles of products).
+// Bound: the tensor cores and the exponentials together (a 128 x 128 tile at d = 128 is 512 cycles of either).
 //
-// A unit is (sequence, kv head, 256 keys); a block per multiprocessor takes every gridDim-th of them, and the next
-// unit's keys are under way while the current one's rows are weighed.
-//   warps 0-3, 4-7   key tile 0 / 1: keys to tensor memory, exponentials and sums (thread = key = TMEM lane)
-//   warp 8           TMA producer of the Q ring          warp 9   issues the products
-//   warp 10          -lse*log2(e) of a Q tile's rows, to shared memory
-// TMEM (512 columns): the keys of both tiles at 0 and 64, three S tiles at 128, 256 and 384, used in turn.
+// A unit is (sequence, kv head, 256 keys); a block per multiprocessor takes every gridDim-th of them.
+//   warps 0-15       exponentials and sums (thread = key = TMEM lane): four warps to a key tile and every other Q tile,
+//                    the pairs of them added at the end; the first eight also put the keys into tensor memory
+//   warp 16          TMA producer of the Q ring          warp 17  issues the products
+//   warp 18          -lse*log2(e) of a Q tile's rows     warp 19  copies keys
+// TMEM (512 columns): the keys of both tiles at 0 and 64, three S tiles at 128, 256 and 384, used in turn; a tile is
+// free as soon as its scores are in registers.
 #include <cstdint>
 
 #include "kv8.cuh"
@@ -30,31 +31,41 @@ namespace {
 
 constexpr int kKeys = 128;             // of a tile; a unit has two
 constexpr int kRowTile = 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kSBufs = 3;
 constexpr int kLseSlots = 4;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
 
 template <int D>
 struct Layout {
   static constexpr int kStageBytes = kRowTile * D * 2;      // 64-channel parts of 128-byte swizzled rows
   static constexpr int kPart = kRowTile * 128;
   static constexpr int kParts = D / 64;
-  static constexpr int kStages = D == 128 ? 6 : 12;
-  static constexpr int kOffCtl = kStages * kStageBytes;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kOffKeys = kStages * kStageBytes;
+  static constexpr int kOffCtl = kOffKeys + 2 * kKeys * D * 2;
 };
 
-enum : int { kSiteQFull = 64, kSiteQEmpty, kSiteKeys, kSiteSFull, kSiteSEmpty, kSiteLseFull, kSiteLseEmpty };
+enum : int {
+  kSiteQFull = 64, kSiteQEmpty, kSiteKeys, kSiteSFull, kSiteSEmpty, kSiteLseFull, kSiteLseEmpty, kSiteLoaded, kSiteTaken, kSiteKeysFree,
+  kSitePart
+};
 
 struct Ctl {
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];
-  uint64_t keys[2];
-  uint64_t s_full[kSBufs], s_empty[kSBufs];
+  uint64_t keys[2], keys_free[2];      // in tensor memory
+  uint64_t loaded, taken;              // in shared memory
+  uint64_t part_full[2], part_empty[2];
+  // S tiles for each of the four groups of warps that weigh, by its own count: a group does not see every use of an S buffer,
+  // and it may have as many tiles waiting as there are buffers.
+  uint64_t s_full[4][kSBufs], s_empty[kSBufs];
   uint64_t l_full[kLseSlots], l_empty[kLseSlots];
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
   alignas(16) float nl[kLseSlots][kRowTile];
+  float part[2][kKeys];
+  int8_t exponent[2 * kKeys];
 };
 
 struct Unit {
@@ -93,14 +104,12 @@ __device__ __forceinline__ Unit next_unit(const KvParams& p, int it, int units, 
   return u;
 }
 
-// sum over 64 columns of 2^(s * c + nl), those below lo or from hi on left out where kMask.
+// sum over 32 columns of 2^(s * c + nl), those below lo or from hi on left out where kMask.
 template <bool kMask>
-__device__ __forceinline__ void weigh64(uint32_t s_tmem, uint32_t nl, float c, int lo, int hi, uint64_t (&acc)[4]) {
-  uint32_t s[64];
-  tmem_ld64(s_tmem, s);
+__device__ __forceinline__ void weigh32(const uint32_t (&s)[32], uint32_t nl, float c, int lo, int hi, uint64_t (&acc)[4]) {
   const uint64_t c2 = f32x2(c, c);
 #pragma unroll
-  for (int e = 0; e < 64; e += 4) {
+  for (int e = 0; e < 32; e += 4) {
     const uint4 l = ld_shared_v4(nl + e * 4);
     const uint64_t a = ffma2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, f32x2(__uint_as_float(l.x), __uint_as_float(l.y)));
     const uint64_t b = ffma2(f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, f32x2(__uint_as_float(l.z), __uint_as_float(l.w)));
@@ -117,6 +126,10 @@ __device__ __forceinline__ void weigh64(uint32_t s_tmem, uint32_t nl, float c, i
   }
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
 template <typename T, int D, bool k8>
 __global__ void __launch_bounds__(kThreads, 1)
 weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ WeighParams wp, const int units, const int blocks) {
@@ -127,19 +140,29 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + Lo::kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t sQ = smem_addr(smem);
+  const uint32_t sQ = smem_addr(smem), sK = smem_addr(smem + Lo::kOffKeys);
   const int row_tile = kRowTile / p.g * p.g;           // whole tokens
+  constexpr int kElem = k8 ? 1 : 2, kLanes = D * kElem / 16;      // 16-byte chunks of a key
+  // Where chunk ch of key r of the unit lies: eight keys' chunks of one number are in different banks.
+  auto key_chunk = [&](int r, int ch) {
+    return sK + r * (kLanes * 16) + (kLanes == 4 ? ch ^ ((r >> 1) & 3) : (ch & ~7) | ((ch ^ r) & 7)) * 16;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < kS; ++i) {
       mbar_init(smem_addr(&ctl->q_full[i]), 1);
       mbar_init(smem_addr(&ctl->q_empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->keys[i]), kKeys);
-    for (int i = 0; i < kSBufs; ++i) {
-      mbar_init(smem_addr(&ctl->s_full[i]), 1);
-      mbar_init(smem_addr(&ctl->s_empty[i]), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ctl->keys[i]), kKeys);
+      mbar_init(smem_addr(&ctl->keys_free[i]), 1);
+      mbar_init(smem_addr(&ctl->part_full[i]), kKeys);
+      mbar_init(smem_addr(&ctl->part_empty[i]), kKeys);
     }
+    mbar_init(smem_addr(&ctl->loaded), 1);
+    mbar_init(smem_addr(&ctl->taken), 8);
+    for (int i = 0; i < 4 * kSBufs; ++i) mbar_init(smem_addr(&ctl->s_full[0][i]), 1);
+    for (int i = 0; i < kSBufs; ++i) mbar_init(smem_addr(&ctl->s_empty[i]), 4);
     for (int i = 0; i < kLseSlots; ++i) {
       mbar_init(smem_addr(&ctl->l_full[i]), 1);
       mbar_init(smem_addr(&ctl->l_empty[i]), 8);
@@ -154,7 +177,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
     st_shared_v4(sQ + part * Lo::kPart + (row_tile + r - part * (kRowTile - row_tile)) * 128 + ch * 16, make_uint4(0u, 0u, 0u, 0u));
   }
   fence_proxy_async_smem();
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_addr(&ctl->tmem_base), 512);
     tmem_relinquish();
   }
@@ -168,7 +191,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
   auto first = [&](int it, bool report = false) { return next_unit(p, it, units, blocks, row_tile, report); };
   const int stride = gridDim.x;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // -------------------------------------------------------------------- Q tiles
     if (lane == 0) tma_prefetch_desc(&tm_q);
     int n = 0;
@@ -191,10 +214,11 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       for (int st = 0; st < kS; ++st)
         if (n > st) drain_wait(smem_addr(&ctl->q_full[st]), ((n - 1 - st) / kS) & 1);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // -------------------------------------------------------------------- products
     constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     int n = 0, seq = 0, filled[2] = {0, 0};
+    int given = 0;                                       // a byte for each group: tiles given to it, mod kSBufs
     bool ok = true;
     for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
       if (u.t0 == u.t1) continue;
@@ -214,15 +238,18 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ts_warp(tmem + 128 + buf * 128, tmem + x * 64 + kk * 8, b + (kk >> 2) * (Lo::kPart >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
-          mma_commit_warp(smem_addr(&ctl->s_full[buf]));
+          const int group = x + 2 * ((t - u.t0) & 1), at = given >> (8 * group) & 255;
+          mma_commit_warp(smem_addr(&ctl->s_full[group][at]));
+          given += at == kSBufs - 1 ? -(at << (8 * group)) : 1 << (8 * group);
         }
         if (!ok) break;
         mma_commit_warp(smem_addr(&ctl->q_empty[st]));
       }
+      for (int x = 0; ok && x < tiles; ++x) mma_commit_warp(smem_addr(&ctl->keys_free[x]));
     }
     mma_commit_warp(smem_addr(&ctl->done));
     drain_wait(smem_addr(&ctl->done), 0);
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // -------------------------------------------------------------------- lse of the rows
     int n = 0;
     bool ok = true;
@@ -248,70 +275,95 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    // -------------------------------------------------------------------- keys, exponentials, sums
-    constexpr int kLoads = D * (k8 ? 1 : 2) / 16;
-    const int x = warp >> 2;                             // key tile
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint4 raw[kLoads];
-    int exponent = 0;
-    auto load_key = [&](const Unit& u) {
-      const int c = u.key0 + x * kKeys + row;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c >= u.sq.len) return;
-      const int pg = c / p.P, slot = c - pg * p.P;
-      const int page = load_i32(p.table + u.s * p.table_stride + pg);
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-        atomicOr(&g_error_word, kErrPage);               // its key reads as zeros
-        return;
-      }
-      const uint8_t* at = static_cast<const uint8_t*>(p.k) + (page * p.k_p + slot * p.k_t + u.hk * p.k_h) * (k8 ? 1 : 2);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) raw[i] = load_b128(at + i * 16);
-      if (k8) exponent = scale_exponent(p.scales.k[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block + u.hk * p.scales.k_head]);
-    };
-    // 32 columns are 64 channels
-    auto write_key = [&] {
-      const uint32_t scale = k8 ? pair_two_to<T>(exponent) : 0u;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        uint32_t y[32];
-#pragma unroll
-        for (int i = 0; i < kLoads / (D / 64); ++i) {
-          const uint4 r = raw[h * (kLoads / (D / 64)) + i];
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (k8)
-              decode4<T>(w[e], scale, y[i * 8 + 2 * e], y[i * 8 + 2 * e + 1]);
-            else
-              y[i * 4 + e] = w[e];
+  } else if (warp == 19) {
+    // -------------------------------------------------------------------- keys to shared memory, a unit ahead
+    int n = 0;
+    bool ok = true;
+    for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
+      if (u.t0 == u.t1) continue;
+      if (n > 0 && !(ok = wait(&ctl->taken, n - 1, kSiteTaken))) break;
+      const int* table = p.table + u.s * p.table_stride;
+      const uint8_t* base = static_cast<const uint8_t*>(p.k) + u.hk * p.k_h * kElem;
+#pragma unroll 1
+      for (int r0 = 0; r0 < u.keys; r0 += 32) {
+        // a lane looks up a key; kLanes lanes copy its row
+        const int c = u.key0 + r0 + lane, pg = c / p.P, slot = c - pg * p.P;
+        long long at = -1;                               // zeros
+        int e = 0;
+        if (c < u.sq.len) {
+          const int page = load_i32(table + pg);
+          if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
+            at = (page * p.k_p + slot * p.k_t) * kElem;
+            if (k8) e = scale_exponent(p.scales.k[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block + u.hk * p.scales.k_head]);
+          } else {
+            atomicOr(&g_error_word, kErrPage);
           }
         }
-        tmem_st32(tmem + lanes + x * 64 + h * 32, y);
+        if (k8) ctl->exponent[r0 + lane] = static_cast<int8_t>(e);
+        const int ch = lane % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int r = i * (32 / kLanes) + lane / kLanes;
+          const long long from = __shfl_sync(0xffffffffu, at, r);
+          copy16(key_chunk(r0 + r, ch), base + max(from, 0ll) + ch * 16, from >= 0);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(smem_addr(&ctl->keys[x]));
-    };
-    int n = 0, seq = 0;
-    bool ok = true;
-    Unit u = first(blockIdx.x);
-    bool ahead = u.it < units && u.has(x) && u.t0 < u.t1;        // raw holds the next key to be written
-    if (ahead) {
-      load_key(u);
-      write_key();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl->loaded));
+      ++n;
     }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------------- exponentials, sums; keys to tensor memory
+    const int x = (warp >> 2) & 1, half = warp >> 3;     // key tile; every other Q tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int n = 0, seq = 0, weighed = 0, parts = 0;
+    int loads = 0, writes = 0;                           // units, units whose keys this tile has
+    bool ok = true;
+    // 32 columns are 64 channels
+    auto write_keys = [&](const Unit& u) {
+      if (u.it >= units || u.t0 == u.t1) return;
+      if (u.has(x) && writes > 0 && !(ok = warp_wait_inline(smem_addr(&ctl->keys_free[x]), (writes - 1) & 1, flag, kSiteKeysFree))) return;
+      if (!(ok = warp_wait_inline(smem_addr(&ctl->loaded), loads & 1, flag, kSiteLoaded))) return;
+      ++loads;
+      if (u.has(x)) {
+        ++writes;
+        tc_fence_after_sync();
+        const int r = x * kKeys + row;
+        const uint32_t scale = k8 ? pair_two_to<T>(ctl->exponent[r]) : 0u;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 4 * kElem; ++i) {
+            const uint4 v = ld_shared_v4(key_chunk(r, h * 4 * kElem + i));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (k8)
+                decode4<T>(w[e], scale, y[i * 8 + 2 * e], y[i * 8 + 2 * e + 1]);
+              else
+                y[i * 4 + e] = w[e];
+            }
+          }
+          tmem_st32(tmem + lanes + x * 64 + h * 32, y);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(smem_addr(&ctl->keys[x]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl->taken));
+    };
+    Unit u = first(blockIdx.x);
+    if (half == 0) write_keys(u);
     while (ok && u.it < units) {
-      const Unit next = first(u.it + stride);
-      ahead = next.it < units && next.has(x) && next.t0 < next.t1;
-      if (ahead) load_key(next);
       const int c = u.key0 + x * kKeys + row;
       const bool live = c < u.sq.len;
       float* w = wp.w + u.s * wp.w_seq + u.hk * wp.w_head + c;
-      const float old = live && c < u.sq.len - u.sq.n ? *w * wp.decay : 0.f;
+      const float old = half == 0 && live && c < u.sq.len - u.sq.n ? *w * wp.decay : 0.f;
       // rows below this one do not see the key; the whole warp's keys are seen from `clear` on
       const long long r0 = live ? static_cast<long long>(first_token(p, u.sq, c)) * p.g : 0;
       const int from = static_cast<int>(min(r0, static_cast<long long>(u.rows)));
@@ -319,48 +371,68 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       const int tiles = u.has(1) ? 2 : 1;
       float total = 0.f;
       for (int t = u.t0; t < u.t1; ++t, ++n, seq += tiles) {
+        if (((t - u.t0) & 1) != half) continue;
         const int slot = n % kLseSlots;
+        if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
         if (u.has(x)) {
           const int buf = (seq + x) % kSBufs;
-          if (!(ok = warp_wait_inline(smem_addr(&ctl->s_full[buf]), ((seq + x) / kSBufs) & 1, flag, kSiteSFull))) break;
+          if (!(ok = warp_wait_inline(smem_addr(&ctl->s_full[x + 2 * half][weighed % kSBufs]), (weighed / kSBufs) & 1, flag, kSiteSFull))) break;
           tc_fence_after_sync();
-          // the last product of this unit with this tile's keys is done: the next unit's take their place
-          if (t + 1 == u.t1 && ahead) write_key();
-          if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
+          ++weighed;
           const int cols = min(row_tile, u.rows - t * row_tile), lo = from - t * row_tile;
           const uint32_t ts = tmem + lanes + 128 + buf * 128, nl = smem_addr(&ctl->nl[slot][0]);
+          const bool whole = cols == row_tile && clear <= t * row_tile;
           uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-          if (cols == row_tile && clear <= t * row_tile) {
-            weigh64<false>(ts, nl, p.scale_log2, 0, 64, acc);
-            weigh64<false>(ts + 64, nl + 256, p.scale_log2, 0, 64, acc);
-          } else {
 #pragma unroll 1
-            for (int ch = 0; ch < cols; ch += 64) weigh64<true>(ts + ch, nl + ch * 4, p.scale_log2, lo - ch, cols - ch, acc);
-          }
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(&ctl->s_empty[buf]));
-            mbar_arrive(smem_addr(&ctl->l_empty[slot]));
+          for (int ch = 0; ch < kRowTile; ch += 32) {
+            if (ch >= cols) continue;                    // not read: free already
+            uint32_t s[32];
+            tmem_ld32(ts + ch, s);
+            if (ch + 32 >= cols) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&ctl->s_empty[buf]));
+            }
+            if (whole)
+              weigh32<false>(s, nl + ch * 4, p.scale_log2, 0, 32, acc);
+            else
+              weigh32<true>(s, nl + ch * 4, p.scale_log2, lo - ch, cols - ch, acc);
           }
           float a, b;
           f32x2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
           total += a + b;
-        } else {
-          if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
-          if (lane == 0) mbar_arrive(smem_addr(&ctl->l_empty[slot]));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_empty[slot]));
       }
       if (!ok) break;
-      if (live) *w = old + total;
-      if (ahead && !(u.has(x) && u.t0 < u.t1)) write_key();
+      const Unit next = first(u.it + stride);
+      if (half == 0) write_keys(next);
+      if (!ok) break;
+      // the sums of the odd Q tiles to those of the even ones
+      if (u.has(x)) {
+        if (u.t1 - u.t0 > 1) {
+          const uint32_t bar = smem_addr(half ? &ctl->part_empty[x] : &ctl->part_full[x]);
+          if (half) {
+            if (parts > 0 && !(ok = warp_wait_inline(bar, (parts - 1) & 1, flag, kSitePart))) break;
+            ctl->part[x][row] = total;
+            mbar_arrive(smem_addr(&ctl->part_full[x]));
+          } else {
+            if (!(ok = warp_wait_inline(bar, parts & 1, flag, kSitePart))) break;
+            total += ctl->part[x][row];
+            mbar_arrive(smem_addr(&ctl->part_empty[x]));
+          }
+          ++parts;
+        }
+        if (half == 0 && live) *w = old + total;
+      }
       u = next;
     }
   }
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
