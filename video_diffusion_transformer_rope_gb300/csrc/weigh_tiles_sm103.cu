@@ -251,25 +251,35 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
     drain_wait(smem_addr(&ctl->done), 0);
   } else if (warp == 18) {
     // -------------------------------------------------------------------- lse of the rows
+    constexpr int kPer = kRowTile / 32;
     int n = 0;
     bool ok = true;
+    long long at[kPer];                                  // where this lane's rows of a head's first tile lie
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = i * 32 + lane;
+      at[i] = x < row_tile ? static_cast<long long>(x % p.g) * p.N + x / p.g : -1;
+    }
     for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
+      const float* lse = wp.lse + static_cast<long long>(u.hk) * p.g * p.N + u.sq.row0;
+      float v[kPer], ahead[kPer];                        // of this tile and the next
+      auto load = [&](int t, float (&to)[kPer]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          to[i] = -INFINITY;                             // no row
+          if (at[i] >= 0 && t * row_tile + i * 32 + lane < u.rows) to[i] = lse[at[i] + t * (row_tile / p.g)];
+        }
+      };
+      load(u.t0, ahead);
       for (int t = u.t0; t < u.t1; ++t, ++n) {
         const int slot = n % kLseSlots;
-        float v[kRowTile / 32];
 #pragma unroll
-        for (int i = 0; i < kRowTile / 32; ++i) {
-          const int x = i * 32 + lane, R = t * row_tile + x;
-          v[i] = -INFINITY;                              // no row, or one that saw no key: 2^-inf = 0
-          if (x < row_tile && R < u.rows) {
-            const int tok = R / p.g, h = u.hk * p.g + (R - tok * p.g);
-            const float l = wp.lse[lse_index(p, u.s, u.sq, h, tok)];
-            if (l != -INFINITY) v[i] = l * -1.4426950408889634f;
-          }
-        }
+        for (int i = 0; i < kPer; ++i) v[i] = ahead[i];
+        if (t + 1 < u.t1) load(t + 1, ahead);
         if (n >= kLseSlots && !(ok = wait(&ctl->l_empty[slot], n / kLseSlots - 1, kSiteLseEmpty))) break;
+        // a row that saw no key weighs 2^-inf = 0
 #pragma unroll
-        for (int i = 0; i < kRowTile / 32; ++i) ctl->nl[slot][i * 32 + lane] = v[i];
+        for (int i = 0; i < kPer; ++i) ctl->nl[slot][i * 32 + lane] = v[i] == -INFINITY ? -INFINITY : v[i] * -1.4426950408889634f;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ctl->l_full[slot]));
       }
