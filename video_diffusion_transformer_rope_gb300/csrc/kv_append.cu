@@ -255,7 +255,41 @@ kv_append(const __grid_constant__ AppendParams p) {
 // A thread block takes the blocks ("segments") of the cache whose first new token is among its kRows8 rows, for keys or
 // values; a segment may reach up to 15 rows further.  One warp looks up those 31 rows, one to a lane.
 constexpr int kRows8 = 16;
+constexpr int kResident8 = 7;
 constexpr int kWindow8 = kRows8 + kBlock8 - 1;
+
+// The 8 channels of a lane as pairs of pairs: even channels (0, 2), (4, 6), odd channels (1, 3), (5, 7), so that the turn of
+// two channel pairs is two packed instructions for each of their channels.
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& x, uint64_t (&even)[2], uint64_t (&odd)[2]) {
+  const float2 a = unpack2<T>(x.x), b = unpack2<T>(x.y), c = unpack2<T>(x.z), d = unpack2<T>(x.w);
+  even[0] = f32x2(a.x, b.x);
+  even[1] = f32x2(c.x, d.x);
+  odd[0] = f32x2(a.y, b.y);
+  odd[1] = f32x2(c.y, d.y);
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float largest2(uint64_t a, float m) {
+  float x, y;
+  f32x2_split(a, x, y);
+  return fmax3(m, fabsf(x), fabsf(y));
+}
+// Codes of 8 channels in order.
+__device__ __forceinline__ uint2 encode_pairs(const uint64_t (&even)[2], const uint64_t (&odd)[2]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a, b, c, d;
+    f32x2_split(even[i], a, b);
+    f32x2_split(odd[i], c, d);
+    w[i] = encode4(a, c, b, d);
+  }
+  return make_uint2(w[0], w[1]);
+}
 
 struct Segment8 {
   int row, count;              // first row in the window, new tokens
@@ -284,7 +318,7 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
   constexpr int kLanes = D / 8;                  // of a row
   constexpr int kPer = 32 / kLanes;              // rows of a warp's step
   constexpr int kSteps = kBlock8 / kPer;
-  __shared__ __align__(16) float2 cs[kKeys ? kWindow8 : 1][D / 2];
+  __shared__ __align__(16) float s_cos[kKeys ? kWindow8 : 1][D / 2], s_sin[kKeys ? kWindow8 : 1][D / 2];
   __shared__ Segment8 segs[kRows8];
   __shared__ int s_axis[kWindow8][3];
   __shared__ int s_count;
@@ -352,7 +386,9 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
     const int from = segs[0].row, to = segs[count - 1].row + segs[count - 1].count;
     for (int i = from * (D / 2) + tid; i < to * (D / 2); i += kThreads) {
       const int j = i / (D / 2), pr = i % (D / 2);
-      cs[j][pr] = cos_sin(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
+      const float2 t = cos_sin(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
+      s_cos[j][pr] = t.x;
+      s_sin[j][pr] = t.y;
     }
     __syncthreads();
   }
@@ -365,8 +401,8 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
   const long long scale_head = kKeys ? p.scales.k_head : p.scales.v_head;
   const int ch = lane % kLanes, sub = lane / kLanes;
   const bool norm = kKeys && p.k_norm;
-  float w[8];
-  unpack8<T>(norm ? load_b128(static_cast<const T*>(p.k_norm) + ch * 8) : make_uint4(0u, 0u, 0u, 0u), w);
+  uint64_t w_even[2], w_odd[2];
+  unpack_pairs<T>(norm ? load_b128(static_cast<const T*>(p.k_norm) + ch * 8) : make_uint4(0u, 0u, 0u, 0u), w_even, w_odd);
   bool past = false;
   for (int t = by * (kThreads / 32) + warp; t < count * p.Hkv; t += ny * (kThreads / 32)) {
     const int si = t / p.Hkv, h = t - si * p.Hkv;
@@ -381,14 +417,49 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
       x[i] = (g.fits >> j & 1) ? load_b128(from + j * src_row) : make_uint4(0u, 0u, 0u, 0u);      // 0 or NaN below: no maximum
     }
     const int e_old = g.older ? scale_exponent(*to_scale) : kMinExp8;
-    float f[kSteps][8];
+    // Twice over the rows, as they were read: their largest value, then their codes.  Held in between the fp32 values
+    // would take twice the registers, and half as many warps would be loading.
+    float inv_rms[kSteps];
+    // a row times the norm's weights, turned; its rsqrt(mean square) is left to the caller
+    auto turned = [&](int i, uint64_t (&even)[2], uint64_t (&odd)[2]) {
+      if (norm) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          even[c] = fmul2(even[c], w_even[c]);
+          odd[c] = fmul2(odd[c], w_odd[c]);
+        }
+      }
+      const int j = min(g.row + i * kPer + sub, kWindow8 - 1);
+      const float4 cn = *reinterpret_cast<const float4*>(&s_cos[j][ch * 4]), sn = *reinterpret_cast<const float4*>(&s_sin[j][ch * 4]);
+      const uint64_t c2[2] = {f32x2(cn.x, cn.y), f32x2(cn.z, cn.w)}, s2[2] = {f32x2(sn.x, sn.y), f32x2(sn.z, sn.w)};
+      const uint64_t n2[2] = {f32x2(-sn.x, -sn.y), f32x2(-sn.z, -sn.w)};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint64_t u = even[c], v = odd[c];
+        even[c] = ffma2(u, c2[c], fmul2(v, n2[c]));
+        odd[c] = ffma2(u, s2[c], fmul2(v, c2[c]));
+      }
+    };
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      unpack8<T>(x[i], f[i]);
-      if (kKeys) norm_rotate<D>(f[i], norm, w, p.eps, &cs[min(g.row + i * kPer + sub, kWindow8 - 1)][ch * 4]);
+      uint64_t even[2], odd[2];
+      unpack_pairs<T>(x[i], even, odd);
+      float scale = 1.f;
+      if (kKeys) {
+        if (norm) {
+          float a, b;
+          f32x2_split(ffma2(odd[1], odd[1], ffma2(even[1], even[1], ffma2(odd[0], odd[0], fmul2(even[0], even[0])))), a, b);
+          float sq = a + b;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(f[i][c]));
+          for (int o = D / 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+          scale = rsqrtf(sq * (1.f / D) + p.eps);
+        }
+        turned(i, even, odd);
+      }
+      inv_rms[i] = scale;
+      const float m = largest2(odd[1], largest2(odd[0], largest2(even[1], largest2(even[0], 0.f))));
+      top = fmaxf(top, m * scale);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -408,22 +479,30 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int j = i * kPer + sub;
-      if (!(g.fits >> j & 1)) continue;
+      asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));      // worked out anew, not held
+      uint64_t even[2], odd[2];
+      unpack_pairs<T>(x[i], even, odd);
+      if (kKeys) turned(i, even, odd);
+      const float by = inv_rms[i] * inv;
+      const uint64_t by2 = f32x2(by, by);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) f[i][c] *= inv;
-      *reinterpret_cast<uint2*>(to + (g.older + j) * dst_token) =
-          make_uint2(encode4(f[i][0], f[i][1], f[i][2], f[i][3]), encode4(f[i][4], f[i][5], f[i][6], f[i][7]));
+      for (int c = 0; c < 2; ++c) {
+        even[c] = fmul2(even[c], by2);
+        odd[c] = fmul2(odd[c], by2);
+      }
+      if (g.fits >> j & 1) *reinterpret_cast<uint2*>(to + (g.older + j) * dst_token) = encode_pairs(even, odd);
     }
     if (lane == 0 && g.fits) *to_scale = static_cast<uint8_t>(e + 127);
   }
   if (past) atomicOr(&g_error_word, kErrRange8);
 }
 
+// The blocks of keys, which take longest, first; then those of values and of queries.  (Side by side, so that issue slots
+// and memory are wanted at the same time, 21600 tokens of 3 x 40 heads take 286 us, not 264.)
 template <typename T, int D, int kTok>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident8)
 kv_append8(const __grid_constant__ AppendParams p, const int nx, const int ny, const int qx) {
   wait_for_earlier_work();
-  // keys, values and queries side by side, as in kv_append; the first two by blocks of kRows8 rows
   const int b = blockIdx.x, each = nx * ny;
   if (b < each)
     append_blocks<T, D, true>(p, b % nx, nx, b / nx, ny);
@@ -467,13 +546,14 @@ cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
   return pairs <= static_cast<long long>(kResident) * sms ? launch_tok<T, D, 2>(p, sms, stream) : launch_tok<T, D, 4>(p, sms, stream);
 }
 
-template <typename T, int D>
-cudaError_t launch8(const AppendParams& p, int sms, cudaStream_t stream) {
-  constexpr int kTok = 2, kGroups = kThreads / (D / 8), kWarps = kThreads / 32;
+template <typename T, int D, int kTok>
+cudaError_t launch8_tok(const AppendParams& p, int sms, cudaStream_t stream) {
+  constexpr int kGroups = kThreads / (D / 8), kWarps = kThreads / 32;
   const int nx = (p.rows - 1) / kRows8 + 1, qx = p.Hq > 0 ? (p.rows - 1) / kTok + 1 : 0;
+  // few rows: the heads over blocks too, as in launch_tok
   int ny = 1, qy = 1;
   const int most = (p.Hkv * kRows8 + kWarps - 1) / kWarps, q_most = (kTok * p.Hq + kGroups - 1) / kGroups;
-  while (ny < most && 2ll * nx * ny < 2ll * sms) ny *= 2;
+  while (ny < most && static_cast<long long>(nx) * ny < sms) ny *= 2;
   while (qy < q_most && static_cast<long long>(qx) * qy < 2ll * sms) qy *= 2;
   ny = ny < most ? ny : most;
   qy = qy < q_most || qx == 0 ? qy : q_most;
@@ -487,6 +567,10 @@ cudaError_t launch8(const AppendParams& p, int sms, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv_append8<T, D, kTok>, p, nx, ny, qx);
+}
+template <typename T, int D>
+cudaError_t launch8(const AppendParams& p, int sms, cudaStream_t stream) {
+  return p.rows <= 1024 ? launch8_tok<T, D, 2>(p, sms, stream) : launch8_tok<T, D, 4>(p, sms, stream);
 }
 
 }  // namespace

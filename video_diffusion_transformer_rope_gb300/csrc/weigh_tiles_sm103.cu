@@ -373,7 +373,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       const int c = u.key0 + x * kKeys + row;
       const bool live = c < u.sq.len;
       float* w = wp.w + u.s * wp.w_seq + u.hk * wp.w_head + c;
-      const float old = half == 0 && live && c < u.sq.len - u.sq.n ? *w * wp.decay : 0.f;
+      const float old = half == 0 && live && c < u.sq.len - u.sq.n ? *w : 0.f;
       // rows below this one do not see the key; the whole warp's keys are seen from `clear` on
       const long long r0 = live ? static_cast<long long>(first_token(p, u.sq, c)) * p.g : 0;
       const int from = static_cast<int>(min(r0, static_cast<long long>(u.rows)));
@@ -434,7 +434,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
           }
           ++parts;
         }
-        if (half == 0 && live) *w = old + total;
+        if (half == 0 && live) *w = old * wp.decay + total;
       }
       u = next;
     }
