@@ -192,7 +192,7 @@ def test_structures_match_the_header(tmp_path):
             assert int(got[f"{name}.{f[0]}"]) == getattr(st, f[0]).offset
 
 
-@pytest.mark.parametrize("name", ["kv8.cuh", "kv_mma.cuh", "kv_weigh.cu", "weigh_tiles_sm103.cu", "sm103_wait.cuh", "kv_evict.cu"])
+@pytest.mark.parametrize("name", ["kv8.cuh", "kv_mma.cuh", "rows_join.cuh", "attn_rows8.cu", "kv_weigh.cu", "weigh_tiles_sm103.cu", "sm103_wait.cuh", "kv_evict.cu"])
 def test_kernels_that_start_early_read_through_the_coherent_path(name):
     text = re.sub(r"//[^\n]*", "", open(os.path.join(_build.CSRC, name)).read())
     assert not re.findall(r"__ldg|ld\.global\.nc|__restrict__|ld_nc", text)

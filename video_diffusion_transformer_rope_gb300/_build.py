@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvdx.so")
 SOURCES = ["vdx_capi.cu", "attn_fwd_sm103.cu", "attn_fwd_f32.cu", "vdx_noalloc.cu", "kv_capi.cu",
-           "kv_append.cu", "attn_rows.cu", "attn_tiles_sm103.cu", "kv_weigh.cu", "weigh_tiles_sm103.cu", "kv_evict.cu", "kv_evict_capi.cu"]
+           "kv_append.cu", "attn_rows.cu", "attn_rows8.cu", "attn_tiles_sm103.cu", "kv_weigh.cu", "weigh_tiles_sm103.cu", "kv_evict.cu", "kv_evict_capi.cu"]
 EXT = os.path.join(PKG, "_streaming_py.so")
 EXT_STAMP = os.path.join(OUT_DIR, "streaming_py.torch")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

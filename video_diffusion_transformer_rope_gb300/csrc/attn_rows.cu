@@ -26,6 +26,7 @@
 
 #include "kv_common.cuh"
 #include "kv_mma.cuh"
+#include "rows_join.cuh"
 
 namespace vdx {
 namespace {
@@ -34,36 +35,15 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 16;        // keys of one stage
 constexpr int kStages = 3;
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// kNT tiles of 8 query rows.  k8: the cache holds 8-bit codes (kv8.cuh).  Then the products are of fp16 whatever the
-// call's type, since codes become fp16 in one instruction (and bf16 in five): queries of bf16 are brought
-// into fp16's range by a power of two of the row's own, exactly, which scores are multiplied back by, as they are by
-// the key's scale; values are multiplied by their scale on the way, exactly; weights are taken times 2^7 (of at
-// most 2^8), so that fp16 keeps those down to 2^-21 of a row's largest.  Codes are laid out for the
-// fragments by what can be exchanged for free: the channels within a step of K Q^T, and those of the output.
-template <typename T, int D, int kNT, bool k8>
+// kNT tiles of 8 query rows.
+template <typename T, int D, int kNT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 attn_rows(const __grid_constant__ KvParams p) {
-  using M = std::conditional_t<k8, __half, T>;         // what the products take
   constexpr int kRows = 8 * kNT;
-  constexpr int kElem = k8 ? 1 : 2;
-  constexpr int kChunks = D * kElem / 16;              // 16-byte chunks of a key
-  constexpr int kRowBytes = D * kElem;
-  constexpr float kLift = k8 ? 7.f : 0.f;              // log2 of what weights are multiplied by
+  constexpr int kChunks = D / 8;                       // 16-byte chunks of a key
+  constexpr int kRowBytes = D * 2;
   constexpr int kTileBytes = kKeys * kRowBytes;        // K or V of one stage
   constexpr int kCopies = kKeys * kChunks / 32;        // 16-byte copies per lane and tile
-  constexpr int kPad = D + 4;
   extern __shared__ __align__(128) uint8_t smem[];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -87,7 +67,6 @@ attn_rows(const __grid_constant__ KvParams p) {
 
   // Query fragments (B operand: k = channel, n = row): row 8*nt + gq, channels 16*ks + 2*c4 (+8).
   uint32_t qf[kNT][D / 16][2];
-  float row_scale[k8 ? kNT : 1][2];      // k8: scale_log2 and the query's power of two, for the two rows below
   int limit[kNT][2];                     // of the two rows whose scores this lane holds
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
@@ -98,11 +77,10 @@ attn_rows(const __grid_constant__ KvParams p) {
       src = static_cast<const T*>(p.q) + (p.cu ? 0 : s * p.q_b) + (static_cast<long long>(sq.row0) + tok) * p.q_t + h * p.q_h;
     }
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {          // k8: channels 4*c4 and up, the order in which a lane gets its codes
-      qf[nt][ks][0] = src ? load_b32(src + ks * 16 + (k8 ? 4 : 2) * c4) : 0u;
-      qf[nt][ks][1] = src ? load_b32(src + ks * 16 + (k8 ? 4 * c4 + 2 : 8 + 2 * c4)) : 0u;
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qf[nt][ks][0] = src ? load_b32(src + ks * 16 + 2 * c4) : 0u;
+      qf[nt][ks][1] = src ? load_b32(src + ks * 16 + 8 + 2 * c4) : 0u;
     }
-    if constexpr (k8) query_to_half<T, D>(qf[nt], nt, c4, row_scale, p.scale_log2);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rr = nt * 8 + 2 * c4 + e;
@@ -129,17 +107,13 @@ attn_rows(const __grid_constant__ KvParams p) {
       for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
   }
 
-  // Chunk `c` of row r of a tile lies at chunk swizzle(c, r), so that 8 rows' chunks of one number fill all banks
-  // (rows of 64 bytes: two to a line of banks).
-  auto swizzle = [](int c, int r) { return kRowBytes == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); };
-
   // ---- the warp's ring of key blocks lo + 16*(warp + 4*i)
   const uint32_t ring = smem_addr(smem) + warp * kStages * 2 * kTileBytes;
   const int step = kKeys * kWarps;
   const int k_first = lo + kKeys * warp;
   const int nblocks = k_first < hi ? (hi - k_first + step - 1) / step : 0;
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + hk * p.k_h * kElem;
-  const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + hk * p.v_h * kElem;
+  const T* kbase = static_cast<const T*>(p.k) + hk * p.k_h;
+  const T* vbase = static_cast<const T*>(p.v) + hk * p.v_h;
   const int* table = p.table ? p.table + static_cast<long long>(s) * p.table_stride : nullptr;
   // Page of the next block to copy and the one after it (a block crosses at most one page end:
   // paged sizes are >= 16, and a dense "page" holds every key).
@@ -158,21 +132,6 @@ attn_rows(const __grid_constant__ KvParams p) {
   };
   fetch_pages(k_first);
   const int ch = lane % kChunks, r_in = lane / kChunks;
-  // k8: scales of the blocks being copied, oldest first: lane l has the exponent of key l, lane 16 + l of value l
-  int exps[kStages - 1];
-  auto fetch_scale = [&](int key) {
-    const int row = lane & 15;
-    int o2 = off + row, page = e0;
-    if (o2 >= p.P) {
-      o2 -= p.P;
-      page = e1;
-    }
-    if (key + row >= hi || static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) return 0;
-    const Scales8& sc = p.scales;
-    const uint8_t* at = lane < 16 ? sc.k + page * sc.k_page + o2 / kBlock8 * sc.k_block + hk * sc.k_head
-                                  : sc.v + page * sc.v_page + o2 / kBlock8 * sc.v_block + hk * sc.v_head;
-    return scale_exponent(*at);
-  };
   auto copy_block = [&](int i) {
     const int key = k_first + i * step;
     const uint32_t dst = ring + (i % kStages) * 2 * kTileBytes;
@@ -185,17 +144,16 @@ attn_rows(const __grid_constant__ KvParams p) {
         page = e1;
       }
       const bool ok = key + row < hi && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-      const uint32_t d = dst + row * kRowBytes + (swizzle(ch, row) << 4);
-      const uint8_t* ks = kbase;
-      const uint8_t* vs = vbase;
+      const uint32_t d = dst + row * kRowBytes + ((ch ^ (row & 7)) << 4);
+      const T* ks = kbase;
+      const T* vs = vbase;
       if (ok) {
-        ks += (page * p.k_p + o2 * p.k_t) * kElem + ch * 16;
-        vs += (page * p.v_p + o2 * p.v_t) * kElem + ch * 16;
+        ks += page * p.k_p + o2 * p.k_t + ch * 8;
+        vs += page * p.v_p + o2 * p.v_t + ch * 8;
       }
       cp_async16(d, ks, ok);
       cp_async16(d + kTileBytes, vs, ok);
     }
-    if constexpr (k8) exps[kStages - 2] = fetch_scale(key);
     off += step;
     while (off >= p.P && table) {
       off -= p.P;
@@ -205,9 +163,6 @@ attn_rows(const __grid_constant__ KvParams p) {
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if constexpr (k8) {
-      for (int j = 0; j + 1 < kStages - 1; ++j) exps[j] = exps[j + 1];
-    }
     if (i < nblocks) copy_block(i);
     cp_commit();
   }
@@ -217,18 +172,6 @@ attn_rows(const __grid_constant__ KvParams p) {
   for (int i = 0; i < nblocks; ++i) {
     cp_wait<kStages - 2>();
     __syncwarp();                       // every lane's copies of block i are in; stage i-1 is free
-    float key_scale[2];                 // k8: of the keys gq and gq + 8
-    uint32_t value_scale[2];            // k8: of the keys 2*c4, 2*c4 + 1 and those 8 on, as pairs
-    if constexpr (k8) {
-      const int e = exps[0];
-      for (int j = 0; j + 1 < kStages - 1; ++j) exps[j] = exps[j + 1];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        key_scale[x] = two_to(__shfl_sync(0xffffffffu, e, gq + 8 * x));
-        const int a = __shfl_sync(0xffffffffu, e, 16 + 8 * x + 2 * c4), b = __shfl_sync(0xffffffffu, e, 17 + 8 * x + 2 * c4);
-        value_scale[x] = half_two_to(a) | (half_two_to(b) << 16);
-      }
-    }
     if (i + kStages - 1 < nblocks) copy_block(i + kStages - 1);
     cp_commit();
     const uint32_t kt = ring + (i % kStages) * 2 * kTileBytes;
@@ -240,32 +183,18 @@ attn_rows(const __grid_constant__ KvParams p) {
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st[nt][e] = 0.f;
-    if constexpr (k8) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ks += 2) {          // a chunk of 16 codes is a step of 16 channels
-        uint32_t c[4];
-        ldsm4(c, kt + lrow_k * kRowBytes + (swizzle(ks + lch_k, lrow_k) << 4));
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4];
+      ldsm4(a, kt + lrow_k * kRowBytes + (((2 * ks + lch_k) ^ (lrow_k & 7)) << 4));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a[4] = {decode2<false>(c[2 * x]), decode2<false>(c[2 * x + 1]), decode2<true>(c[2 * x]), decode2<true>(c[2 * x + 1])};
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks + x][0], qf[nt][ks + x][1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[4];
-        ldsm4(a, kt + lrow_k * kRowBytes + (((2 * ks + lch_k) ^ (lrow_k & 7)) << 4));
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-      }
+      for (int nt = 0; nt < kNT; ++nt) mma16816<T>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
     }
     bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st[nt][e] *= k8 ? row_scale[k8 ? nt : 0][e & 1] * key_scale[e >> 1] : p.scale_log2;
+      for (int e = 0; e < 4; ++e) st[nt][e] *= p.scale_log2;
       if (key0 + kKeys > full_to) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -299,131 +228,28 @@ attn_rows(const __grid_constant__ KvParams p) {
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       // a row that has seen no key yet: every score is -inf and weighs 2^-inf = 0
-      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kLift;
-      const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kLift;
+      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+      const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
       const float p0 = ex2_approx(st[nt][0] - m0), p1 = ex2_approx(st[nt][1] - m1);
       const float p2 = ex2_approx(st[nt][2] - m0), p3 = ex2_approx(st[nt][3] - m1);
       l[nt][0] += p0 + p2;
       l[nt][1] += p1 + p3;
-      b[nt][0] = transpose8x8(pack2<M>(p0, p1));
-      b[nt][1] = transpose8x8(pack2<M>(p2, p3));
+      b[nt][0] = transpose8x8(pack2<T>(p0, p1));
+      b[nt][1] = transpose8x8(pack2<T>(p2, p3));
     }
-    if constexpr (k8) {
-      // Transposed as pairs of codes, a lane gets channels 2*gq and 2*gq + 1 of two keys: they are the product's
-      // rows gq and gq + 8, once the four codes are put in order.
 #pragma unroll
-      for (int mt = 0; mt < D / 16; mt += 2) {
-        uint32_t c[4];
-        ldsm4_trans(c, vt + lrow_v * kRowBytes + (swizzle(mt + lch_v, lrow_v) << 4));
+    for (int mt = 0; mt < D / 16; ++mt) {
+      uint32_t a[4];
+      ldsm4_trans(a, vt + lrow_v * kRowBytes + (((2 * mt + lch_v) ^ (lrow_v & 7)) << 4));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t lo = __byte_perm(c[x], 0u, 0x3120), up = __byte_perm(c[x + 2], 0u, 0x3120);
-          const uint32_t a[4] = {half2_mul(decode2<false>(lo), value_scale[0]), half2_mul(decode2<true>(lo), value_scale[0]),
-                                 half2_mul(decode2<false>(up), value_scale[1]), half2_mul(decode2<true>(up), value_scale[1])};
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(o[nt][mt + x], a, b[nt][0], b[nt][1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        uint32_t a[4];
-        ldsm4_trans(a, vt + lrow_v * kRowBytes + (((2 * mt + lch_v) ^ (lrow_v & 7)) << 4));
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) mma16816<M>(o[nt][mt], a, b[nt][0], b[nt][1]);
-      }
+      for (int nt = 0; nt < kNT; ++nt) mma16816<T>(o[nt][mt], a, b[nt][0], b[nt][1]);
     }
     __syncwarp();
   }
   cp_wait<0>();
   __syncthreads();                      // the rings become the warps' partial results
 
-  float* so = reinterpret_cast<float*>(smem);                       // [kWarps][kRows][kPad]
-  float* sm = so + kWarps * kRows * kPad;                           // [kWarps][kRows]
-  float* sl = sm + kWarps * kRows;
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float t = l[nt][e];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-      const int r = nt * 8 + 2 * c4 + e;
-      if (gq == 0) {
-        sm[warp * kRows + r] = m[nt][e] - kLift;
-        sl[warp * kRows + r] = t;
-      }
-      float* dst = so + (warp * kRows + r) * kPad;
-#pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        dst[mt * 16 + (k8 ? 2 * gq : gq)] = o[nt][mt][e];
-        dst[mt * 16 + (k8 ? 2 * gq + 1 : gq + 8)] = o[nt][mt][e + 2];
-      }
-    }
-  }
-  __syncthreads();
-  // Four channels per thread.
-  const long long slot = static_cast<long long>(unit) * p.nsplit + z;
-  float* cm = sl + kWarps * kRows;                                  // [kRows]: this CTA's maximum and sum
-  float* cl = cm + kRows;
-  auto store = [&](int r, int dq, float mx, float lt, const float4& acc) {
-    const int tok = r / p.g, h = hk * p.g + (r - tok * p.g);
-    const bool none = mx == -INFINITY && lt == lt;                  // no key seen; a NaN sum is an answer
-    const float inv = none ? 0.f : 1.f / lt;
-    uint2 w2;
-    w2.x = pack2<T>(acc.x * inv, acc.y * inv);
-    w2.y = pack2<T>(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (out_row(p, s, sq, tok) * p.Hq + h) * D + dq) = w2;
-    if (dq == 0 && p.lse)
-      p.lse[lse_index(p, s, sq, h, tok)] = none ? -INFINITY : (mx + __log2f(lt)) * 0.69314718055994530942f;
-  };
-  for (int i = threadIdx.x; i < live * (D / 4); i += kWarps * 32) {
-    const int r = i / (D / 4), dq = (i % (D / 4)) * 4;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w * kRows + r]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float lt = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float wt = ex2_approx(sm[w * kRows + r] - base);
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * kPad + dq);
-      lt += wt * sl[w * kRows + r];
-      acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
-    }
-    if (p.cluster) {
-      *reinterpret_cast<float4*>(so + r * kPad + dq) = acc;          // over warp 0's, which only this thread reads
-      if (dq == 0) {
-        cm[r] = mx;
-        cl[r] = lt;
-      }
-    } else if (p.nsplit > 1) {
-      *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + dq) = acc;
-      if (dq == 0) p.part_ml[slot * kRows + r] = make_float2(mx, lt);
-    } else {
-      store(r, dq, mx, lt, acc);
-    }
-  }
-  if (!p.cluster) return;
-  cluster_sync_all();                   // every CTA's part is in its shared memory
-  for (int i = threadIdx.x + z * kWarps * 32; i < live * (D / 4); i += p.nsplit * kWarps * 32) {
-    const int r = i / (D / 4), dq = (i % (D / 4)) * 4;
-    const uint32_t am = smem_addr(cm + r), al = smem_addr(cl + r), ao = smem_addr(so + r * kPad + dq);
-    float mx = -INFINITY;
-    for (int w = 0; w < p.nsplit; ++w) mx = fmaxf(mx, ld_cluster_f32(mapa_shared(am, w)));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float lt = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < p.nsplit; ++w) {
-      const float wt = ex2_approx(ld_cluster_f32(mapa_shared(am, w)) - base);
-      const float4 v = ld_cluster_f32x4(mapa_shared(ao, w));
-      lt += wt * ld_cluster_f32(mapa_shared(al, w));
-      acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
-    }
-    store(r, dq, mx, lt, acc);
-  }
-  cluster_sync_all();                   // no CTA leaves while another reads its part
+  join_warps<T, D, kNT, kWarps, false>(p, s, hk, unit, z, sq, live, smem, o, m, l, 0.f);
 }
 
 // Join the key splits of every row: out = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z.  kPer warps per
@@ -520,13 +346,13 @@ attn_join(const __grid_constant__ KvParams p) {
     p.lse[lse_index(p, s, sq, h, tok)] = empty ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
 }
 
-template <typename T, int D, int kNT, bool k8>
+template <typename T, int D, int kNT>
 cudaError_t launch_nt(const KvParams& p, cudaStream_t stream) {
-  const int ring = kWarps * kStages * 2 * kKeys * D * (k8 ? 1 : 2);
+  const int ring = kWarps * kStages * 2 * kKeys * D * 2;
   const int join = (kWarps * (D + 4 + 2) + 2) * 8 * kNT * 4;
   const int smem = ring > join ? ring : join;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_shared(attn_rows<T, D, kNT, k8>, smem, &done);
+  const cudaError_t e = allow_shared(attn_rows<T, D, kNT>, smem, &done);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.S) * p.Hkv * p.nblk * p.nsplit;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -543,17 +369,13 @@ cudaError_t launch_nt(const KvParams& p, cudaStream_t stream) {
   attr[1] = launch_early();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, attn_rows<T, D, kNT, k8>, p);
-}
-template <typename T, int D, bool k8>
-cudaError_t launch_kind(const KvParams& p, cudaStream_t stream) {
-  if (p.block_rows == 8) return launch_nt<T, D, 1, k8>(p, stream);
-  if (p.block_rows == 16) return launch_nt<T, D, 2, k8>(p, stream);
-  return launch_nt<T, D, 4, k8>(p, stream);
+  return cudaLaunchKernelEx(&cfg, attn_rows<T, D, kNT>, p);
 }
 template <typename T, int D>
 cudaError_t launch(const KvParams& p, cudaStream_t stream) {
-  return p.eight ? launch_kind<T, D, true>(p, stream) : launch_kind<T, D, false>(p, stream);
+  if (p.block_rows == 8) return launch_nt<T, D, 1>(p, stream);
+  if (p.block_rows == 16) return launch_nt<T, D, 2>(p, stream);
+  return launch_nt<T, D, 4>(p, stream);
 }
 template <typename T, int D>
 cudaError_t join(const KvParams& p, cudaStream_t stream) {

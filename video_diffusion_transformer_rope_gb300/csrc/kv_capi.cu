@@ -140,7 +140,7 @@ vdx_status launch(const Problem& pb, void* stream) {
   cudaError_t e;
   const char* what = nullptr;
   if (pb.p.rows_kernel) {
-    e = vdx::launch_attn_rows(pb.p, pb.d, pb.dtype, st);
+    e = (pb.p.eight ? vdx::launch_attn_rows8 : vdx::launch_attn_rows)(pb.p, pb.d, pb.dtype, st);
   } else {
     vdx::EncodeTiledFn encode = nullptr;
     if (!vdx::encode_tiled_fn(&encode)) return VDX_ERR_CUDA;

@@ -105,6 +105,7 @@ inline cudaError_t allow_shared(Kernel* kernel, int bytes, std::atomic<uint64_t>
 size_t plan_attention(KvParams* p, int d, int sms);
 
 cudaError_t launch_attn_rows(const KvParams& p, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_rows8(const KvParams& p, int d, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_tiles(const KvParams& p, int d, int dtype, EncodeTiledFn encode, int sms,
                               cudaStream_t stream, const char** what);
 cudaError_t launch_attn_combine(const KvParams& p, int d, int dtype, cudaStream_t stream);
@@ -149,6 +150,7 @@ cudaError_t launch_evict(const EvictParams& p, int d, bool eight, int sms, cudaS
 // Read and reset the error words of these translation units (synchronous).
 cudaError_t read_and_clear_error_word_append(unsigned int* word);
 cudaError_t read_and_clear_error_word_rows(unsigned int* word);
+cudaError_t read_and_clear_error_word_rows8(unsigned int* word);
 cudaError_t read_and_clear_error_word_tiles(unsigned int* word);
 cudaError_t read_and_clear_error_word_weigh_rows(unsigned int* word);
 cudaError_t read_and_clear_error_word_weigh_tiles(unsigned int* word);
