@@ -5,7 +5,7 @@
 // for a kv head's rows r, the (token, query head of its group) pairs; lse comes from the attention call.
 //
 // This file, few rows: bound by DRAM, which each key crosses once (its value is not needed), so K streams as in attn_rows.cu:
-// a warp takes 16 keys at a time through a ring of its own, S^T = K Q^T by m16n8k16 products with the keys on the
+// a warp takes 32 keys at a time through a ring of its own, S^T = K Q^T by m16n8k16 products with the keys on the
 // 16-wide side, and a key's sum over its rows ends as a shuffle over four lanes.  Nothing is shared between warps and
 // each w is written by one lane: the same call gives the same bits.  More than 32 rows: weigh_tiles_sm103.cu.
 #include <cstdint>
@@ -16,18 +16,18 @@ namespace vdx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;
-constexpr int kStages = 4;
+constexpr int kKeys = 32;        // keys of one stage, a lane each
+constexpr int kStages = 3;
 
 template <typename T, int D, int kNT, bool k8>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 weigh_rows(const __grid_constant__ WeighParams wp) {
-  using M = std::conditional_t<k8, __half, T>;
+  using M = std::conditional_t<k8, __half, T>;         // what the products take (attn_rows8.cu)
   constexpr int kElem = k8 ? 1 : 2;
-  constexpr int kChunks = D * kElem / 16;
   constexpr int kRowBytes = D * kElem;
+  constexpr int kChunks = kRowBytes / 16;              // 16-byte chunks of a key
   constexpr int kTileBytes = kKeys * kRowBytes;
-  constexpr int kCopies = kKeys * kChunks / 32;
+  constexpr int kPer = 32 / kChunks;                   // rows that the lanes copy at once
   const KvParams& p = wp.kv;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -44,17 +44,66 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
   const int lo = static_cast<int>(min(lo64, static_cast<long long>(sq.len)));
   const int hi = static_cast<int>(min(lo64 + wp.split_keys, static_cast<long long>(sq.len)));
 
+  constexpr int step = kKeys * kWarps;
   const uint32_t ring = smem_addr(smem) + warp * kStages * kTileBytes;
-  const int step = kKeys * kWarps;
   const int k_first = lo + kKeys * warp;
   const int nblocks = k_first < hi ? (hi - k_first + step - 1) / step : 0;
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + hk * p.k_h * kElem;
   const int* table = p.table + static_cast<long long>(s) * p.table_stride;
+  const int ch = lane % kChunks, r_in = lane / kChunks;
+  const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + hk * p.k_h * kElem + ch * 16;
+  const uint8_t* kscale = p.scales.k + hk * p.scales.k_head;
   float* w = wp.w + s * wp.w_seq + hk * wp.w_head;
   const int old_to = sq.len - sq.n;                     // keys below were there before the call
   auto swizzle = [](int c, int r) { return kRowBytes == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); };
-  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
-  const int ch = lane % kChunks, r_in = lane / kChunks;
+
+  // This lane's key of the block to be copied next: entry of the page table and token in the page; its page, when it has come.
+  int pg = 0, off = 0, page = 0;
+  if (nblocks > 0) {
+    pg = (k_first + lane) / p.P;
+    off = k_first + lane - pg * p.P;
+    if (k_first + lane < hi) page = load_i32(table + pg);
+  }
+  // Scales and weights so far of the blocks being copied, oldest first: those of this lane's key
+  int exps[kStages];
+  float old[kStages];
+  auto copy_block = [&](int i) {
+    const int key = k_first + i * step + lane;
+    const bool there = key < hi, ok = there && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+    if (there && !ok) atomicOr(&g_error_word, kErrPage);              // reads as zeros
+    long long at = -1;
+    exps[kStages - 1] = 127;
+    if (ok) {
+      at = (page * p.k_p + off * p.k_t) * kElem;
+      if (k8) exps[kStages - 1] = kscale[page * p.scales.k_page + off / kBlock8 * p.scales.k_block];
+    }
+    old[kStages - 1] = there && key < old_to ? w[key] : 0.f;
+    off += step;
+    while (off >= p.P) {
+      off -= p.P;
+      ++pg;
+    }
+    if (key + step < hi) page = load_i32(table + pg);                 // of the next block
+    const uint32_t dst = ring + (i % kStages) * kTileBytes;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int row = c * kPer + r_in;
+      const long long from = __shfl_sync(0xffffffffu, at, row);
+      cp_async16(dst + row * kRowBytes + (swizzle(ch, row) << 4), kbase + max(from, 0ll), from >= 0);
+    }
+  };
+  auto shift = [&] {
+#pragma unroll
+    for (int j = 0; j + 1 < kStages; ++j) {
+      exps[j] = exps[j + 1];
+      old[j] = old[j + 1];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    shift();
+    if (i < nblocks) copy_block(i);
+    cp_commit();
+  }
 
   uint32_t qf[kNT][D / 16][2];
   float row_scale[kNT][2], lse2[kNT][2];
@@ -89,124 +138,67 @@ weigh_rows(const __grid_constant__ WeighParams wp) {
   }
   const int full_to = min(hi, visible_limit(p, sq, 0));     // below it every row sees everything
 
-  int pg = nblocks > 0 ? k_first / p.P : 0;
-  int off = nblocks > 0 ? k_first - pg * p.P : 0;
-  int e0 = 0, e1 = 0;
-  auto fetch_pages = [&](int key) {
-    e0 = key < hi ? load_i32(table + pg) : 0;
-    e1 = (off + kKeys > p.P && key + (p.P - off) < hi) ? load_i32(table + pg + 1) : 0;
-    if (static_cast<unsigned>(e0) >= static_cast<unsigned>(p.num_pages) ||
-        static_cast<unsigned>(e1) >= static_cast<unsigned>(p.num_pages)) {
-      if (lane == 0) atomicOr(&g_error_word, kErrPage);
-    }
-  };
-  fetch_pages(k_first);
-  // scales and weights so far of the blocks being copied, oldest first: lane l has those of key l
-  int exps[kStages - 1];
-  float old[kStages - 1];
-  auto copy_block = [&](int i) {
-    const int key = k_first + i * step;
-    const uint32_t dst = ring + (i % kStages) * kTileBytes;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      const int row = r_in + c * (32 / kChunks);
-      int o2 = off + row, page = e0;
-      if (o2 >= p.P) {
-        o2 -= p.P;
-        page = e1;
-      }
-      const bool ok = key + row < hi && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-      cp_async16(dst + row * kRowBytes + (swizzle(ch, row) << 4),
-                 ok ? kbase + (page * p.k_p + o2 * p.k_t) * kElem + ch * 16 : kbase, ok);
-    }
-    const int row = lane & 15, mine = key + row;
-    if constexpr (k8) {
-      int o2 = off + row, page = e0;
-      if (o2 >= p.P) {
-        o2 -= p.P;
-        page = e1;
-      }
-      exps[kStages - 2] = mine < hi && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)
-                              ? scale_exponent(p.scales.k[page * p.scales.k_page + o2 / kBlock8 * p.scales.k_block + hk * p.scales.k_head])
-                              : 0;
-    }
-    old[kStages - 2] = mine < hi && mine < old_to ? w[mine] * wp.decay : 0.f;
-    off += step;
-    while (off >= p.P) {
-      off -= p.P;
-      ++pg;
-    }
-    if (i + 1 < nblocks) fetch_pages(key + step);
-  };
-  auto shift = [&] {
-#pragma unroll
-    for (int j = 0; j + 1 < kStages - 1; ++j) {
-      exps[j] = exps[j + 1];
-      old[j] = old[j + 1];
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    shift();
-    if (i < nblocks) copy_block(i);
-    cp_commit();
-  }
+  const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
   for (int i = 0; i < nblocks; ++i) {
     cp_wait<kStages - 2>();
-    __syncwarp();
-    float key_scale[2] = {1.f, 1.f}, before[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if constexpr (k8) key_scale[x] = two_to(__shfl_sync(0xffffffffu, exps[0], gq + 8 * x));
-      before[x] = __shfl_sync(0xffffffffu, old[0], gq + 8 * x);
-    }
+    __syncwarp();                       // every lane's copies of block i are in; stage i-1 is free
     shift();
     if (i + kStages - 1 < nblocks) copy_block(i + kStages - 1);
     cp_commit();
     const uint32_t kt = ring + (i % kStages) * kTileBytes;
     const int key0 = k_first + i * step;
-    float sum[2] = {0.f, 0.f};
-    float st[kNT][4];
+    const float key_scale = k8 ? two_to(scale_exponent(static_cast<uint8_t>(exps[0]))) : 1.f;
+    float mine = 0.f;                   // this lane's key's sum
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int h = 0; h < 2; ++h) {       // 16 keys
+      const int row = h * 16 + lrow;
+      float st[kNT][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st[nt][e] = 0.f;
-    if constexpr (k8) {
+      for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ks += 2) {
-        uint32_t c[4];
-        ldsm4(c, kt + lrow * kRowBytes + (swizzle(ks + lch, lrow) << 4));
+        for (int e = 0; e < 4; ++e) st[nt][e] = 0.f;
+      if constexpr (k8) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a[4] = {decode2<false>(c[2 * x]), decode2<false>(c[2 * x + 1]), decode2<true>(c[2 * x]), decode2<true>(c[2 * x + 1])};
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          uint32_t c[4];
+          ldsm4(c, kt + row * kRowBytes + (swizzle(ks + lch, row) << 4));
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks + x][0], qf[nt][ks + x][1]);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a[4] = {decode2<false>(c[2 * x]), decode2<false>(c[2 * x + 1]), decode2<true>(c[2 * x]), decode2<true>(c[2 * x + 1])};
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks + x][0], qf[nt][ks + x][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t a[4];
+          ldsm4(a, kt + row * kRowBytes + (swizzle(2 * ks + lch, row) << 4));
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
         }
       }
-    } else {
+      const float f[2] = {__shfl_sync(0xffffffffu, key_scale, h * 16 + gq), __shfl_sync(0xffffffffu, key_scale, h * 16 + gq + 8)};
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[4];
-        ldsm4(a, kt + lrow * kRowBytes + (swizzle(2 * ks + lch, lrow) << 4));
+      for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) mma16816<M>(st[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+        for (int e = 0; e < 4; ++e) {
+          float x = fmaf(st[nt][e] * f[e >> 1], row_scale[nt][e & 1], -lse2[nt][e & 1]);
+          if (key0 + kKeys > full_to && key0 + h * 16 + gq + (e >> 1) * 8 >= limit[nt][e & 1]) x = -INFINITY;
+          sum[e >> 1] += ex2_approx(x);
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+        // key h * 16 + x * 8 + k is in lanes 4k to 4k + 3; its own lane is the one of its number
+        const float y = __shfl_sync(0xffffffffu, sum[x], (lane & 7) * 4);
+        if (lane >> 3 == 2 * h + x) mine = y;
       }
     }
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = fmaf(st[nt][e] * (k8 ? key_scale[e >> 1] : 1.f), row_scale[nt][e & 1], -lse2[nt][e & 1]);
-        if (key0 + kKeys > full_to && key0 + gq + (e >> 1) * 8 >= limit[nt][e & 1]) x = -INFINITY;
-        sum[e >> 1] += ex2_approx(x);
-      }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-      sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-      const int key = key0 + gq + 8 * x;
-      if (c4 == 0 && key < hi) w[key] = before[x] + sum[x];
-    }
+    // one store of 32 neighbours
+    if (key0 + lane < hi) w[key0 + lane] = old[0] * wp.decay + mine;
   }
   cp_wait<0>();
 }
@@ -248,7 +240,7 @@ cudaError_t launch_weigh_rows(WeighParams p, int d, int dtype, int sms, cudaStre
   // blocks of 64 to 1024 keys, several to a multiprocessor where there are enough
   const long long units = static_cast<long long>(p.kv.S) * p.kv.Hkv;
   long long n = (8ll * sms + units - 1) / units;
-  n = n < (p.kv.max_kv + 1023) / 1024 ? (p.kv.max_kv + 1023) / 1024 : n;
+  n = n < (p.kv.max_kv + 2047) / 2048 ? (p.kv.max_kv + 2047) / 2048 : n;
   long long keys = (p.kv.max_kv + n - 1) / n;
   keys = (keys + 63) / 64 * 64;
   p.split_keys = static_cast<int>(keys < 64 ? 64 : keys);
