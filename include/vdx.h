@@ -404,7 +404,8 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* cache, const vdx_kv8_scale
  * wanted), with which the next token appended stands where it would have stood; index[s, h, j], the old
  * cache index of the key that is now at j, and w_out[s, h, j], its weight (both for j < keep; -1 and 0 past the new length).
  *   w_out may be w (same strides); otherwise outputs must not overlap inputs, nor each other.
- *   max_kv: host bound on L (0: what the page table and width hold); L past it is clamped and reported.
+ *   max_kv: host bound on L (0: what the page table and width hold), at most 393216 (VDX_ERR_UNSUPPORTED past it); L past
+ *   it is clamped and reported.
  *   Slots of `into` that `into`'s table does not reach, or whose page is outside it, are skipped and reported. */
 typedef struct vdx_paged_evict_args {
   const float* w;           /* [seqs, Hkv, width], the entries of a head contiguous               */

@@ -156,6 +156,13 @@ def test_evict_refusals(L, kw, status, msg):
     _refused(L, L.vdx_paged_evict(ref(_cache()), ref(_scales()), ref(_to()), ref(_to_scales()), ref(_evict(**kw)), None), status, msg)
 
 
+def test_evict_says_how_many_keys_it_takes(L):
+    big = dict(page_size=1 << 14, max_pages=25, table_stride=25, num_pages=30, k_page=1 << 23, v_page=1 << 23)
+    c, to = _cache(**big), _to(**dict(big, k=FAKE + 30 * G, v=FAKE + 31 * G))
+    a = dict(w_head=1 << 19, w_seq=1 << 21, width=1 << 19)
+    _refused(L, L.vdx_paged_evict(ref(c), None, ref(to), None, ref(_evict(**a)), None), B.VDX_ERR_UNSUPPORTED, "393216 keys")
+
+
 @pytest.mark.parametrize("tkw,msg", [
     (dict(Hkv=3), "one kind"), (dict(d=64), "one kind"), (dict(dtype=1), "one kind"), (dict(seqs=2), "one kind"),
     (dict(k=FAKE, v=FAKE + G, page_table=FAKE + 2 * G), "same page table"), (dict(k=FAKE, v=FAKE + G, num_pages=19), "same strides"),

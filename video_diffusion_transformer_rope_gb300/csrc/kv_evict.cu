@@ -1,11 +1,12 @@
 // Eviction from a paged cache by the weight that each key has gathered: which keys of a (sequence, kv head) stay, and
 // the move of what stays into the pages of another table.
 //
-// evict_select, a block per (sequence, head): of the first L - recent weights the `need` largest, of equals the lowest
-// indices.  The border is found digit by digit (8 bits of the weights as ordered integers, from the top: a histogram
-// of those that share the digits so far, then the digit that holds the need-th largest), then one walk in order
-// writes index and weights of what stays; a key's place is the number of keys above the border before it and of those
-// equal to it, up to the last that fits.
+// evict_select, a cluster of up to 8 blocks per (sequence, head), a run of the weights in each one's shared memory: of the
+// first L - recent weights the `need` largest, of equals the lowest indices.  The border is found digit by digit (8 bits
+// of the weights as ordered integers, from the top: a histogram of those that share the digits so far, summed over the
+// blocks, then the digit that holds the need-th largest), then one walk in order writes index and weights of what
+// stays; a key's place is the number of keys above the border before it and of those equal to it, up to the last that fits.
+// Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 FILL).
 //
 // evict_move, a warp per (16 slots of a page, head): rows of 16 keys and values, found through the index and the old
 // page table, 16 bytes a lane; in 8 bits their largest value gives the new scale first.  Bound by DRAM: what stays is read
@@ -18,8 +19,10 @@
 namespace vdx {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 4;               // weights of a thread in one step of a walk
+constexpr int kMaxRun = kMaxEvictKeys / 8;      // weights that a block's shared memory holds
 
 // Larger weights are larger numbers; NaN is the largest, -0 is 0.
 __device__ __forceinline__ uint32_t ordered(float w) {
@@ -34,16 +37,31 @@ __device__ __forceinline__ int evict_length(const EvictParams& p, int s, bool re
   return used;
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_addr(p), rank)) : "memory");
+  return v;
+}
+
 __global__ void __launch_bounds__(kThreads)
-evict_select(const __grid_constant__ EvictParams p) {
-  __shared__ uint32_t hist[32][256 + 1];
+evict_select(const __grid_constant__ EvictParams p, const int cluster) {
+  extern __shared__ __align__(16) float run[];             // this block's weights
+  __shared__ uint32_t hist[kWarps][256 + 1];
+  __shared__ uint32_t s_total[2][256], s_all[256], s_count[2];
   __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint2 s_sum[2][32];
+  __shared__ uint2 s_sum[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x % p.Hkv, s = blockIdx.x / p.Hkv;
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / cluster, hk = unit % p.Hkv, s = unit / p.Hkv;
+  auto sync_all = [&] {
+    if (cluster > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+  };
   wait_for_earlier_work();
-  const int len = evict_length(p, s, tid == 0 && hk == 0), left = min(len, p.keep);
-  if (tid == 0 && hk == 0) {
+  const int len = evict_length(p, s, tid == 0 && rank == 0 && hk == 0), left = min(len, p.keep);
+  if (tid == 0 && rank == 0 && hk == 0) {
     p.kv_len_out[s] = left;
     if (p.pos_offset_out) p.pos_offset_out[s] = (p.pos_offset ? load_i32(p.pos_offset + s) : 0) + (len - left);
   }
@@ -51,30 +69,46 @@ evict_select(const __grid_constant__ EvictParams p) {
   float* w_out = p.w_out + s * p.w_out_seq + hk * p.w_out_head;
   int* index = p.index + (static_cast<long long>(s) * p.Hkv + hk) * p.keep;
 
+  const int per = ((len + cluster - 1) / cluster + kPer - 1) / kPer * kPer;
+  const int begin = min(rank * per, len), count = min(per, len - begin);
+#pragma unroll 4
+  for (int i = tid; i < count; i += kThreads) run[i] = w[begin + i];
   const int older = len > p.keep ? len - p.recent : 0;      // the candidates; the rest stays
+  const int mine = min(max(older - begin, 0), count);       // of them in this run
   uint32_t border = 0, need = len > p.keep ? p.keep - p.recent : 0;
   if (need > 0) {
     uint32_t prefix = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 32 * 257; i += kThreads) (&hist[0][0])[i] = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      for (int i = tid; i < kWarps * 257; i += kThreads) (&hist[0][0])[i] = 0;
       __syncthreads();
-      for (int i = tid; i < older; i += kThreads) {
-        const uint32_t u = ordered(w[i]);
+      for (int i = tid; i < mine; i += kThreads) {
+        const uint32_t u = ordered(run[i]);
         // a histogram per warp: weights crowd into few digits
-        if (shift == 24 || (u >> (shift + 8)) == prefix) atomicAdd(&hist[warp][(u >> shift) & 255], 1u);
+        if (pass == 0 || (u >> (shift + 8)) == prefix) atomicAdd(&hist[warp][(u >> shift) & 255], 1u);
       }
       __syncthreads();
       if (tid < 256) {
         uint32_t n = 0;
-        for (int i = 0; i < 32; ++i) n += hist[i][tid];
-        hist[0][tid] = n;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) n += hist[i][tid];
+        s_total[pass & 1][tid] = n;
+      }
+      sync_all();
+      if (tid < 256) {
+        uint32_t n = s_total[pass & 1][tid];
+        if (cluster > 1) {
+          n = 0;
+          for (int r = 0; r < cluster; ++r) n += ld_cluster_u32(&s_total[pass & 1][tid], r);
+        }
+        s_all[tid] = n;
       }
       __syncthreads();
       if (warp == 0) {
         // from the top digit down, 8 digits to a lane: where the need-th largest lies
         uint32_t n[8], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += n[i] = hist[0][255 - (lane * 8 + i)];
+        for (int i = 0; i < 8; ++i) sum += n[i] = s_all[255 - (lane * 8 + i)];
         uint32_t before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -97,61 +131,85 @@ evict_select(const __grid_constant__ EvictParams p) {
     }
     border = prefix;
   }
-  // In order: above the border stays, of those at it the first `need`.  Everything is read before anything is
-  // written at or behind it, so w_out may be w.
+  auto above_border = [&](int i, uint32_t u) { return i >= mine || (need > 0 && u > border); };
+  auto at_border = [&](int i, uint32_t u) { return i < mine && need > 0 && u == border; };
+  // What lies before this run: counted by its blocks.
   uint32_t above = 0, equal = 0;
-  for (int base = 0, step = 0; base < len; base += kThreads * kPer, ++step) {
+  if (cluster > 1) {
+    if (tid < 2) s_count[tid] = 0;
+    __syncthreads();
+    uint32_t g = 0, q = 0;
+    for (int i = tid; i < count; i += kThreads) {
+      const uint32_t u = ordered(run[i]);
+      g += above_border(i, u);
+      q += at_border(i, u);
+    }
+    g = __reduce_add_sync(0xffffffffu, g);
+    q = __reduce_add_sync(0xffffffffu, q);
+    if (lane == 0) {
+      atomicAdd(&s_count[0], g);
+      atomicAdd(&s_count[1], q);
+    }
+    cluster_sync_all();
+    for (int r = 0; r < rank; ++r) {
+      above += ld_cluster_u32(&s_count[0], r);
+      equal += ld_cluster_u32(&s_count[1], r);
+    }
+  } else {
+    __syncthreads();
+  }
+  // In order: above the border stays, of those at it the first `need`.  Every weight of the head is in shared memory by
+  // now, so w_out may be w.
+  for (int base = 0, step = 0; base < count; base += kThreads * kPer, ++step) {
     float x[kPer];
     uint32_t gt = 0, eq = 0;                                // bits
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int i = base + tid * kPer + e;
-      x[e] = i < len ? w[i] : 0.f;
-      if (i < len) {
+      x[e] = i < count ? run[i] : 0.f;
+      if (i < count) {
         const uint32_t u = ordered(x[e]);
-        if (i >= older || (need > 0 && u > border))
-          gt |= 1u << e;
-        else if (need > 0 && u == border)
-          eq |= 1u << e;
+        if (above_border(i, u)) gt |= 1u << e;
+        if (at_border(i, u)) eq |= 1u << e;
       }
     }
-    uint2 run = make_uint2(__popc(gt), __popc(eq));
-    const uint2 own = run;
+    uint2 sum = make_uint2(__popc(gt), __popc(eq));
+    const uint2 own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t a = __shfl_up_sync(0xffffffffu, run.x, o), b = __shfl_up_sync(0xffffffffu, run.y, o);
-      if (lane >= o) run = make_uint2(run.x + a, run.y + b);
+      const uint32_t a = __shfl_up_sync(0xffffffffu, sum.x, o), b = __shfl_up_sync(0xffffffffu, sum.y, o);
+      if (lane >= o) sum = make_uint2(sum.x + a, sum.y + b);
     }
-    if (lane == 31) s_sum[step & 1][warp] = run;
+    if (lane == 31) s_sum[step & 1][warp] = sum;
     __syncthreads();
-    const uint2 mine = s_sum[step & 1][lane];
-    uint2 all = mine;
+    const uint2 of_warp = lane < kWarps ? s_sum[step & 1][lane] : make_uint2(0u, 0u);
+    uint2 all = of_warp;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kWarps; o <<= 1) {
       const uint32_t a = __shfl_up_sync(0xffffffffu, all.x, o), b = __shfl_up_sync(0xffffffffu, all.y, o);
       if (lane >= o) all = make_uint2(all.x + a, all.y + b);
     }
-    uint32_t g = above + run.x - own.x + __shfl_sync(0xffffffffu, all.x - mine.x, warp);
-    uint32_t q = equal + run.y - own.y + __shfl_sync(0xffffffffu, all.y - mine.y, warp);
+    uint32_t g = above + sum.x - own.x + __shfl_sync(0xffffffffu, all.x - of_warp.x, warp);
+    uint32_t q = equal + sum.y - own.y + __shfl_sync(0xffffffffu, all.y - of_warp.y, warp);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const bool is_gt = gt >> e & 1, is_eq = eq >> e & 1;
       if (is_gt || (is_eq && q < need)) {
         const uint32_t at = g + min(q, need);
-        index[at] = base + tid * kPer + e;
+        index[at] = begin + base + tid * kPer + e;
         w_out[at] = x[e];
       }
       g += is_gt;
       q += is_eq;
     }
-    above += __shfl_sync(0xffffffffu, all.x, 31);
-    equal += __shfl_sync(0xffffffffu, all.y, 31);
+    above += __shfl_sync(0xffffffffu, all.x, kWarps - 1);
+    equal += __shfl_sync(0xffffffffu, all.y, kWarps - 1);
   }
-  __syncthreads();
-  for (int j = left + tid; j < p.keep; j += kThreads) {
+  for (int j = left + rank * kThreads + tid; j < p.keep; j += cluster * kThreads) {
     index[j] = -1;
     w_out[j] = 0.f;
   }
+  if (cluster > 1) cluster_sync_all();                      // no block leaves while another reads its counts
 }
 
 constexpr int kMoveWarps = 4;
@@ -273,17 +331,32 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, int d, bool eight, int sms, cudaStream_t stream) {
-  (void)sms;
+cudaError_t launch_evict(const EvictParams& p, int d, bool eight, cudaStream_t stream) {
   note_launch();
+  // runs of about 4096 weights; one block reads them fast enough, and barriers of a cluster cost more than they save
+  int cluster = 1;
+  while (cluster < 8 && p.max_kv > cluster * 4096) cluster *= 2;
+  const int run = ((p.max_kv + cluster - 1) / cluster + kPer - 1) / kPer * kPer;
+  const int smem = run * 4;
+  const long long blocks = static_cast<long long>(p.S) * p.Hkv * cluster;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(evict_select, kMaxRun * 4, &done);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.S * p.Hkv));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr = launch_early();
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select, p);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = launch_early();
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, evict_select, p, cluster);
   if (e != cudaSuccess) return e;
   if (eight) return d == 128 ? launch_move<128, true>(p, stream) : launch_move<64, true>(p, stream);
   return d == 128 ? launch_move<128, false>(p, stream) : launch_move<64, false>(p, stream);

@@ -200,6 +200,8 @@ vdx_status vdx_paged_evict(const vdx_paged_kv* c, const vdx_kv8_scales* scales, 
   p.S = c->seqs; p.Hkv = c->Hkv; p.keep = a->keep; p.recent = a->recent;
   const int cap = std::min(c->max_pages * c->page_size, a->width);
   p.max_kv = a->max_kv > 0 ? std::min(a->max_kv, cap) : cap;
+  if (p.max_kv > vdx::kMaxEvictKeys)
+    return fail(VDX_ERR_UNSUPPORTED, "eviction from up to %d keys; max_kv, the page table and width allow %d", vdx::kMaxEvictKeys, p.max_kv);
   p.w = a->w; p.w_out = a->w_out; p.w_seq = a->w_seq; p.w_head = a->w_head; p.w_out_seq = a->w_out_seq; p.w_out_head = a->w_out_head;
   p.kv_len = a->kv_len; p.pos_offset = a->pos_offset; p.kv_len_out = a->kv_len_out; p.pos_offset_out = a->pos_offset_out;
   p.index = a->index;
@@ -207,7 +209,7 @@ vdx_status vdx_paged_evict(const vdx_paged_kv* c, const vdx_kv8_scales* scales, 
     p.scales = device_scales(*scales);
     p.scales_to = device_scales(*to_scales);
   }
-  const cudaError_t e = vdx::launch_evict(p, c->d, scales != nullptr, multiprocessors(), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = vdx::launch_evict(p, c->d, scales != nullptr, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(VDX_ERR_CUDA, "eviction kernel launch: %s", cudaGetErrorString(e));

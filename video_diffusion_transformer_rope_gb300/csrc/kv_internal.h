@@ -145,7 +145,8 @@ struct EvictParams {
   int* index;
   Scales8 scales, scales_to;
 };
-cudaError_t launch_evict(const EvictParams& p, int d, bool eight, int sms, cudaStream_t stream);
+constexpr int kMaxEvictKeys = 8 * 49152;      // weights of a head, in the shared memory of a cluster
+cudaError_t launch_evict(const EvictParams& p, int d, bool eight, cudaStream_t stream);
 
 // Read and reset the error words of these translation units (synchronous).
 cudaError_t read_and_clear_error_word_append(unsigned int* word);
