@@ -402,7 +402,8 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* cache, const vdx_kv8_scale
  * blocks of `into` get scales by the rule of vdx_rope3d_append8, as if the values were appended at once.
  * Written beside: kv_len_out[s] = min(L, keep); pos_offset_out[s] = pos_offset[s] + L - kv_len_out[s] (NULL: not
  * wanted), with which the next token appended stands where it would have stood; index[s, h, j], the old
- * cache index of the key that is now at j, and w_out[s, h, j], its weight (both for j < keep; -1 and 0 past the new length).
+ * cache index of the key that is now at j, and w_out[s, h, j], its weight (both for j < keep; -1 and 0 past the new length; a
+ * weight of -0 comes out as 0, a NaN as a NaN).
  *   w_out may be w (same strides); otherwise outputs must not overlap inputs, nor each other.
  *   max_kv: host bound on L (0: what the page table and width hold), at most 393216 (VDX_ERR_UNSUPPORTED past it); L past
  *   it is clamped and reported.

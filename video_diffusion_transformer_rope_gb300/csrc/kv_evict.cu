@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = 4;               // weights of a thread in one step of a walk
+constexpr int kPer = 8;               // weights of a thread in one step of a walk
 constexpr int kMaxRun = kMaxEvictKeys / 8;      // weights that a block's shared memory holds
 
 // Larger weights are larger numbers; NaN is the largest, -0 is 0.
@@ -30,6 +30,9 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
   return b >> 31 ? ~b : b | 0x80000000u;
 }
+
+// The weight that it was (-0 comes back as 0, a NaN as some NaN).
+__device__ __forceinline__ float weight_of(uint32_t u) { return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u); }
 
 __device__ __forceinline__ int evict_length(const EvictParams& p, int s, bool report) {
   const int len = load_i32(p.kv_len + s), used = min(max(len, 0), p.max_kv);
@@ -45,7 +48,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, int rank) 
 
 __global__ void __launch_bounds__(kThreads)
 evict_select(const __grid_constant__ EvictParams p, const int cluster) {
-  extern __shared__ __align__(16) float run[];             // this block's weights
+  extern __shared__ __align__(16) uint32_t run[];          // this block's weights, as ordered integers
   __shared__ uint32_t hist[kWarps][256 + 1];
   __shared__ uint32_t s_total[2][256], s_all[256], s_count[2];
   __shared__ uint32_t s_prefix, s_need;
@@ -71,8 +74,15 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
 
   const int per = ((len + cluster - 1) / cluster + kPer - 1) / kPer * kPer;
   const int begin = min(rank * per, len), count = min(per, len - begin);
-#pragma unroll 4
-  for (int i = tid; i < count; i += kThreads) run[i] = w[begin + i];
+  for (int base = tid; base < count; base += 8 * kThreads) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (base + e * kThreads < count) x[e] = w[begin + base + e * kThreads];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (base + e * kThreads < count) run[base + e * kThreads] = ordered(x[e]);
+  }
   const int older = len > p.keep ? len - p.recent : 0;      // the candidates; the rest stays
   const int mine = min(max(older - begin, 0), count);       // of them in this run
   uint32_t border = 0, need = len > p.keep ? p.keep - p.recent : 0;
@@ -83,7 +93,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
       for (int i = tid; i < kWarps * 257; i += kThreads) (&hist[0][0])[i] = 0;
       __syncthreads();
       for (int i = tid; i < mine; i += kThreads) {
-        const uint32_t u = ordered(run[i]);
+        const uint32_t u = run[i];
         // a histogram per warp: weights crowd into few digits
         if (pass == 0 || (u >> (shift + 8)) == prefix) atomicAdd(&hist[warp][(u >> shift) & 255], 1u);
       }
@@ -99,7 +109,8 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
         uint32_t n = s_total[pass & 1][tid];
         if (cluster > 1) {
           n = 0;
-          for (int r = 0; r < cluster; ++r) n += ld_cluster_u32(&s_total[pass & 1][tid], r);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) n += ld_cluster_u32(&s_total[pass & 1][tid], min(r, cluster - 1)) * (r < cluster ? 1u : 0u);
         }
         s_all[tid] = n;
       }
@@ -140,7 +151,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
     __syncthreads();
     uint32_t g = 0, q = 0;
     for (int i = tid; i < count; i += kThreads) {
-      const uint32_t u = ordered(run[i]);
+      const uint32_t u = run[i];
       g += above_border(i, u);
       q += at_border(i, u);
     }
@@ -151,9 +162,10 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
       atomicAdd(&s_count[1], q);
     }
     cluster_sync_all();
-    for (int r = 0; r < rank; ++r) {
-      above += ld_cluster_u32(&s_count[0], r);
-      equal += ld_cluster_u32(&s_count[1], r);
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      above += ld_cluster_u32(&s_count[0], min(r, rank)) * (r < rank ? 1u : 0u);
+      equal += ld_cluster_u32(&s_count[1], min(r, rank)) * (r < rank ? 1u : 0u);
     }
   } else {
     __syncthreads();
@@ -161,16 +173,20 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
   // In order: above the border stays, of those at it the first `need`.  Every weight of the head is in shared memory by
   // now, so w_out may be w.
   for (int base = 0, step = 0; base < count; base += kThreads * kPer, ++step) {
-    float x[kPer];
+    uint32_t x[kPer];
     uint32_t gt = 0, eq = 0;                                // bits
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4) {
+      const int i = base + tid * kPer + e;                  // runs are padded to kPer
+      const uint4 v = i < count ? *reinterpret_cast<const uint4*>(run + i) : make_uint4(0u, 0u, 0u, 0u);
+      x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+    }
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int i = base + tid * kPer + e;
-      x[e] = i < count ? run[i] : 0.f;
       if (i < count) {
-        const uint32_t u = ordered(x[e]);
-        if (above_border(i, u)) gt |= 1u << e;
-        if (at_border(i, u)) eq |= 1u << e;
+        if (above_border(i, x[e])) gt |= 1u << e;
+        if (at_border(i, x[e])) eq |= 1u << e;
       }
     }
     uint2 sum = make_uint2(__popc(gt), __popc(eq));
@@ -197,7 +213,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
       if (is_gt || (is_eq && q < need)) {
         const uint32_t at = g + min(q, need);
         index[at] = begin + base + tid * kPer + e;
-        w_out[at] = x[e];
+        w_out[at] = weight_of(x[e]);
       }
       g += is_gt;
       q += is_eq;
