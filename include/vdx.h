@@ -355,8 +355,9 @@ typedef struct vdx_kv8_scales {
 vdx_status vdx_rope3d_append8(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_append_args* args, void* stream);
 
 /* vdx_paged_attn_offset over such a cache.  Codes and scales enter the products as the values they stand for; the
- * softmax weights are rounded to fp16 after a multiplication by 2^7 (weights below 2^-21 of a row's
- * largest lose bits, below 2^-32 they vanish) where a kv head has at most 32 rows, else to the call's type. */
+ * softmax weights are rounded to fp16 after a multiplication by 2^7 (weights below 2^-21 of a row's largest lose
+ * bits, below 2^-32 they vanish).  Queries of bf16 are taken as fp16 times a power of two of the row's own: what lies below
+ * 2^-29 of a row's largest loses bits. */
 vdx_status vdx_paged_attn8(const vdx_paged_kv* cache, const vdx_kv8_scales* scales, const vdx_paged_attn_args* args,
                            const int32_t* pos_offset, void* stream);
 /* 0 also where the call would be refused: vdx_last_error() is not empty then. */
@@ -397,7 +398,7 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* cache, const vdx_kv8_scale
 /* Eviction: of every sequence's L = kv_len[s] keys at most `keep` stay, for each kv head its own.  Where L > keep
  * these are the last `recent` and, of the others, the keep - recent with the largest w (of equals the one with
  * the lowest index; NaN counts as the largest); otherwise all.  Keys and values of a head that stay move, in their order,
- * to cache indices 0, 1, .. of the same sequence of `into`: the same kind of cache by another page table, and
+ * to cache indices 0, 1, .. of the same sequence of `into`: the same kind of cache by another page table, no page twice, and
  * possibly in the same pools, whose pages the call must not read too (the old pages are free afterwards).  In 8 bits the
  * blocks of `into` get scales by the rule of vdx_rope3d_append8, as if the values were appended at once.
  * Written beside: kv_len_out[s] = min(L, keep); pos_offset_out[s] = pos_offset[s] + L - kv_len_out[s] (NULL: not

