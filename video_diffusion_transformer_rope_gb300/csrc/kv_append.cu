@@ -253,13 +253,11 @@ kv_append(const __grid_constant__ AppendParams p) {
 // does that too, so nothing is shared between warps.
 //
 // Bound: DRAM, and nearly the issue slots (the rows are worked out twice, kv_append's once): 21600 tokens of 3 x 40 heads,
-// 1.11 GB, 233 us, 4.75 TB/s, 71 % of a plain copy's rate; queries by fours of tokens (by twos 259 us).
+// 1.11 GB, 233 us, 4.75 TB/s, 71 % of a plain copy's rate.
 //
-// A thread block takes the blocks ("segments") of the cache whose first new token is among its kRows8 rows, for keys or
-// values; a segment may reach up to 15 rows further.  One warp looks up those 31 rows, one to a lane.
-constexpr int kRows8 = 16;
+// A thread block takes the blocks ("segments") of the cache whose first new token is among its kRows (16 or fewer) rows,
+// for keys or values; a segment may reach up to 15 rows further.  One warp looks up those rows, one to a lane.
 constexpr int kResident8 = 7;
-constexpr int kWindow8 = kRows8 + kBlock8 - 1;
 
 // The 8 channels of a lane as pairs of pairs: even channels (0, 2), (4, 6), odd channels (1, 3), (5, 7), so that the turn of
 // two channel pairs is two packed instructions for each of their channels.
@@ -316,23 +314,25 @@ __device__ __forceinline__ int find_sequence_lane(const int* cu, int S, int r) {
   return lo;
 }
 
-template <typename T, int D, bool kKeys>
+template <typename T, int D, bool kKeys, int kRows>
 __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int nx, int by, int ny) {
   constexpr int kLanes = D / 8;                  // of a row
   constexpr int kPer = 32 / kLanes;              // rows of a warp's step
   constexpr int kSteps = kBlock8 / kPer;
-  __shared__ __align__(16) float s_cos[kKeys ? kWindow8 : 1][D / 2], s_sin[kKeys ? kWindow8 : 1][D / 2];
-  __shared__ Segment8 segs[kRows8];
-  __shared__ int s_axis[kWindow8][3];
+  constexpr int kWindow = kRows + kBlock8 - 1;
+  static_assert(kWindow <= 32, "a lane looks up a row");
+  __shared__ __align__(16) float s_cos[kKeys ? kWindow : 1][D / 2], s_sin[kKeys ? kWindow : 1][D / 2];
+  __shared__ Segment8 segs[kRows];
+  __shared__ int s_axis[kWindow][3];
   __shared__ int s_count;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = bx * kRows8;
+  const int row0 = bx * kRows;
 
   if (warp == 0) {
     const int r = row0 + lane;
     int seq = 0, begin = 0, end = 0, slot = 0, page = -1, axis[3] = {0, 0, 0};
     bool mine = false, fits = false, bad_page = false, bad_position = false;
-    if (lane < kWindow8 && r < p.rows) {
+    if (lane < kWindow && r < p.rows) {
       seq = find_sequence_lane(p.cu, p.S, r);
       begin = load_i32(p.cu + seq);
       end = load_i32(p.cu + seq + 1);
@@ -360,13 +360,13 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
         }
       }
     }
-    if (lane < kRows8 && (bad_page || bad_position)) atomicOr(&g_error_word, (bad_page ? kErrPage : 0u) | (bad_position ? kErrPosition : 0u));
-    if (lane < kWindow8)
+    if (lane < kRows && (bad_page || bad_position)) atomicOr(&g_error_word, (bad_page ? kErrPage : 0u) | (bad_position ? kErrPosition : 0u));
+    if (lane < kWindow)
 #pragma unroll
       for (int i = 0; i < 3; ++i) s_axis[lane][i] = axis[i];
     const unsigned placed = __ballot_sync(0xffffffffu, fits);
     // a segment starts with its sequence's first new row or a block's first token (so does index 0, whatever is before it)
-    const bool leads = mine && lane < kRows8 && !bad_page && (slot % kBlock8 == 0 || r == begin);
+    const bool leads = mine && lane < kRows && !bad_page && (slot % kBlock8 == 0 || r == begin);
     const unsigned all = __ballot_sync(0xffffffffu, leads);
     if (leads) {
       Segment8& g = segs[__popc(all & ((1u << lane) - 1))];
@@ -432,7 +432,7 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
           odd[c] = fmul2(odd[c], w_odd[c]);
         }
       }
-      const int j = min(g.row + i * kPer + sub, kWindow8 - 1);
+      const int j = min(g.row + i * kPer + sub, kWindow - 1);
       const float4 cn = *reinterpret_cast<const float4*>(&s_cos[j][ch * 4]), sn = *reinterpret_cast<const float4*>(&s_sin[j][ch * 4]);
       const uint64_t c2[2] = {f32x2(cn.x, cn.y), f32x2(cn.z, cn.w)}, s2[2] = {f32x2(sn.x, sn.y), f32x2(sn.z, sn.w)};
       const uint64_t n2[2] = {f32x2(-sn.x, -sn.y), f32x2(-sn.z, -sn.w)};
@@ -446,6 +446,7 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
+      if (i * kPer >= g.count) break;                   // a single token fills one row in 16
       uint64_t even[2], odd[2];
       unpack_pairs<T>(x[i], even, odd);
       float scale = 1.f;
@@ -481,6 +482,7 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
     }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
+      if (i * kPer >= g.count) break;
       const int j = i * kPer + sub;
       asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));      // worked out anew, not held
       uint64_t even[2], odd[2];
@@ -502,15 +504,15 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
 
 // The blocks of keys, which take longest, first; then those of values and of queries.  (Side by side, so that issue slots
 // and memory are wanted at the same time, 21600 tokens of 3 x 40 heads take 286 us, not 264.)
-template <typename T, int D, int kTok>
+template <typename T, int D, int kTok, int kRows>
 __global__ void __launch_bounds__(kThreads, kResident8)
 kv_append8(const __grid_constant__ AppendParams p, const int nx, const int ny, const int qx) {
   wait_for_earlier_work();
   const int b = blockIdx.x, each = nx * ny;
   if (b < each)
-    append_blocks<T, D, true>(p, b % nx, nx, b / nx, ny);
+    append_blocks<T, D, true, kRows>(p, b % nx, nx, b / nx, ny);
   else if (b < 2 * each)
-    append_blocks<T, D, false>(p, (b - each) % nx, nx, (b - each) / nx, ny);
+    append_blocks<T, D, false, kRows>(p, (b - each) % nx, nx, (b - each) / nx, ny);
   else
     append_rows<T, D, kTok, 0>(p, (b - 2 * each) % qx * kTok, (b - 2 * each) / qx, (gridDim.x - 2 * each) / qx);
 }
@@ -549,13 +551,13 @@ cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
   return pairs <= static_cast<long long>(kResident) * sms ? launch_tok<T, D, 2>(p, sms, stream) : launch_tok<T, D, 4>(p, sms, stream);
 }
 
-template <typename T, int D, int kTok>
+template <typename T, int D, int kTok, int kRows>
 cudaError_t launch8_tok(const AppendParams& p, int sms, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8), kWarps = kThreads / 32;
-  const int nx = (p.rows - 1) / kRows8 + 1, qx = p.Hq > 0 ? (p.rows - 1) / kTok + 1 : 0;
+  const int nx = (p.rows - 1) / kRows + 1, qx = p.Hq > 0 ? (p.rows - 1) / kTok + 1 : 0;
   // few rows: the heads over blocks too, as in launch_tok
   int ny = 1, qy = 1;
-  const int most = (p.Hkv * kRows8 + kWarps - 1) / kWarps, q_most = (kTok * p.Hq + kGroups - 1) / kGroups;
+  const int most = (p.Hkv * kRows + kWarps - 1) / kWarps, q_most = (kTok * p.Hq + kGroups - 1) / kGroups;
   while (ny < most && static_cast<long long>(nx) * ny < sms) ny *= 2;
   while (qy < q_most && static_cast<long long>(qx) * qy < 2ll * sms) qy *= 2;
   ny = ny < most ? ny : most;
@@ -569,11 +571,19 @@ cudaError_t launch8_tok(const AppendParams& p, int sms, cudaStream_t stream) {
   cudaLaunchAttribute attr = launch_early();
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_append8<T, D, kTok>, p, nx, ny, qx);
+  return cudaLaunchKernelEx(&cfg, kv_append8<T, D, kTok, kRows>, p, nx, ny, qx);
 }
 template <typename T, int D>
 cudaError_t launch8(const AppendParams& p, int sms, cudaStream_t stream) {
-  return p.rows <= 1024 ? launch8_tok<T, D, 2>(p, sms, stream) : launch8_tok<T, D, 4>(p, sms, stream);
+  // Few rows: blocks of 4 rows, which have fewer angles to work out one after the other; but of a chunk one in four of them has
+  // a segment.  us with 4 and 16 rows to a block, single tokens of many sequences | one sequence's chunk, d = 128:
+  //   kv heads   48 tokens                 256 tokens                 512 tokens
+  //      8       4.9   6.2 | 7.3   8.7      7.1   9.4 |  9.3  10.0     9.9  12.5 | 10.0  10.4
+  //     12       5.1   6.7 | 7.7   9.2      7.7  10.2 |  8.9   9.6    12.3  14.6 | 13.3  10.2
+  //     40       7.2   8.5 | 8.0   9.4     17.2  20.0 | 17.0  13.4    31.1  33.5 | 27.1  17.0
+  if (static_cast<long long>(p.rows) * p.Hkv <= 4096) return launch8_tok<T, D, 2, 4>(p, sms, stream);
+  // queries by two tokens as in launch while there are few (21600 tokens by fours: 233, by twos 259 us)
+  return p.rows <= 1024 ? launch8_tok<T, D, 2, 16>(p, sms, stream) : launch8_tok<T, D, 4, 16>(p, sms, stream);
 }
 
 }  // namespace
