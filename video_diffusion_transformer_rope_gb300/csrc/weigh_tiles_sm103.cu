@@ -11,9 +11,10 @@
 // threads that own them put them into tensor memory, 8-bit codes as T, exactly.
 //
 // Bound: the tensor cores and the exponentials together (a 128 x 128 tile at d = 128 is 512 cycles of either).  1560
-// tokens of 2 x 12 heads over 31200 keys, a causal block each: 304 us, 1030 TFLOP/s, the exponential units 43 % busy; what it
-// waits for is the way from a product to its weighers and back over three S tiles.  Eight weighing warps of whole rows take 335
-// to 349 us, loads of 64 columns 376, the odd tiles' warps writing keys 312 to 318, a register split of 104 and 64 363.
+// tokens of 2 x 12 heads over 31200 keys, a causal block each: 287 us, 1090 TFLOP/s, the exponential units 46 % busy; what it
+// waits for is the way from a product to its weighers and back over three S tiles.  While masked and whole tiles shared a loop
+// it was 304 us; from there eight weighing warps of whole rows took 335 to 349 us, loads of 64 columns 376, the odd tiles'
+// warps writing keys 312 to 318, a register split of 104 and 64 363, a unit's Q tiles over clusters of two 429.
 //
 // A unit is (sequence, kv head, 256 keys); a block per multiprocessor takes every gridDim-th of them.
 //   warps 0-15       exponentials and sums (thread = key = TMEM lane): four warps to a key tile and every other Q tile,
@@ -396,20 +397,27 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
           const uint32_t ts = tmem + lanes + 128 + buf * 128, nl = smem_addr(&ctl->nl[slot][0]);
           const bool whole = cols == row_tile && clear <= t * row_tile;
           uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          auto free_s = [&] {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl->s_empty[buf]));
+          };
+          if (whole) {
 #pragma unroll 1
-          for (int ch = 0; ch < kRowTile; ch += 32) {
-            if (ch >= cols) continue;                    // not read: free already
-            uint32_t s[32];
-            tmem_ld32(ts + ch, s);
-            if (ch + 32 >= cols) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(&ctl->s_empty[buf]));
-            }
-            if (whole)
+            for (int ch = 0; ch < row_tile; ch += 32) {
+              uint32_t s[32];
+              tmem_ld32(ts + ch, s);
+              if (ch + 32 >= row_tile) free_s();
               weigh32<false>(s, nl + ch * 4, p.scale_log2, 0, 32, acc);
-            else
+            }
+          } else {
+#pragma unroll 1
+            for (int ch = 0; ch < cols; ch += 32) {
+              uint32_t s[32];
+              tmem_ld32(ts + ch, s);
+              if (ch + 32 >= cols) free_s();
               weigh32<true>(s, nl + ch * 4, p.scale_log2, lo - ch, cols - ch, acc);
+            }
           }
           float a, b;
           f32x2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
