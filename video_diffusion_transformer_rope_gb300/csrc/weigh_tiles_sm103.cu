@@ -19,8 +19,9 @@
 // A unit is (sequence, kv head, 256 keys); a block per multiprocessor takes every gridDim-th of them.
 //   warps 0-15       exponentials and sums (thread = key = TMEM lane): four warps to a key tile and every other Q tile,
 //                    the pairs of them added at the end; the first eight also put the keys into tensor memory
-//   warp 16          TMA producer of the Q ring          warp 17  issues the products
-//   warp 18          -lse*log2(e) of a Q tile's rows     warp 19  copies keys
+//   warp 16          TMA producer of the Q ring; copies half of the keys of units of few Q tiles
+//   warp 17          issues the products                 warp 18  -lse*log2(e) of a Q tile's rows
+//   warp 19          copies keys
 // TMEM (512 columns): the keys of both tiles at 0 and 64, three S tiles at 128, 256 and 384, used in turn; a tile is
 // free as soon as its scores are in registers.
 #include <cstdint>
@@ -163,7 +164,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       mbar_init(smem_addr(&ctl->part_full[i]), kKeys);
       mbar_init(smem_addr(&ctl->part_empty[i]), kKeys);
     }
-    mbar_init(smem_addr(&ctl->loaded), 1);
+    mbar_init(smem_addr(&ctl->loaded), 2);
     mbar_init(smem_addr(&ctl->taken), 8);
     for (int i = 0; i < 4 * kSBufs; ++i) mbar_init(smem_addr(&ctl->s_full[0][i]), 1);
     for (int i = 0; i < kSBufs; ++i) mbar_init(smem_addr(&ctl->s_empty[i]), 4);
@@ -195,12 +196,53 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
   auto first = [&](int it, bool report = false) { return next_unit(p, it, units, blocks, row_tile, report); };
   const int stride = gridDim.x;
 
+  // Keys `from` .. of every `step`, 32 each, of a unit to shared memory, by one warp.
+  auto copy_keys = [&](const Unit& u, int from, int step) {
+    const int* table = p.table + u.s * p.table_stride;
+    const uint8_t* base = static_cast<const uint8_t*>(p.k) + u.hk * p.k_h * kElem;
+#pragma unroll 1
+    for (int r0 = from; r0 < u.keys; r0 += step) {
+      // a lane looks up a key; kLanes lanes copy its row
+      const int c = u.key0 + r0 + lane, pg = c / p.P, slot = c - pg * p.P;
+      long long at = -1;                               // zeros
+      int e = 0;
+      if (c < u.sq.len) {
+        const int page = load_i32(table + pg);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
+          at = (page * p.k_p + slot * p.k_t) * kElem;
+          if (k8) e = scale_exponent(p.scales.k[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block + u.hk * p.scales.k_head]);
+        } else {
+          atomicOr(&g_error_word, kErrPage);
+        }
+      }
+      if (k8) ctl->exponent[r0 + lane] = static_cast<int8_t>(e);
+      const int ch = lane % kLanes;
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const int r = i * (32 / kLanes) + lane / kLanes;
+        const long long row = __shfl_sync(0xffffffffu, at, r);
+        copy16(key_chunk(r0 + r, ch), base + max(row, 0ll) + ch * 16, row >= 0);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&ctl->loaded));
+  };
+  auto short_unit = [&](const Unit& u) { return u.t1 - u.t0 <= kS; };
+
   if (warp == 16) {
     // -------------------------------------------------------------------- Q tiles
     if (lane == 0) tma_prefetch_desc(&tm_q);
-    int n = 0;
+    int n = 0, loads = 0;
     bool ok = true;
     for (Unit u = first(blockIdx.x, lane == 0); ok && u.it < units; u = first(u.it + stride, lane == 0)) {
+      if (u.t0 == u.t1) continue;
+      // A warp's copies are ~3 bytes a clock.  The keys of a unit whose Q tiles are all under way at once would be waited for: this
+      // warp copies half of them (12 heads of 30 tokens over 35 thousand keys of 3 sequences 70 -> 53 us; of all units' keys, a
+      // 480p frame takes 293 us, not 287).  Of others it says that it has none to copy: who waits for `taken` sees every phase.
+      if (loads > 0 && !(ok = wait(&ctl->taken, loads - 1, kSiteTaken))) break;
+      ++loads;
+      copy_keys(u, short_unit(u) ? 32 : u.keys, 64);
       for (int t = u.t0; t < u.t1; ++t, ++n) {
         const int st = n % kS;
         if (n >= kS && !(ok = wait(&ctl->q_empty[st], n / kS - 1, kSiteQEmpty))) break;
@@ -296,35 +338,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
     for (Unit u = first(blockIdx.x); ok && u.it < units; u = first(u.it + stride)) {
       if (u.t0 == u.t1) continue;
       if (n > 0 && !(ok = wait(&ctl->taken, n - 1, kSiteTaken))) break;
-      const int* table = p.table + u.s * p.table_stride;
-      const uint8_t* base = static_cast<const uint8_t*>(p.k) + u.hk * p.k_h * kElem;
-#pragma unroll 1
-      for (int r0 = 0; r0 < u.keys; r0 += 32) {
-        // a lane looks up a key; kLanes lanes copy its row
-        const int c = u.key0 + r0 + lane, pg = c / p.P, slot = c - pg * p.P;
-        long long at = -1;                               // zeros
-        int e = 0;
-        if (c < u.sq.len) {
-          const int page = load_i32(table + pg);
-          if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
-            at = (page * p.k_p + slot * p.k_t) * kElem;
-            if (k8) e = scale_exponent(p.scales.k[page * p.scales.k_page + slot / kBlock8 * p.scales.k_block + u.hk * p.scales.k_head]);
-          } else {
-            atomicOr(&g_error_word, kErrPage);
-          }
-        }
-        if (k8) ctl->exponent[r0 + lane] = static_cast<int8_t>(e);
-        const int ch = lane % kLanes;
-#pragma unroll 4
-        for (int i = 0; i < kLanes; ++i) {
-          const int r = i * (32 / kLanes) + lane / kLanes;
-          const long long from = __shfl_sync(0xffffffffu, at, r);
-          copy16(key_chunk(r0 + r, ch), base + max(from, 0ll) + ch * 16, from >= 0);
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&ctl->loaded));
+      copy_keys(u, 0, short_unit(u) ? 64 : 32);
       ++n;
     }
     __syncwarp();
