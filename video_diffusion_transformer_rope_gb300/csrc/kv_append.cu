@@ -314,6 +314,19 @@ __device__ __forceinline__ int find_sequence_lane(const int* cu, int S, int r) {
   return lo;
 }
 
+// cos_sin with the angle reduced to an eighth of a turn before it becomes a float: within 2^-28 turns, not 2^-26.  A code has 4
+// bits, and a value that rounds to its neighbour is off by an eighth of itself, so here each bit of the angle halves
+// the number of codes that differ from those of exact keys.
+__device__ __forceinline__ float2 cos_sin8(const AppendParams& p, int pr, unsigned x) {
+  const unsigned long long frac = static_cast<unsigned long long>(x) * p.turn[pr];       // turns * 2^64
+  const unsigned quarter = static_cast<unsigned>((frac + (1ull << 61)) >> 62);
+  const int rest = static_cast<int>(static_cast<long long>(frac - (static_cast<unsigned long long>(quarter) << 62)) >> 30);     // [-1/8, 1/8] turns * 2^34
+  float sn, cn;
+  sincospif(static_cast<float>(rest) * 0x1p-33f, &sn, &cn);
+  const float a = quarter & 1 ? sn : cn, b = quarter & 1 ? cn : sn;
+  return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
+}
+
 template <typename T, int D, bool kKeys, int kRows>
 __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int nx, int by, int ny) {
   constexpr int kLanes = D / 8;                  // of a row
@@ -389,7 +402,7 @@ __device__ __forceinline__ void append_blocks(const AppendParams& p, int bx, int
     const int from = segs[0].row, to = segs[count - 1].row + segs[count - 1].count;
     for (int i = from * (D / 2) + tid; i < to * (D / 2); i += kThreads) {
       const int j = i / (D / 2), pr = i % (D / 2);
-      const float2 t = cos_sin(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
+      const float2 t = cos_sin8(p, pr, static_cast<unsigned>(s_axis[j][pr < p.half_t ? 0 : (pr < p.half_t + p.half_h ? 1 : 2)]));
       s_cos[j][pr] = t.x;
       s_sin[j][pr] = t.y;
     }
