@@ -1,4 +1,4 @@
-// Argument checks shared by the C-ABI front ends of the paged-cache calls (kv_capi.cu, kv8_capi.cu): messages,
+// Argument checks shared by the C-ABI front ends of the paged-cache calls (kv_capi.cu, kv_evict_capi.cu): messages,
 // strided tensors, and what may lie over what.  Host code; nothing here touches the device.
 #pragma once
 #include <algorithm>

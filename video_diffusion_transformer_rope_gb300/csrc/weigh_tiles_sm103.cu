@@ -11,7 +11,7 @@
 // threads that own them put them into tensor memory, 8-bit codes as T, exactly.
 //
 // Bound: the tensor cores and the exponentials together (a 128 x 128 tile at d = 128 is 512 cycles of either).  1560
-// tokens of 2 x 12 heads over 31200 keys, a causal block each: 287 us, 1090 TFLOP/s, the exponential units 46 % busy; what it
+// tokens of 2 x 12 heads over 32760 keys, a causal block each: 287 us, 1090 TFLOP/s, the exponential units 46 % busy; what it
 // waits for is the way from a product to its weighers and back over three S tiles.  While masked and whole tiles shared a loop
 // it was 304 us; from there eight weighing warps of whole rows took 335 to 349 us, loads of 64 columns 376, the odd tiles'
 // warps writing keys 312 to 318, a register split of 104 and 64 363, a unit's Q tiles over clusters of two 429.
