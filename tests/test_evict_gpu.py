@@ -43,6 +43,13 @@ WEIGH = [
 ]
 
 
+# more units of 256 keys than multiprocessors, of no, few and many query tiles one after another in a block
+WEIGH += [
+    ("bf16", 128, 8, 8, 64, [600, 40, 0, 1200, 130, 33], [1500, 1490, 700, 1290, 1025, 1501], 1, 1.0),
+    ("fp16", 64, 12, 6, 16, [33, 700, 40, 1, 90, 1030], [1280, 1100, 1, 257, 1800, 1030], 50, 0.75),
+]
+
+
 @pytest.mark.parametrize("case", WEIGH, ids=lambda c: f"{c[0]}-d{c[1]}-{c[2]}over{c[3]}-page{c[4]}-{max(c[5])}of{max(c[6])}-block{c[7]}")
 @pytest.mark.parametrize("bits", [16, 8])
 def test_gathered_weights_match_the_formula(case, bits):

@@ -110,6 +110,29 @@ def test_append_matches_the_definition(dtype, d, Hq, Hkv, page, news, ctxs, grid
     assert torch.equal(c.k_scale.view(torch.uint8)[~scaled], before.k_scale.view(torch.uint8)[~scaled])
 
 
+@pytest.mark.parametrize("dtype,d,norm", [("bf16", 128, True), ("fp16", 64, False)])
+def test_a_chunk_and_its_pieces_give_the_same_bits(dtype, d, norm):
+    # blocks that are appended whole have one scale, however many tokens the call has beside them
+    dt, H, n = DT[dtype], 12, 1104
+    q, k, v = (_rand((n, H, d), dt, 60 + i) for i in range(3))
+    w = (1 + 0.1 * _rand((d,), torch.float32, 63)).to(dt) if norm else None
+    got = []
+    for pieces in ([1104], [800, 304], [320, 320, 320, 144], [16] * 69):
+        c = Paged8(d, H, 128, [0], seed=1, width=9)
+        c.k, c.v = (torch.zeros(9, 128, H, d, dtype=torch.uint8, device="cuda").view(c.k.dtype) for _ in range(2))
+        c.k_scale, c.v_scale = (torch.zeros(9, 8, H, dtype=torch.uint8, device="cuda").view(c.k_scale.dtype) for _ in range(2))
+        c.table = torch.arange(9, dtype=torch.int32, device="cuda").view(1, 9)
+        at, qs = 0, []
+        for m in pieces:
+            kv_len = torch.tensor([at + m], dtype=torch.int32, device="cuda")
+            qs.append(vdx.rope3d_append(q[at:at + m], k[at:at + m], v[at:at + m], c.cache(vdx), cu_of([m]), kv_len, (99, 6, 7), q_norm=w, k_norm=w))
+            at += m
+        vdx.sync_check()
+        got.append([torch.cat(qs)] + [x.view(torch.uint8) for x in (c.k, c.v, c.k_scale, c.v_scale)])
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64)])
 def test_a_scale_grows_and_older_codes_are_rounded_again(dtype, d):
     # one token at a time, each larger than the one before; then smaller ones, which leave the scale alone
