@@ -235,6 +235,29 @@ def test_eviction_matches_the_definition(case, bits, kind):
     _check_evicted(got, into, before, c, kept_w, lens, keep, recent, bits, offset)
 
 
+@pytest.mark.parametrize("L", [120, 9000])
+@pytest.mark.parametrize("keep", [30, 31, 60, 90])
+def test_borders_between_groups_of_alike_weights(L, keep):
+    # quarters of the keys far apart, near each other and the least that there are: where the border falls between groups that
+    # share their upper bits, inside one, and among equals
+    d, H, dt = 64, 3, torch.bfloat16
+    c, cache, _ = _cache(16, dt, d, H, 64, [L], 91)
+    keep = keep * L // 120
+    into, into_cache, _ = _into(16, dt, d, H, 64, [L], keep, 92)
+    before = Paged.__new__(Paged)
+    before.__dict__.update(into.__dict__)
+    before.k, before.v = into.k.clone(), into.v.clone()
+    group = torch.randperm(L, generator=torch.Generator().manual_seed(93)).cuda() % 4
+    rest = torch.rand(1, H, L, generator=torch.Generator(device="cuda").manual_seed(94), device="cuda")
+    w = torch.empty(1, H, L, device="cuda")
+    w[:, 0] = torch.tensor([-math.inf, 2.0 ** -60, 1.0, 2.0 ** 60], device="cuda")[group] * (1 + 0.9 * rest[:, 0])
+    w[:, 1] = 1 + group * 2.0 ** -7 + rest[:, 1] * 2.0 ** -9
+    w[:, 2] = torch.tensor([-math.inf, -math.inf, -0.0, 5.0], device="cuda")[group]
+    got = vdx.paged_evict(cache, w, c.kv_len, keep, into_cache)
+    vdx.sync_check()
+    _check_evicted(got, into, before, c, w, [L], keep, 0, 16, [0])
+
+
 def test_eviction_in_one_pool_with_weights_in_place_and_on_a_side_stream():
     bits, dt, d, H, page, lens, keep = 8, torch.bfloat16, 128, 2, 16, [5000, 300, 60], 130
     c = Paged8(d, H, page, lens, seed=91, spare=30, width=320)

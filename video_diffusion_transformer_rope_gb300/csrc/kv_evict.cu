@@ -4,9 +4,9 @@
 // evict_select, a cluster of up to 8 blocks per (sequence, head), a run of the weights in each one's shared memory: of the
 // first L - recent weights the `need` largest, of equals the lowest indices.  The border is found digit by digit (8 bits
 // of the weights as ordered integers, from the top: a histogram of those that share the digits so far, summed over the
-// blocks, then the digit that holds the need-th largest), then one walk in order writes index and weights of what
+// blocks, then the digit that holds the need-th largest; no further one where all that share the digits so far stay), then one walk in order writes index and weights of what
 // stays; a key's place is the number of keys above the border before it and of those equal to it, up to the last that fits.
-// Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 43 us).
+// Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 39 us).
 //
 // evict_move, a warp per (16 slots of a page, head): rows of 16 keys and values, found through the index and the old
 // page table, 16 bytes a lane; in 8 bits their largest value gives the new scale first.  Bound by DRAM: what stays is read
@@ -51,7 +51,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
   extern __shared__ __align__(16) uint32_t run[];          // this block's weights, as ordered integers
   __shared__ uint32_t hist[kWarps][256 + 1];
   __shared__ uint32_t s_total[2][256], s_all[256], s_count[2];
-  __shared__ uint32_t s_prefix, s_need;
+  __shared__ uint32_t s_prefix, s_need, s_whole;
   __shared__ uint2 s_sum[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -88,6 +88,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
   uint32_t border = 0, need = len > p.keep ? p.keep - p.recent : 0;
   if (need > 0) {
     uint32_t prefix = 0;
+#pragma unroll
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
       for (int i = tid; i < kWarps * 257; i += kThreads) (&hist[0][0])[i] = 0;
@@ -132,6 +133,7 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
           if (before < need && need <= before + n[i]) {
             s_prefix = (prefix << 8) | static_cast<uint32_t>(255 - (lane * 8 + i));
             s_need = need - before;
+            s_whole = need - before == n[i];
           }
           before += n[i];
         }
@@ -139,8 +141,9 @@ evict_select(const __grid_constant__ EvictParams p, const int cluster) {
       __syncthreads();
       prefix = s_prefix;
       need = s_need;                                        // of the weights that share these digits
+      border = prefix << shift;
+      if (s_whole) break;                                   // all of them stay: no digit further down matters
     }
-    border = prefix;
   }
   auto above_border = [&](int i, uint32_t u) { return i >= mine || (need > 0 && u > border); };
   auto at_border = [&](int i, uint32_t u) { return i < mine && need > 0 && u == border; };
