@@ -4,8 +4,9 @@
 // evict_select, a cluster of up to 8 blocks per (sequence, head), a run of the weights in each one's shared memory: of the
 // first L - recent weights the `need` largest, of equals the lowest indices.  The border is found digit by digit (8 bits
 // of the weights as ordered integers, from the top: a histogram of those that share the digits so far, summed over the
-// blocks, then the digit that holds the need-th largest; no further one where all that share the digits so far stay), then one walk in order writes index and weights of what
-// stays; a key's place is the number of keys above the border before it and of those equal to it, up to the last that fits.
+// blocks, then the digit that holds the need-th largest; no further one where all that share the digits so far stay), then
+// one walk in order writes index and weights of what stays; a key's place is the number of keys above the border before it
+// and of those equal to it, up to the last that fits.
 // Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 39 us).
 //
 // evict_move, a warp per (16 slots of a page, head): rows of 16 keys and values, found through the index and the old
