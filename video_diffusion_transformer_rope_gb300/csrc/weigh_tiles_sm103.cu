@@ -64,11 +64,13 @@ struct Ctl {
   // S tiles for each of the four groups of warps that weigh, by its own count: a group does not see every use of an S buffer,
   // and it may have as many tiles waiting as there are buffers.
   uint64_t s_full[4][kSBufs], s_empty[kSBufs];
-  uint64_t l_full[kLseSlots], l_empty[kLseSlots];
+  // Rows' lse for the warps of the even and of the odd Q tiles apart, by their own counts: in units of one Q tile the odd
+  // ones wait for nothing, so of barriers that they shared they could miss more than one phase.
+  uint64_t l_full[2][kLseSlots], l_empty[2][kLseSlots];
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float nl[kLseSlots][kRowTile];
+  alignas(16) float nl[2][kLseSlots][kRowTile];
   float part[2][kKeys];
   int8_t exponent[2 * kKeys];
 };
@@ -168,9 +170,9 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
     mbar_init(smem_addr(&ctl->taken), 8);
     for (int i = 0; i < 4 * kSBufs; ++i) mbar_init(smem_addr(&ctl->s_full[0][i]), 1);
     for (int i = 0; i < kSBufs; ++i) mbar_init(smem_addr(&ctl->s_empty[i]), 4);
-    for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(smem_addr(&ctl->l_full[i]), 1);
-      mbar_init(smem_addr(&ctl->l_empty[i]), 8);
+    for (int i = 0; i < 2 * kLseSlots; ++i) {
+      mbar_init(smem_addr(&ctl->l_full[0][i]), 1);
+      mbar_init(smem_addr(&ctl->l_empty[0][i]), 8);
     }
     mbar_init(smem_addr(&ctl->done), 1);
     ctl->abort_flag = 0;
@@ -298,7 +300,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
   } else if (warp == 18) {
     // -------------------------------------------------------------------- lse of the rows
     constexpr int kPer = kRowTile / 32;
-    int n = 0;
+    int evens = 0, odds = 0;                             // Q tiles so far
     bool ok = true;
     long long at[kPer];                                  // where this lane's rows of a head's first tile lie
 #pragma unroll
@@ -317,17 +319,17 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
         }
       };
       load(u.t0, ahead);
-      for (int t = u.t0; t < u.t1; ++t, ++n) {
-        const int slot = n % kLseSlots;
+      for (int t = u.t0; t < u.t1; ++t) {
+        const int odd = (t - u.t0) & 1, n = odd ? odds++ : evens++, slot = n % kLseSlots;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) v[i] = ahead[i];
         if (t + 1 < u.t1) load(t + 1, ahead);
-        if (n >= kLseSlots && !(ok = wait(&ctl->l_empty[slot], n / kLseSlots - 1, kSiteLseEmpty))) break;
+        if (n >= kLseSlots && !(ok = wait(&ctl->l_empty[odd][slot], n / kLseSlots - 1, kSiteLseEmpty))) break;
         // a row that saw no key weighs 2^-inf = 0
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) ctl->nl[slot][i * 32 + lane] = v[i] == -INFINITY ? -INFINITY : v[i] * -1.4426950408889634f;
+        for (int i = 0; i < kPer; ++i) ctl->nl[odd][slot][i * 32 + lane] = v[i] == -INFINITY ? -INFINITY : v[i] * -1.4426950408889634f;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_full[slot]));
+        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_full[odd][slot]));
       }
     }
     __syncwarp();
@@ -347,7 +349,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
     const int x = (warp >> 2) & 1, half = warp >> 3;     // key tile; every other Q tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    int n = 0, seq = 0, weighed = 0, parts = 0;
+    int n = 0, seq = 0, weighed = 0, parts = 0;          // n: this half's Q tiles
     int loads = 0, writes = 0;                           // units, units whose keys this tile has
     bool ok = true;
     // 32 columns are 64 channels
@@ -398,17 +400,17 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
       const int clear = __reduce_max_sync(0xffffffffu, from);
       const int tiles = u.has(1) ? 2 : 1;
       float total = 0.f;
-      for (int t = u.t0; t < u.t1; ++t, ++n, seq += tiles) {
+      for (int t = u.t0; t < u.t1; ++t, seq += tiles) {
         if (((t - u.t0) & 1) != half) continue;
         const int slot = n % kLseSlots;
-        if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
+        if (!(ok = warp_wait_inline(smem_addr(&ctl->l_full[half][slot]), (n / kLseSlots) & 1, flag, kSiteLseFull))) break;
         if (u.has(x)) {
           const int buf = (seq + x) % kSBufs;
           if (!(ok = warp_wait_inline(smem_addr(&ctl->s_full[x + 2 * half][weighed % kSBufs]), (weighed / kSBufs) & 1, flag, kSiteSFull))) break;
           tc_fence_after_sync();
           ++weighed;
           const int cols = min(row_tile, u.rows - t * row_tile), lo = from - t * row_tile;
-          const uint32_t ts = tmem + lanes + 128 + buf * 128, nl = smem_addr(&ctl->nl[slot][0]);
+          const uint32_t ts = tmem + lanes + 128 + buf * 128, nl = smem_addr(&ctl->nl[half][slot][0]);
           const bool whole = cols == row_tile && clear <= t * row_tile;
           uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
           auto free_s = [&] {
@@ -438,7 +440,8 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
           total += a + b;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_empty[slot]));
+        if (lane == 0) mbar_arrive(smem_addr(&ctl->l_empty[half][slot]));
+        ++n;
       }
       if (!ok) break;
       const Unit next = first(u.it + stride);
