@@ -29,12 +29,14 @@
 //   warp 11          stores finished output tiles: one TMA store, or the live rows of a tile that
 //                    ends with its sequence
 //   warps 12-15      8-bit caches only, in warp 8's place: load codes and write them to the K and V rings
-//                    as the values they stand for (in fp16, as are Q, which they convert, and P times 2^7)
+//                    as the values they stand for (in fp16, as are Q, which they convert, and P times 2^7);
+//                    rank 1's relay passes their arrivals on with a release of cluster scope
 //
-// A 720p frame of 3600 tokens of 40 heads over 75600 keys in 8 bits takes 4.24 ms, 1310 TFLOP/s: the converters keep up
+// A 720p frame of 3600 tokens of 40 heads over 75600 keys in 8 bits takes 4.28 ms, 1300 TFLOP/s: the converters keep up
 // (waits for K and V are no more than in 16 bits), but leave the softmax 144 registers, so that a row comes in two halves and
 // its maximum and its weights read S twice; P is ready ~500 cycles later.  Whole rows with 184 or 192 registers spill
-// elsewhere: 4.47 and 4.63 ms; halves with 176: 4.53; 152 and 104: 4.43.
+// elsewhere: 4.47 and 4.63 ms; halves with 176: 4.53; 152 and 104: 4.43.  (Those with rank 1's converters telling rank 0
+// themselves at CTA scope, which took 4.24 ms but orders nothing between two CTAs.  A second relay, for K alone: 4.45.)
 //
 // TMEM (512 columns): S0, S1 at 0 and 128, O0, O1 at 256 and 384; P overwrites the first half of S
 // as packed 16-bit pairs and is the A operand of the second product.  Issue order per key tile j:
@@ -482,10 +484,10 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     // rank 0's full barriers also count one relayed arrival from rank 1, its P-ready and O-empty
     // barriers one arrival from each of rank 1's softmax warps
     const uint32_t full = leader ? 2 : 1, rows = leader ? 128 + 4 : 128;
-    const uint32_t landed = k8 ? 8 : full;              // K and V: both CTAs' converter warps instead of producer and relay
+    const uint32_t landed = k8 ? full + 3 : full;       // K and V: four converter warps instead of the producer, and the relay
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(smem_addr(&ctl->q_full[i]), k8 ? 1 : full);
-      mbar_init(smem_addr(&ctl->q_ready[i]), 8);
+      mbar_init(smem_addr(&ctl->q_ready[i]), landed);
       mbar_init(smem_addr(&ctl->q_scaled[i]), 4);
       mbar_init(smem_addr(&ctl->q_empty[i]), 1);
     }
@@ -535,10 +537,9 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     constexpr int kKLanes = D / 16, kKStep = 32 / kKLanes, kKLoads = 16 / kKStep;        // K: 16 keys a warp
     constexpr int kVLanes = D / 32, kVStep = 32 / kVLanes, kVLoads = 32 / kVStep;        // V: 32 keys, this CTA's channels
     const int cw = warp - 12;
-    // Both CTAs' converters arrive at rank 0, whose MMA warp waits for all of them.  What rank 1 wrote lies in its own
-    // shared memory, where the products read it, fenced against the async proxy by each lane: a release of CTA scope
-    // orders it before the arrival (of cluster scope it waits for every load in flight: 7.5 ms, not 6.2, for a 720p frame when this was the one change).
-    const uint32_t leader_ctl = mapa_shared(sCtl, 0);
+    // Converters arrive in their own CTA, each lane's writes fenced against the async proxy.  The products that rank 0 issues
+    // read rank 1's shared memory too, so rank 1's relay passes its arrivals on with a release of cluster scope.  (From
+    // here that would wait for every load in flight: 7.5 ms, not 6.2, for a 720p frame when this was the one change.)
     const int kc = lane % kKLanes, kr = lane / kKLanes, vc = lane % kVLanes, vr = lane / kVLanes;
     // Where this lane's codes of row r wait in a stage (in 128-byte rows of 64 channels: the upper part's row, where there
     // is one, else half of the row): within what the row's own lanes will write.
@@ -636,7 +637,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(sCtl + kBarQScaled + 8 * b);
-          mbar_arrive_remote_release(leader_ctl + kBarQReady + 8 * b);
+          mbar_arrive(sCtl + kBarQReady + 8 * b);
         }
       }
       if (!ok) break;
@@ -663,7 +664,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           expand_chunk<128>(kt + kc / 4 * Lo::kKPart, cw * 16 + i * kKStep + kr, kc % 4, x[i], __shfl_sync(0xffffffffu, sk, i * kKStep + kr));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarKFull + 8 * st);
+        if (lane == 0) mbar_arrive(sCtl + kBarKFull + 8 * st);
         if (t + 1 < t1) copy_values(kv + 1);
         copies_commit();
         if (!ok) break;
@@ -678,7 +679,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           expand_chunk<Lo::kVRow>(vt, cw * 32 + i * kVStep + vr, vc, x[i], __shfl_sync(0xffffffffu, sv, i * kVStep + vr));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_release(leader_ctl + kBarVFull + 8 * st);
+        if (lane == 0) mbar_arrive(sCtl + kBarVFull + 8 * st);
         ++kv;
       }
       if (!ok) break;
@@ -799,6 +800,8 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // the second Q tile's product with V that is still to be issued
       bool have = false, first = false, last = false;
       int st1 = 0;
+      // K, V and (8 bits) Q: rank 1's converters wrote their halves by plain stores, so the wait acquires at cluster scope
+      auto wait_tile = [&](uint32_t bar, int parity, int site) { return warp_wait<k8>(bar, parity & 1, sCtl + kOffAbort, site); };
       auto finish_second = [&]() {                        // O1 += P1 V of the key tile before
         ok = wait(sCtl + kBarPReady + 8, pr1, kSitePReady);
         pr1 ^= 1;
@@ -830,7 +833,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         const int q0 = sQ + 2 * (n & 1) * Lo::kQBytes, qph = n >> 1;
         const uint32_t q_full = sCtl + (k8 ? kBarQReady : kBarQFull) + 8 * (2 * (n & 1));
-        if (!(ok = wait(q_full, qph, kSiteQFull) && wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
+        if (!(ok = wait_tile(q_full, qph, kSiteQFull) && wait_tile(sCtl + kBarKFull + 8 * st, ph, kSiteKFull))) break;
         bool fresh = true;
         while (true) {
           const uint32_t kt = sK + st * Lo::kStageBytes, vt = sV + st * Lo::kStageBytes;
@@ -845,14 +848,14 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           if (two) {
             if (fresh) {
-              if (!(ok = wait(q_full + 8, qph, kSiteQFull))) break;
+              if (!(ok = wait_tile(q_full + 8, qph, kSiteQFull))) break;
               tc_fence_after_sync();
             }
             issue_qk<D>(tmem + 128, q0 + Lo::kQBytes, kt, kIdQK);
             mma_commit_pair_warp(sCtl + kBarSFull + 8);
             mma_commit_pair_warp(sCtl + kBarKEmpty + 8 * st);
           }
-          ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
+          ok = wait_tile(sCtl + kBarVFull + 8 * st, ph, kSiteVFull);
           if (!k8 && end && tail < kBN) {
             // rank 1 zeroed rows of its half before it arrived: seen at cluster scope (the phase is complete,
             // so this returns at once)
@@ -866,7 +869,7 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             st = 0;
             ph ^= 1;
           }
-          if (!end && ok) ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
+          if (!end && ok) ok = wait_tile(sCtl + kBarKFull + 8 * st, ph, kSiteKFull);
           if (ok) ok = wait(sCtl + kBarPReady, pr0, kSitePReady);
           pr0 ^= 1;
           if (fresh && n > 0 && ok) ok = wait(sCtl + kBarOEmpty, n + 1, kSiteOEmpty);
@@ -907,20 +910,28 @@ attn_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         const int tail = VDX_UNIT(in, tail);
         in.release();
         if (left <= 0) continue;
-        for (int i = 0; !k8 && ok && i < 2; ++i) {          // 8 bits: the converters tell rank 0 themselves
-          const int b = 2 * (n & 1) + i;
-          ok = wait(sCtl + kBarQFull + 8 * b, n >> 1, kSiteRelay);
-          if (ok && lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarQFull + 8 * b, 0));
+        constexpr uint32_t kBarQ = k8 ? kBarQReady : kBarQFull;
+        auto pass_on = [&](uint32_t bar) {                  // copies have landed; what warps wrote must be seen as well
+          if (lane != 0) return;
+          if (k8)
+            mbar_arrive_remote_cluster(mapa_shared(bar, 0));
+          else
+            mbar_arrive_remote(mapa_shared(bar, 0));
+        };
+        for (int i = 0; ok && i < 2; ++i) {
+          const uint32_t bar = sCtl + kBarQ + 8 * (2 * (n & 1) + i);
+          ok = wait(bar, n >> 1, kSiteRelay);
+          if (ok) pass_on(bar);
         }
-        for (; !k8 && ok && left > 0; --left) {
+        for (; ok && left > 0; --left) {
           if (!(ok = wait(sCtl + kBarKFull + 8 * st, ph, kSiteRelay))) break;
-          if (lane == 0) mbar_arrive_remote(mapa_shared(sCtl + kBarKFull + 8 * st, 0));
+          pass_on(sCtl + kBarKFull + 8 * st);
           if (!(ok = wait(sCtl + kBarVFull + 8 * st, ph, kSiteRelay))) break;
-          if (left == 1 && tail < kBN) {
+          if (!k8 && left == 1 && tail < kBN) {
             zero_v_rows<D>(sV + st * Lo::kStageBytes, tail, lane);
             if (lane == 0) mbar_arrive_remote_cluster(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
-          } else if (lane == 0) {
-            mbar_arrive_remote(mapa_shared(sCtl + kBarVFull + 8 * st, 0));
+          } else {
+            pass_on(sCtl + kBarVFull + 8 * st);
           }
           if (++st == kS) {
             st = 0;
