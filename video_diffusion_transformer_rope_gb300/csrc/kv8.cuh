@@ -51,7 +51,8 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Four codes as two pairs of T times a power of two, exactly: `scale` is pair_two_to<T>(e).
+// Four codes as two pairs of T times a power of two, exactly: `scale` is pair_two_to<T>(e).  NaN codes come out as NaN in
+// fp16 and as 480 in bf16; any_nan(top) tells whether there was one among the codes of all calls that shared `top`, 0 at first.
 template <typename T>
 __device__ __forceinline__ uint32_t pair_two_to(int e);
 template <>
@@ -63,26 +64,28 @@ __device__ __forceinline__ uint32_t pair_two_to<__nv_bfloat16>(int e) {
   return static_cast<uint32_t>(e + 120 + 127) * 0x800080u;       // times the 2^120 that decode4 leaves out
 }
 template <typename T>
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi);
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi, uint32_t& top);
 template <>
-__device__ __forceinline__ void decode4<__half>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void decode4<__half>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi, uint32_t&) {
   lo = half2_mul(decode2<false>(w), scale);
   hi = half2_mul(decode2<true>(w), scale);
 }
 // A code's exponent and mantissa, moved to where bf16 has its own, are its value times 2^-120 (subnormals too).
 template <>
-__device__ __forceinline__ void decode4<__nv_bfloat16>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void decode4<__nv_bfloat16>(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi, uint32_t& top) {
   const uint32_t h[2] = {__byte_perm(w, 0u, 0x1404), __byte_perm(w, 0u, 0x3424)};
-  uint32_t r[2];
+  uint32_t m[2], r[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t m = (h[i] & 0x7f007f00u) >> 4;
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&scale));
+    m[i] = (h[i] & 0x7f007f00u) >> 4;
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m[i]), *reinterpret_cast<const __nv_bfloat162*>(&scale));
     r[i] = *reinterpret_cast<const uint32_t*>(&v) | (h[i] & 0x80008000u);
   }
+  top = __vimax3_u16x2(top, m[0], m[1]);               // NaN put in its place here costs 4 for each pair: a 480p frame's weights 310 us, not 299
   lo = r[0];
   hi = r[1];
 }
+__device__ __forceinline__ bool any_nan(uint32_t top) { return max(top & 0xffffu, top >> 16) == 0x7f0u; }
 __device__ __forceinline__ void decode8(const uint2& x, float (&f)[8]) {
   const uint32_t h[4] = {decode2<false>(x.x), decode2<true>(x.x), decode2<false>(x.y), decode2<true>(x.y)};
 #pragma unroll

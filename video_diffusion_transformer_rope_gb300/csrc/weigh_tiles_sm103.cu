@@ -363,6 +363,7 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
         tc_fence_after_sync();
         const int r = x * kKeys + row;
         const uint32_t scale = k8 ? pair_two_to<T>(ctl->exponent[r]) : 0u;
+        uint32_t top = 0;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
           uint32_t y[32];
@@ -373,11 +374,13 @@ weigh_tiles(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ We
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if constexpr (k8)
-                decode4<T>(w[e], scale, y[i * 8 + 2 * e], y[i * 8 + 2 * e + 1]);
+                decode4<T>(w[e], scale, y[i * 8 + 2 * e], y[i * 8 + 2 * e + 1], top);
               else
                 y[i * 4 + e] = w[e];
             }
           }
+          // a NaN channel makes every score of the key NaN: the last one stands for all
+          if (k8 && h == D / 64 - 1 && any_nan(top)) y[31] = 0x7fff7fffu;
           tmem_st32(tmem + lanes + x * 64 + h * 32, y);
         }
         tmem_wait_st();
