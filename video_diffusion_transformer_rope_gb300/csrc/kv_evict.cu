@@ -254,7 +254,7 @@ evict_move(const __grid_constant__ EvictParams p, const int blocks, const int bl
   if (count <= 0) return;
   const int page_to = pg < p.max_pages_to ? load_i32(p.table_to + s * p.table_to_stride + pg) : -1;
   if (page_to < 0 || page_to >= p.num_pages_to) {
-    if (lane == 0) atomicOr(&g_error_word, pg < p.max_pages_to ? kErrPage : kErrPosition);
+    if (lane == 0) atomicOr(&g_error_word, pg < p.max_pages_to ? kErrPage : kErrInto);
     return;
   }
   // lane l (and 16 + l): where the l-th key comes from

@@ -14,6 +14,7 @@ constexpr unsigned kErrPage = 8u;       // a page index outside the cache
 constexpr unsigned kErrLength = 16u;    // a length or row range past its bound
 constexpr unsigned kErrPosition = 32u;  // a token outside the position grid or its page table
 constexpr unsigned kErrRange8 = 64u;    // a value past what an 8-bit cache holds
+constexpr unsigned kErrInto = 128u;     // what an eviction keeps has no place in its new page table
 
 // Scales of an 8-bit cache (kv8.cuh): a byte per block of 16 tokens and head, strides in bytes.
 struct Scales8 {

@@ -459,6 +459,8 @@ vdx_status vdx_sync_check(void* stream) {
     return fail(VDX_ERR_ARG, "cu or kv_len broke a bound of its call (rows, max_q, max_kv); it was clamped, or its tokens not appended");
   if (word & vdx::kErrPosition)
     return fail(VDX_ERR_ARG, "an appended token was outside the position grid or its page table; it was skipped");
+  if (word & vdx::kErrInto)
+    return fail(VDX_ERR_ARG, "the page table that an eviction moves to was too short; the keys past its end were not moved");
   if (word & vdx::kErrRange8)
     return fail(VDX_ERR_RANGE, "a key or value was past 448 * 2^%d, the largest that an 8-bit cache holds, and was clamped to it", VDX_KV8_MAX_EXP);
   return VDX_OK;
