@@ -85,7 +85,8 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* c, const vdx_kv8_scales* s
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const char* what = nullptr;
-  if (static_cast<long long>(p.max_q) * p.g <= 32) {
+  // No place for any key (width 0): the kernel of few rows looks at lengths, which are reported; that of tiles has no units.
+  if (static_cast<long long>(p.max_q) * p.g <= 32 || p.max_kv == 0) {
     e = vdx::launch_weigh_rows(wp, c->d, c->dtype, multiprocessors(), st);
   } else {
     vdx::EncodeTiledFn encode = nullptr;
