@@ -121,7 +121,7 @@ vdx_status vdx_paged_evict(const vdx_paged_kv* c, const vdx_kv8_scales* scales, 
   if (same && a->width < a->keep) return fail(VDX_ERR_ARG, "width %d of w, which is w_out too, is smaller than keep %d", a->width, a->keep);
   const Weights w{a->w, a->w_seq, a->w_head, c->seqs, c->Hkv, a->width};
   const Weights wo{a->w_out, a->w_out_seq, a->w_out_head, c->seqs, c->Hkv, a->keep};
-  if (vdx_status s = check_weights("w", w, false)) return s;
+  if (vdx_status s = check_weights("w", w, same)) return s;       // in place a head is written while others are read
   if (vdx_status s = check_weights("w_out", wo, true)) return s;
   if (vdx_status s = check_i32("kv_len", a->kv_len, false)) return s;
   if (vdx_status s = check_i32("pos_offset", a->pos_offset, true)) return s;
