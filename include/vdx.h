@@ -376,7 +376,7 @@ size_t vdx_paged_attn8_workspace_bytes(const vdx_paged_kv* cache, const vdx_kv8_
  * entries NaN.
  *   scales: NULL for a 16-bit cache.  The cache's values are not read.
  *   w: float32 [seqs, Hkv, width], the entries of a head contiguous; kv_len past width or max_kv is clamped and
- *   reported.  pos_offset as in vdx_paged_attn_offset. */
+ *   reported.  pos_offset as in vdx_paged_attn_offset.  max_q (or rows) times Hq / Hkv: at most 2^26 (VDX_ERR_UNSUPPORTED). */
 typedef struct vdx_paged_weights_args {
   const void* q;            /* [rows, Hq, d]                                                      */
   const float* lse;         /* [Hq, rows]                                                         */

@@ -64,6 +64,10 @@ vdx_status vdx_paged_attn_weights(const vdx_paged_kv* c, const vdx_kv8_scales* s
   if (q.empty()) return VDX_OK;
   if (static_cast<long long>(p.max_q) * p.g > 0x7ffff000ll)
     return fail(VDX_ERR_ARG, "%d rows of %d heads per kv head are too many", p.max_q, p.g);
+  // 256 keys take 1.1 us for every 128 rows (0.6 s at this many), and a warp of the tile kernel waits for all of them, a second at most
+  if (static_cast<long long>(p.max_q) * p.g > vdx::kMaxWeighRows)
+    return fail(VDX_ERR_UNSUPPORTED, "more than %d rows per kv head (%d of %d heads); where sequences have fewer, pass max_q", vdx::kMaxWeighRows,
+                p.max_q, p.g);
   if (static_cast<long long>(p.S) * p.Hkv > 0x3fffffffll)
     return fail(VDX_ERR_ARG, "%d sequences of %d kv heads are too many", p.S, p.Hkv);
   if (vdx_status s = check_i32("cu", a->cu, false)) return s;

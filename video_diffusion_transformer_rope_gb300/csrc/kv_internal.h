@@ -120,6 +120,7 @@ struct WeighParams {
   float decay;
   int nsplit, split_keys;     // keys of a block (few-row kernel)
 };
+constexpr int kMaxWeighRows = 1 << 26;        // (token, query head) rows of a sequence and kv head
 cudaError_t launch_weigh_rows(WeighParams p, int d, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_weigh_tiles(const WeighParams& p, int d, int dtype, EncodeTiledFn encode, int sms, cudaStream_t stream,
                                const char** what);
