@@ -7,11 +7,12 @@
 // blocks, then the digit that holds the need-th largest; no further one where all that share the digits so far stay), then
 // one walk in order writes index and weights of what stays; a key's place is the number of keys above the border before it
 // and of those equal to it, up to the last that fits.
-// Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 39 us).
+// Bound by latency: passes and barriers (75600 weights of 40 heads: one block a head 76 us, clusters of 8 37 us).
 //
 // evict_move, a warp per (16 slots of a page, head): rows of 16 keys and values, found through the index and the old
 // page table, 16 bytes a lane; in 8 bits their largest value gives the new scale first.  Bound by DRAM: what stays is read
-// and written once (28800 of 75600 keys of 40 heads of 128 channels in 16 bits, 1.18 GB: 171 us, the rate of a plain copy).
+// and written once (28800 of 75600 keys of 40 heads of 128 channels in 16 bits, 1.18 GB: 171 us, the rate of a plain copy;
+// in 8 bits 166 for half of that, rows of 128 bytes gathered by head).
 #include <cstdint>
 
 #include "kv8.cuh"
